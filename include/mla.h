@@ -82,6 +82,9 @@ extern "C" {
 #define MLA_MODE_CHUNK_LATENT 4
 #define MLA_MODE_CHUNK_ABSORBED 5
 #define MLA_MODE_FOLD 6
+#define MLA_MODE_PAGED_APPEND 8
+#define MLA_MODE_PAGED_ATTN 9
+#define MLA_MODE_WINDOW_ATTN 10
 
 /* Weights of one MLA sublayer: device pointers to bf16, nn.Linear [out, in].
  * Key-value compression page, MLA __init__ excerpt, for the projections;
@@ -150,6 +153,12 @@ typedef struct {
  *                                  with B * T only).
  *   mode = MLA_MODE_FOLD:          mla_fold_wuv_into_wo (B, t_or_p, cap
  *                                  ignored: a status region only).
+ *   mode = MLA_MODE_PAGED_APPEND:  mla_paged_append, B sequences of at most
+ *                                  t_or_p new tokens (`cap` ignored).
+ *   mode = MLA_MODE_PAGED_ATTN:    mla_paged_attention, B sequences of
+ *                                  t_or_p new tokens (`cap` ignored).
+ *   mode = MLA_MODE_WINDOW_ATTN:   mla_window_attention, B sequences of
+ *                                  t_or_p queries (`cap` ignored).
  * Returns 0 when the arguments are out of range. */
 size_t mla_workspace_size(int mode, int B, int t_or_p, int cap);
 
@@ -386,6 +395,121 @@ typedef struct {
  * ALIGNMENT, WORKSPACE, CUDA. */
 int mla_ffn(const mla_ffn_weights_t* w, const mla_params_t* params, const void* x, int n_tok, void* out,
             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- paged 8-bit cache ------------------------------------------------------
+ * The rebuilt per-head cache ("Mix and project" page: keys and values of every
+ * head, 20,480 values per position) in pages of a few tokens, with the 128
+ * unrotated key values and the 128 values of a head as E4M3 codes and one
+ * scale per page and head, and the rotary key, which all heads share, once
+ * per token in bf16: heads * 256 + 128 bytes a position (16.5 KB at 64 heads)
+ * where the bf16 cache takes 40 KB.
+ *   k_codes, v_codes  uint8 [n_pages, heads, page, 128], E4M3 (the OCP FP8
+ *                     encoding, largest finite 448)
+ *   k_pe              bf16 [n_pages, page, 64], rotated
+ *   k_scales, v_scales float [n_pages, heads], positive; mla_paged_append
+ *                     writes powers of two, 2^-60 .. 2^60
+ *   table             int [B, max_pages] in DEVICE memory: the pages of each
+ *                     sequence in order, position p in page table[b][p / page],
+ *                     slot p % page.  Read by the kernels: a captured graph
+ *                     can be replayed with a new table.
+ * A key is code * scale.  A page that receives tokens belongs to one sequence;
+ * pages that are only read may be shared.  Codes, scales and rotary keys are
+ * 16-byte aligned, the table 4-byte aligned.
+ *   page   16, 32, 64 or 128
+ *   heads  a multiple of 4, at most 128 (the sublayer's entry points need 64;
+ *          a shard of the heads has fewer)
+ * n_pages * heads and n_pages * page must fit a 31-bit int. */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_pe;
+  float* k_scales;
+  float* v_scales;
+  const int* table;
+  int n_pages, max_pages, page, heads;
+} mla_paged_cache_t;
+
+/* Appends new tokens to the paged cache, rotating their rotary keys on the
+ * way.  Sequence b's T_b new tokens take positions P[b] .. P[b] + T_b - 1.
+ *   k, v     bf16: the 128 key / value numbers of (token row n, head h) are
+ *            contiguous at k + n * k_token + h * k_head (strides in elements,
+ *            multiples of 8: e.g. both halves of a kv_b product [N, heads, 256])
+ *   k_pe     bf16, the 64 unrotated values of row n at k_pe + n * pe_token
+ *            (a multiple of 8); rotated as RoPE above, angle formed in double
+ *   P        int [B] in DEVICE memory; -1 marks an idle sequence: nothing is
+ *            appended for it
+ *   T, cu    cu NULL: T tokens each, row n = b * T + t, N = B * T.  Else cu is
+ *            int [B + 1] in DEVICE memory, sequence b's rows are cu[b] ..
+ *            cu[b + 1] - 1, at most T of them (0 is allowed), N >= cu[B].
+ *   params   rope_base (eps, softmax_scale, delta_out, timing: not used)
+ *   workspace mla_workspace_size(MLA_MODE_PAGED_APPEND, B, T, 0)
+ * Scales: with k the smallest integer in [-60, 60] for which the new tokens
+ * of a page and head have amax <= 448 * 2^k, the page's scale becomes 2^k; in
+ * a page that already holds tokens (P[b] not on a page's start) it only grows:
+ * the larger of that and the old scale, and the codes already there are
+ * re-expressed at the new scale (rounded again).  Code = x / scale rounded to
+ * nearest even, saturating at +-448 (an infinity gives the page 2^60); NaN
+ * stays NaN and does not count for amax.  Slots behind the last token, and
+ * every other page, are left as they were.
+ * A P[b] below -1, T_b outside [0, T], rows outside [0, N), positions past
+ * max_pages * page or a page number outside [0, n_pages) cannot be checked on
+ * the host: the kernel skips that sequence (or page) and mla_device_status
+ * then returns MLA_ERR_INVALID_ARG.
+ * Errors: INVALID_ARG (null pointer, B, T or N < 1, N > 2^24, N < B * T
+ * without cu, a stride not a multiple of 8 or below 0), UNSUPPORTED (page,
+ * heads), ALIGNMENT, WORKSPACE, CUDA. */
+int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params, const void* k, long long k_token,
+                     long long k_head, const void* v, long long v_token, long long v_head, const void* k_pe,
+                     long long pe_token, const int* P, const int* cu, int B, int T, int N, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Attention of T new tokens per sequence (1 for a decode step, up to 8 to
+ * verify drafted tokens) over the paged cache, which already holds them.
+ * Query t of sequence b sits at position i = P[b] + t and sees key j iff
+ * j <= i and, with window > 0, i - j < window or j < sinks (the first `sinks`
+ * positions stay visible).
+ *   q        bf16, row b * T + t at q + row * q_row: heads x [128 nope | 64 pe],
+ *            pe rotated (the q_b product after RoPE); q_row a multiple of 8,
+ *            >= heads * 192
+ *   out      bf16, row b * T + t at out + row * out_row: heads x 128; out_row a
+ *            multiple of 8, >= heads * 128
+ *   P        int [B] in DEVICE memory, -1 .. P_max; P[b] = -1 marks an idle
+ *            sequence (its output rows are zeros).  P_max sizes the launch;
+ *            P_max + T <= max_pages * page.
+ *   window   0 = every key; sinks is then ignored
+ *   params   softmax_scale (the others are not used)
+ *   workspace mla_workspace_size(MLA_MODE_PAGED_ATTN, B, T, 0); not shared by
+ *            calls that may run concurrently, or by two captured graphs that may
+ * Keys that no query of the sequence sees are not used, whatever their pages
+ * hold (table entries of pages without a visible key are not looked at, so
+ * pages that a window has passed can be given back).  Scores, softmax
+ * statistics and sums are float32; probabilities enter the product with V as
+ * two float16 parts (22 bits).
+ * A P[b] outside [-1, P_max] is taken as idle, a page number outside
+ * [0, n_pages) is clamped, and mla_device_status then returns
+ * MLA_ERR_INVALID_ARG.
+ * Errors: INVALID_ARG (null pointer, B or T < 1, P_max < 0, P_max + T >
+ * max_pages * page, window or sinks < 0, row strides), UNSUPPORTED (T > 8,
+ * page, heads), ALIGNMENT, WORKSPACE, CUDA. */
+int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* params, const void* q, long long q_row,
+                        int B, int T, const int* P, int P_max, int window, int sinks, void* out, long long out_row,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Causal prefill attention under a sliding window with sinks, over the dense
+ * rebuilt cache: query t of sequence b at position i = P0 + t sees key j iff
+ * j <= i and (i - j < window or j < sinks).
+ *   q        [B, T, 64 * 192]  per head [128 nope | 64 pe], pe rotated
+ *   k_cache  [B, 64, cap, 192], v_cache [B, 64, cap, 128]: positions that some
+ *            query sees are read
+ *   out      [B, T, 64 * 128]
+ *   window   >= 1;  sinks >= 0;  P0 >= 0, P0 + T <= cap
+ *   params   softmax_scale (the others are not used)
+ *   workspace mla_workspace_size(MLA_MODE_WINDOW_ATTN, B, T, 0)
+ * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
+ * Errors: INVALID_ARG (null pointer, sizes), ALIGNMENT, WORKSPACE, CUDA. */
+int mla_window_attention(const mla_params_t* params, const void* q, int B, int T, int P0, const void* k_cache,
+                         const void* v_cache, int cap, int window, int sinks, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream` and reads the device status word the last call on
  * this workspace left: MLA_OK, MLA_ERR_TIMEOUT if a bounded device wait

@@ -18,6 +18,7 @@ D, HEADS, Q_LORA, KV_LORA, QK_NOPE, QK_ROPE, QK, V = 7168, 64, 1536, 512, 128, 6
 FFN_INTER = 18432
 MODE_PREFILL, MODE_DECODE, MODE_DECODE_LATENT, MODE_FFN, MODE_CHUNK_LATENT, MODE_CHUNK_ABSORBED = 0, 1, 2, 3, 4, 5
 MODE_FOLD = 6
+MODE_PAGED_APPEND, MODE_PAGED_ATTN, MODE_WINDOW_ATTN = 8, 9, 10
 STAGES = ["input_norm", "a_proj", "latent", "q_b", "kv_b", "attn", "combine", "absorb_q", "absorb_o", "o_proj",
           "ffn_norm", "gate_up", "down"]
 MAX_STAGES = len(STAGES)
@@ -57,6 +58,11 @@ class MlaFfnWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in FFN_WEIGHT_NAMES]
 
 
+class MlaPagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_pe", "k_scales", "v_scales", "table")] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "max_pages", "page", "heads")]
+
+
 class MlaTiming(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p * MAX_STAGES), ("stop", ctypes.c_void_p * MAX_STAGES),
                 ("n_launches", ctypes.c_int)]
@@ -69,7 +75,7 @@ class MlaParams(ctypes.Structure):
 
 _lib = None
 
-_VP, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_VP, _I, _SZ, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
 _SIGS = {
     "mla_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "mla_prefill": (_I, [ctypes.POINTER(MlaWeights), ctypes.POINTER(MlaParams), _VP, _I, _I, _VP, _VP, _VP, _VP,
@@ -97,6 +103,12 @@ _SIGS = {
     "mla_quantize_fp8": (_I, [_VP, _I, _I, _VP, _VP, _VP]),
     "mla_decode_fp8": (_I, [ctypes.POINTER(MlaWeightsFp8), ctypes.POINTER(MlaParams), _VP, _I, _I, _VP, _VP, _I, _VP,
                             _VP, _SZ, _VP]),
+    "mla_paged_append": (_I, [ctypes.POINTER(MlaPagedCache), ctypes.POINTER(MlaParams), _VP, _LL, _LL, _VP, _LL, _LL,
+                              _VP, _LL, _VP, _VP, _I, _I, _I, _VP, _SZ, _VP]),
+    "mla_paged_attention": (_I, [ctypes.POINTER(MlaPagedCache), ctypes.POINTER(MlaParams), _VP, _LL, _I, _I, _VP, _I,
+                                 _I, _I, _VP, _LL, _VP, _SZ, _VP]),
+    "mla_window_attention": (_I, [ctypes.POINTER(MlaParams), _VP, _I, _I, _I, _VP, _VP, _I, _I, _I, _VP, _VP, _SZ,
+                                  _VP]),
     "mla_device_status": (_I, [_VP, _VP]),
     "mla_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -341,6 +353,117 @@ def mla_decode_fp8(weights: MlaWeightsFp8, x, P: int, k_cache, v_cache, out, wor
                               _ptr(k_cache), _ptr(v_cache), cap, _ptr(out), _ptr(workspace), workspace.numel(),
                               _stream(stream))
     _check(rc, "mla_decode_fp8")
+
+
+PAGED_TENSORS = ["k_codes", "v_codes", "k_pe", "k_scales", "v_scales"]
+
+
+def alloc_paged_cache(n_pages: int, page: int = 64, heads: int = HEADS, device="cuda") -> dict:
+    """The tensors of an empty paged 8-bit cache (codes uint8, E4M3; without a table)."""
+    import torch
+    t = {n: torch.zeros((n_pages, heads, page, 128), dtype=torch.uint8, device=device) for n in ("k_codes", "v_codes")}
+    t["k_pe"] = torch.zeros((n_pages, page, QK_ROPE), dtype=torch.bfloat16, device=device)
+    for n in ("k_scales", "v_scales"):
+        t[n] = torch.ones((n_pages, heads), dtype=torch.float32, device=device)
+    return t
+
+
+def make_paged_cache(t: dict) -> MlaPagedCache:
+    """Pack the tensors of a paged cache (PAGED_TENSORS) and its int32 table [B, max_pages] into the C struct.
+    The struct points at the tensors: a table changed in place is seen by the next call."""
+    import torch
+    n_pages, heads, page, _ = t["k_codes"].shape
+    shapes = {"k_codes": (n_pages, heads, page, 128), "v_codes": (n_pages, heads, page, 128),
+              "k_pe": (n_pages, page, QK_ROPE), "k_scales": (n_pages, heads), "v_scales": (n_pages, heads)}
+    dtypes = {"k_codes": torch.uint8, "v_codes": torch.uint8, "k_pe": torch.bfloat16, "k_scales": torch.float32,
+              "v_scales": torch.float32, "table": torch.int32}
+    for n in PAGED_TENSORS + ["table"]:
+        x = t[n]
+        if x.dtype != dtypes[n] or not x.is_cuda or not x.is_contiguous() or \
+                (tuple(x.shape) != shapes[n] if n != "table" else x.dim() != 2) or x.device != t["k_codes"].device:
+            raise ValueError(f"paged cache {n}: need a contiguous {dtypes[n]} CUDA tensor of shape "
+                             f"{shapes.get(n, '[B, max_pages]')} on one device")
+    s = MlaPagedCache(*[t[n].data_ptr() for n in PAGED_TENSORS], t["table"].data_ptr(), n_pages, t["table"].shape[1],
+                      page, heads)
+    s._keep = dict(t)
+    return s
+
+
+def _rows(x, what: str, cols: int):
+    """Row stride of a bf16 CUDA tensor [rows, cols] whose rows are contiguous."""
+    import torch
+    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2 or x.shape[1] != cols or x.stride(1) != 1:
+        raise ValueError(f"{what}: need a bf16 CUDA tensor [rows, {cols}] with contiguous rows")
+    return x.stride(0)
+
+
+def _head_rows(x, what: str, heads: int):
+    """Token and head strides of a bf16 CUDA tensor [rows, heads, 128] whose last dimension is contiguous."""
+    import torch
+    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != 128 or \
+            x.stride(2) != 1:
+        raise ValueError(f"{what}: need a bf16 CUDA tensor [rows, {heads}, 128] with a contiguous last dimension")
+    return x.stride(0), x.stride(1)
+
+
+def _ints(x, what: str, n: int):
+    import torch
+    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or x.dim() != 1 or x.numel() != n:
+        raise ValueError(f"{what}: need a contiguous int32 CUDA tensor of {n} elements")
+
+
+def mla_paged_append(cache: MlaPagedCache, k, v, k_pe, P, T: int, workspace, cu=None,
+                     params: MlaParams | None = None, stream=None):
+    """k, v: bf16 [N, heads, 128] (views of a kv_b product are fine); k_pe: bf16 [N, 64], unrotated; P: int32 CUDA
+    [B], position of each sequence's first new token (-1: idle); T tokens each, or with cu (int32 CUDA [B + 1],
+    row offsets) at most T; workspace of MODE_PAGED_APPEND."""
+    B, N = cache._keep["table"].shape[0], k.shape[0]
+    k_token, k_head = _head_rows(k, "k", cache.heads)
+    v_token, v_head = _head_rows(v, "v", cache.heads)
+    pe_token = _rows(k_pe, "k_pe", QK_ROPE)
+    _ints(P, "P", B)
+    if cu is not None:
+        _ints(cu, "cu", B + 1)
+    if v.shape[0] != N or k_pe.shape[0] != N:
+        raise ValueError("k, v and k_pe: need the same number of rows")
+    rc = lib().mla_paged_append(ctypes.byref(cache), None if params is None else ctypes.byref(params), k.data_ptr(),
+                                k_token, k_head, v.data_ptr(), v_token, v_head, k_pe.data_ptr(), pe_token,
+                                P.data_ptr(), None if cu is None else cu.data_ptr(), B, T, N, workspace.data_ptr(),
+                                workspace.numel(), _stream(stream))
+    _check(rc, "mla_paged_append")
+
+
+def mla_paged_attention(cache: MlaPagedCache, q, P, P_max: int, out, workspace, window: int = 0, sinks: int = 0,
+                        params: MlaParams | None = None, stream=None):
+    """q: bf16 [B * T, heads * 192] (rotated); out: bf16 [B * T, heads * 128]; P: int32 CUDA [B], position of each
+    sequence's first query (-1: idle, its rows become zeros), at most P_max; window 0 = every key, else the last
+    `window` keys and the first `sinks`; workspace of MODE_PAGED_ATTN."""
+    B = cache._keep["table"].shape[0]
+    q_row, out_row = _rows(q, "q", cache.heads * QK), _rows(out, "out", cache.heads * V)
+    _ints(P, "P", B)
+    if q.shape[0] % B or out.shape[0] != q.shape[0]:
+        raise ValueError("q and out: need the same number of rows, T for each sequence of the table")
+    rc = lib().mla_paged_attention(ctypes.byref(cache), None if params is None else ctypes.byref(params),
+                                   q.data_ptr(), q_row, B, q.shape[0] // B, P.data_ptr(), P_max, window, sinks,
+                                   out.data_ptr(), out_row, workspace.data_ptr(), workspace.numel(), _stream(stream))
+    _check(rc, "mla_paged_attention")
+
+
+def mla_window_attention(q, P0: int, k_cache, v_cache, out, workspace, window: int, sinks: int = 0,
+                         params: MlaParams | None = None, stream=None):
+    """q: bf16 [B, T, 64 * 192] at positions P0..P0+T-1; k_cache [B, 64, cap, 192], v_cache [B, 64, cap, 128];
+    out: bf16 [B, T, 64 * 128]; a query sees the last `window` keys up to its own and the first `sinks`;
+    workspace of MODE_WINDOW_ATTN."""
+    import torch
+    B, T, cap = q.shape[0], q.shape[1], k_cache.shape[2]
+    for x, what, shape in ((q, "q", (B, T, HEADS * QK)), (k_cache, "k_cache", (B, HEADS, cap, QK)),
+                           (v_cache, "v_cache", (B, HEADS, cap, V)), (out, "out", (B, T, HEADS * V))):
+        if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != shape:
+            raise ValueError(f"{what}: need a contiguous bf16 CUDA tensor of shape {shape}")
+    rc = lib().mla_window_attention(None if params is None else ctypes.byref(params), _ptr(q), B, T, P0,
+                                    _ptr(k_cache), _ptr(v_cache), cap, window, sinks, _ptr(out), _ptr(workspace),
+                                    workspace.numel(), _stream(stream))
+    _check(rc, "mla_window_attention")
 
 
 def mla_device_status(workspace, stream=None) -> int:

@@ -29,6 +29,15 @@ struct Layout {
 // (kMaxSplitCounters ints); cleared at the start of every call.
 constexpr size_t kStatusRegion = 256 + kMaxSplitCounters * sizeof(int);
 
+// Regions of the paged attention: partials of up to two pieces per CTA, and
+// the number of key tiles before each sequence.
+template <class Take>
+void take_paged(Layout& L, int B, int T, Take& take) {
+  L.part_o = take((size_t)2 * kPagedMaxCtas * T * 4 * MLA_V * sizeof(float));
+  L.part_ml = take((size_t)2 * kPagedMaxCtas * T * 4 * sizeof(float2));
+  L.plan = take(((size_t)B + 1) * sizeof(int));
+}
+
 Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
   Layout L{};
   const bool pre = mode == MLA_MODE_PREFILL || mode == MLA_MODE_CHUNK_LATENT;
@@ -43,7 +52,13 @@ Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
     return at;
   };
   L.status = take(kStatusRegion);
-  if (mode == MLA_MODE_FOLD) {  // the fold of W_UV into W_o: the status region only
+  // the fold of W_UV into W_o, the append and the window attention: the status region only
+  if (mode == MLA_MODE_FOLD || mode == MLA_MODE_PAGED_APPEND || mode == MLA_MODE_WINDOW_ATTN) {
+    L.total = off;
+    return L;
+  }
+  if (mode == MLA_MODE_PAGED_ATTN) {  // two partial pieces per CTA, and the sequences' first tiles
+    take_paged(L, B, t_or_p, take);
     L.total = off;
     return L;
   }
@@ -454,6 +469,10 @@ size_t mla_workspace_size(int mode, int B, int t_or_p, int cap) {
   } else if (mode == MLA_MODE_CHUNK_ABSORBED) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens || cap < t_or_p || cap >= (1 << 24)) return 0;
   } else if (mode == MLA_MODE_FOLD) {
+  } else if (mode == MLA_MODE_PAGED_APPEND || mode == MLA_MODE_WINDOW_ATTN) {
+    if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
+  } else if (mode == MLA_MODE_PAGED_ATTN) {
+    if (t_or_p < 1 || t_or_p > kPagedMaxT || B > kMaxTokens) return 0;
   } else {
     return 0;
   }
@@ -476,10 +495,18 @@ const char* mla_status_string(int s) {
 int mla_device_status(const void* workspace, void* stream) {
   if (!workspace) return MLA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t word = 0;
-  if (cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  uint32_t head[2] = {0, 0};  // the word and the number of further words (kStatusExtraWord)
+  if (cudaMemcpyAsync(head, workspace, sizeof(head), cudaMemcpyDeviceToHost, s) != cudaSuccess) return MLA_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return MLA_ERR_CUDA;
+  uint32_t word = head[0];
+  if (head[1] > 0 && head[1] <= (uint32_t)kMaxStatusExtra) {
+    uint32_t extra[kMaxStatusExtra];
+    if (cudaMemcpyAsync(extra, static_cast<const uint32_t*>(workspace) + kStatusExtraFirst, head[1] * sizeof(uint32_t),
+                        cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    for (uint32_t i = 0; i < head[1]; ++i) word |= extra[i];
+  }
   if (word & kStatusTimeout) return MLA_ERR_TIMEOUT;
   return (word & kStatusBadLength) ? MLA_ERR_INVALID_ARG : MLA_OK;
 }
@@ -1019,6 +1046,151 @@ int mla_ffn(const mla_ffn_weights_t* w, const mla_params_t* params, const void* 
   sg.stop(MLA_STAGE_FFN_DOWN);
   if (p.timing) p.timing->n_launches = launches;
   return MLA_OK;
+}
+
+}  // extern "C"
+
+// ---- paged 8-bit cache ------------------------------------------------------
+namespace {
+
+int check_cache(const mla_paged_cache_t* c) {
+  if (!c) return MLA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)c->k_codes, (const void*)c->v_codes, (const void*)c->k_pe,
+                        (const void*)c->k_scales, (const void*)c->v_scales}) {
+    if (!p) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(p)) return MLA_ERR_ALIGNMENT;
+  }
+  if (!c->table || c->n_pages < 1 || c->max_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(c->table) & 3) return MLA_ERR_ALIGNMENT;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MLA_ERR_UNSUPPORTED;
+  if (c->heads < 4 || c->heads > 128 || c->heads % 4) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->heads > INT32_MAX || (int64_t)c->n_pages * c->page > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+PagedCache device_cache(const mla_paged_cache_t* c) {
+  return PagedCache{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes),
+                    static_cast<__nv_bfloat16*>(c->k_pe), c->k_scales, c->v_scales, c->table,
+                    c->n_pages, c->max_pages, c->page, c->heads};
+}
+
+int check_workspace(const void* ws, size_t bytes, int mode, int B, int T) {
+  if (!ws) return MLA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MLA_ERR_ALIGNMENT;
+  return bytes < make_layout(mode, B, T, kMaxSmsForSizing).total ? MLA_ERR_WORKSPACE : MLA_OK;
+}
+
+// strides in elements whose rows stay 16-byte aligned
+bool good_stride(long long s) { return s >= 0 && s % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params, const void* k, long long k_token,
+                     long long k_head, const void* v, long long v_token, long long v_head, const void* k_pe,
+                     long long pe_token, const int* P, const int* cu, int B, int T, int N, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  const Params p = resolve(params);
+  if (!params_ok(p)) return MLA_ERR_INVALID_ARG;
+  if (!k || !v || !k_pe || !P || B < 1 || T < 1 || N < 1 || N > kMaxTokens || (int64_t)B * T > kMaxTokens)
+    return MLA_ERR_INVALID_ARG;
+  if (!cu && (int64_t)B * T > N) return MLA_ERR_INVALID_ARG;
+  for (long long s : {k_token, k_head, v_token, v_head, pe_token})
+    if (!good_stride(s)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pe) || (reinterpret_cast<uintptr_t>(P) & 3) ||
+      (reinterpret_cast<uintptr_t>(cu) & 3))
+    return MLA_ERR_ALIGNMENT;
+  rc = check_workspace(workspace, workspace_bytes, MLA_MODE_PAGED_APPEND, B, T);
+  if (rc) return rc;
+  PagedAppendArgs a{};
+  a.c = device_cache(cache);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.pe = static_cast<const __nv_bfloat16*>(k_pe);
+  a.pe_token = pe_token;
+  a.P = P;
+  a.cu = cu;
+  a.B = B;
+  a.T = T;
+  a.N = N;
+  for (int i = 0; i < 32; ++i) a.inv_freq[i] = pow((double)p.base, -2.0 * i / 64.0);
+  a.status = static_cast<uint32_t*>(workspace);
+  return launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* params, const void* q, long long q_row,
+                        int B, int T, const int* P, int P_max, int window, int sinks, void* out, long long out_row,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  const Params p = resolve(params);
+  if (!params_ok(p)) return MLA_ERR_INVALID_ARG;
+  if (!q || !out || !P || B < 1 || B > kMaxTokens || T < 1 || P_max < 0 || window < 0 || sinks < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (T > kPagedMaxT) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)P_max + T > (int64_t)cache->max_pages * cache->page || (int64_t)P_max + T > (1 << 24))
+    return MLA_ERR_INVALID_ARG;
+  if (!good_stride(q_row) || q_row < cache->heads * MLA_QK || !good_stride(out_row) ||
+      out_row < cache->heads * MLA_V)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(P) & 3)) return MLA_ERR_ALIGNMENT;
+  rc = check_workspace(workspace, workspace_bytes, MLA_MODE_PAGED_ATTN, B, T);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  const Layout L = make_layout(MLA_MODE_PAGED_ATTN, B, T, kMaxSmsForSizing);
+  PagedAttnArgs a{};
+  a.c = device_cache(cache);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(out);
+  a.q_row = q_row;
+  a.o_row = out_row;
+  a.P = P;
+  a.B = B;
+  a.T = T;
+  a.P_max = P_max;
+  a.window = window;
+  a.sinks = window ? sinks : 0;
+  a.scale = p.scale;
+  a.status = at<uint32_t>(workspace, L.status);
+  a.part_o = at<float>(workspace, L.part_o);
+  a.part_ml = at<float2>(workspace, L.part_ml);
+  a.first_tile = at<int>(workspace, L.plan);
+  const DevStatusHost st{a.status, kDefaultWaitLimitNs};
+  int launches = 0;
+  return launch_paged_attention(a, st, sms, static_cast<cudaStream_t>(stream), &launches) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int mla_window_attention(const mla_params_t* params, const void* q, int B, int T, int P0, const void* k_cache,
+                         const void* v_cache, int cap, int window, int sinks, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const Params p = resolve(params);
+  if (!params_ok(p)) return MLA_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !out || B < 1 || T < 1 || P0 < 0 || (int64_t)B * T > kMaxTokens ||
+      (int64_t)P0 + T > cap || window < 1 || sinks < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MLA_ERR_ALIGNMENT;
+  int rc = check_workspace(workspace, workspace_bytes, MLA_MODE_WINDOW_ATTN, B, T);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  const DevStatusHost st{static_cast<uint32_t*>(workspace), kDefaultWaitLimitNs};
+  if (cudaMemsetAsync(st.word, 0, 256, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+  PrefillAttnArgs a{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k_cache),
+                    static_cast<const __nv_bfloat16*>(v_cache), static_cast<__nv_bfloat16*>(out), B, T, cap,
+                    p.scale, P0, window, sinks};
+  return launch_prefill_attention(a, st, sms, stream_) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // extern "C"

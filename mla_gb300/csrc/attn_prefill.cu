@@ -14,6 +14,8 @@
 // enough work for every SM to take one of its heaviest tiles early, and so
 // that its heads' K/V fit comfortably in L2).  Each item's Q load and first
 // scores overlap the previous item's last P.V and epilogue.
+// Sliding window (WIN): an item's key tiles are those of the sinks and of the
+// keys its queries see, so the work of a query tile is bounded by the window.
 // Chunked prefill: the queries sit at positions past..past+T-1 and attend to
 // keys 0..past+T-1 of the cache (the chunk's own keys written after the
 // cached ones), the causal mask offset by past.
@@ -50,6 +52,8 @@
 #include "common.cuh"
 #include "internal.h"
 
+#include <algorithm>
+
 namespace mla {
 
 namespace {
@@ -85,10 +89,16 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-// Work item w (the order described above) -> its query tile, head, sequence.
+// Work item w (the order described above) -> its query tile, head, sequence
+// and key tiles.  Under a sliding window (WIN) the tile's queries together
+// see the keys from w0 on, and the sinks before w0: first n_sink tiles over
+// keys 0 .. n_first - 1, then tiles from w0 on (a TMA box may start at any
+// row, so no key before w0 is loaded).
+template <bool WIN>
 struct Item {
   int qt, h, b, q0, n_kv;
-  __device__ __forceinline__ Item(int w, int n_qt, int T, int past, int G) {
+  int w0, n_first, n_sink;
+  __device__ __forceinline__ Item(int w, int n_qt, int T, int past, int G, int window, int sinks) {
     const int per_seq = 64 * n_qt;
     b = w / per_seq;
     const int r = w - b * per_seq;
@@ -108,6 +118,18 @@ struct Item {
     q0 = qt * 128;
     // keys 0 .. past + q0 + 127 (the tile's last query), at most past + T of them
     n_kv = min((past + q0 + 127) / 128 + 1, (past + T + 127) / 128);
+    w0 = n_first = n_sink = 0;
+    if constexpr (WIN) {
+      w0 = max(0, past + q0 - window + 1);  // window >= 1: no overflow
+      n_first = min(sinks, w0);
+      n_sink = (n_first + 127) / 128;
+      n_kv = n_sink + (min(past + q0 + 127, past + T - 1) - w0) / 128 + 1;
+    }
+  }
+  // first key of the item's key tile j
+  __device__ __forceinline__ int key0(int j) const {
+    if constexpr (WIN) return j < n_sink ? j * 128 : w0 + (j - n_sink) * 128;
+    return j * 128;
   }
 };
 
@@ -120,11 +142,12 @@ __device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, const DevSt
   return true;
 }
 
+template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, __nv_bfloat16* __restrict__ o, int T, int n_qt,
-                    int n_items, float sl2, int past, int head_group, int* __restrict__ work,
-                    const DevStatus st) {
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVsink,
+                    __nv_bfloat16* __restrict__ o, int T, int n_qt, int n_items, float sl2, int past, int head_group,
+                    int window, int sinks, int* __restrict__ work, const DevStatus st) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bar = reinterpret_cast<Bars*>(smem + kBarOff);
@@ -185,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar->item[slot] = w;
         mbar_arrive(&bar->item_full[slot]);  // release: the index is visible to every waiting role
         if (w < 0) break;
-        const Item t(w, n_qt, T, past, head_group);
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         // the Q tile: dims 0-127 into the staging atoms once the softmax threads
         // copied the previous item's into tensor memory, dims 128-191 into the
         // slot of this item's parity once the S of the item two back are done
@@ -206,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(&bar->k_full[ks], 3 * kAtom);
           for (int c = 0; c < 3; ++c)
-            tma_load_3d(smem + kKOff + (ks * 3 + c) * kAtom, &tmK, &bar->k_full[ks], 64 * c, j * 128, kv_row);
+            tma_load_3d(smem + kKOff + (ks * 3 + c) * kAtom, &tmK, &bar->k_full[ks], 64 * c, t.key0(j), kv_row);
           issued[ks]++;
         }
         if (!ok) break;
@@ -226,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok; ++it) {
         int w;
         if (!read_item(bar, it, w, st, abort_flag) || w < 0) break;
-        const Item t(w, n_qt, T, past, head_group);
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         const int kv_row = t.b * 64 + t.h;
         for (int j = 0; j < t.n_kv; ++j, ++gt) {
           const int vs = gt & 1;
@@ -235,8 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&bar->v_full[vs], 2 * kAtom);
+          // a sink tile's view ends behind the last sink: the rows of a key that
+          // no query sees are zeros there, whatever the cache holds
+          const CUtensorMap* mv = WIN && j < t.n_sink ? &tmVsink : &tmV;
           for (int c = 0; c < 2; ++c)
-            tma_load_3d(smem + kVOff + (vs * 2 + c) * kAtom, &tmV, &bar->v_full[vs], 64 * c, j * 128, kv_row);
+            tma_load_3d(smem + kVOff + (vs * 2 + c) * kAtom, mv, &bar->v_full[vs], 64 * c, t.key0(j), kv_row);
           issued[vs]++;
         }
       }
@@ -254,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok; ++it) {
         int w;
         if (!read_item(bar, it, w, st, abort_flag) || w < 0) break;
-        const Item t(w, n_qt, T, past, head_group);
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         if (!mbar_wait(&bar->q_tmem, it & 1, st, abort_flag, 44)) break;  // this item's Q in tensor memory
         const uint32_t qpe_addr = smem_u32(smem + kQpeOff + (it & 1) * kAtom);
         for (int j = 0; j < t.n_kv; ++j, ++gt) {
@@ -300,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok; ++it) {
         int w;
         if (!read_item(bar, it, w, st, abort_flag) || w < 0) break;
-        const Item t(w, n_qt, T, past, head_group);
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         for (int j = 0; j < t.n_kv; ++j, ++gt) {
           const int sb = gt & 1;
           // P_j is written (and, for an item's first tile, the previous item's
@@ -391,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prev_last = -1;
       }
       if (w < 0) break;
-      const Item t(w, n_qt, T, past, head_group);
+      const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
       const int qpos = t.q0 + row;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < t.n_kv; ++j, ++gt) {
@@ -414,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&bar->s_free[sb]);  // the score buffer may take S_{j+2}
-        const int k0 = j * 128;
+        const int k0 = t.key0(j);
         // max of the raw scores (the scale is positive), causal mask (key k
         // visible to query position past + qpos iff k <= past + qpos) on the
         // tiles that reach beyond the tile's first query
@@ -422,6 +448,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (k0 + c > past + qpos) s[c] = __float_as_uint(-INFINITY);
+        }
+        if constexpr (WIN) {
+          if (j < t.n_sink) {  // sinks before the window: every query sees them
+            if (k0 + 127 >= t.n_first) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (k0 + c >= t.n_first) s[c] = __float_as_uint(-INFINITY);
+            }
+          } else if (past + t.q0 + 127 - k0 >= window) {  // keys that the tile's later queries have passed
+            const int lo = past + qpos - window;  // the last key behind this query's window
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (k0 + c <= lo && k0 + c >= sinks) s[c] = __float_as_uint(-INFINITY);
+          }
         }
         // eight independent partial maxima / sums keep the reductions off a
         // single serial dependency chain; three-input maxima and two-lane
@@ -510,11 +550,18 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
       !make_tmap_bf16_3d(&tk, a.k, 192, n_keys, (uint64_t)a.B * 64, 384, (uint64_t)a.cap * 384, 64, 128) ||
       !make_tmap_bf16_3d(&tv, a.v, 128, n_keys, (uint64_t)a.B * 64, 256, (uint64_t)a.cap * 256, 64, 128))
     return cudaErrorInvalidValue;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  const bool win = a.window > 0;
+  CUtensorMap tvs = tv;
+  if (win && a.sinks > 0 &&
+      !make_tmap_bf16_3d(&tvs, a.v, 128, (uint64_t)a.sinks < n_keys ? (uint64_t)a.sinks : n_keys, (uint64_t)a.B * 64,
+                         256, (uint64_t)a.cap * 256, 64, 128))
+    return cudaErrorInvalidValue;
+  auto kern = win ? prefill_attn_tc<true> : prefill_attn_tc<false>;
+  static bool attr_set[2] = {false, false};
+  if (!attr_set[win]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set = true;
+    attr_set[win] = true;
   }
   const int n_qt = (a.T + 127) / 128;
   const long long items = (long long)n_qt * 64 * a.B;
@@ -529,8 +576,13 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   // of the group down to 4 heads made the attention faster, 2.013 -> 1.977 ms,
   // as the heads in flight read their K/V from L2; at B=1 groups under 8
   // heads leave heavy tiles of the last groups for the end)
-  const long long past_t = a.past / 128, heavy = past_t + n_qt + 1;
-  const long long per_head = (long long)n_qt * past_t + (long long)n_qt * (n_qt + 1) / 2 + n_qt;
+  const long long past_t = a.past / 128;
+  long long heavy = past_t + n_qt + 1;
+  long long per_head = (long long)n_qt * past_t + (long long)n_qt * (n_qt + 1) / 2 + n_qt;
+  if (win) {  // no tile takes more than the window's and the sinks' key tiles
+    heavy = std::min(heavy, ((long long)a.window + 254) / 128 + ((long long)a.sinks + 127) / 128 + 1);
+    per_head = std::min(per_head, n_qt * heavy);
+  }
   const long long need = (3 * (long long)grid * heavy + 2 * per_head - 1) / (2 * per_head);
   const long long kv_head_bytes = ((long long)a.past + a.T) * (192 + 128) * 2;
   int G = 1;
@@ -539,8 +591,8 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   // the work counter: an int of the status region (cleared before every call)
   int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
   DevStatus dst{st.word, st.wait_limit_ns};
-  return launch_pdl(prefill_attn_tc, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, a.o, a.T, n_qt,
-                    n_items, a.scale * 1.4426950408889634f, a.past, G, work, dst);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, tvs, a.o, a.T, n_qt, n_items,
+                    a.scale * 1.4426950408889634f, a.past, G, a.window, a.sinks, work, dst);
 }
 
 }  // namespace mla

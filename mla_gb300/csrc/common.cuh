@@ -497,6 +497,18 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// (cos, sin) of pos * inv_freq: the angle formed and reduced modulo 2 pi in
+// double precision (Cody-Waite style, 2 pi split in two doubles), then a
+// float sincos of the reduced angle, so that large positions keep float accuracy.
+__device__ __forceinline__ float2 rope_cos_sin(int pos, double inv_freq) {
+  const double ang = (double)pos * inv_freq;
+  const double kq = rint(ang * 0.15915494309189535);  // 1 / (2 pi)
+  const double red = fma(-kq, 6.283185307179586, ang) - kq * 2.4492935982947064e-16;
+  float sn, cn;
+  sincosf((float)red, &sn, &cn);
+  return make_float2(cn, sn);
+}
+
 // Packed two-lane float32 arithmetic (one instruction for both lanes, each
 // lane rounded as the scalar operation): d = a * b + c and d = a + b.
 __device__ __forceinline__ void fma_x2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0,

@@ -81,6 +81,11 @@ bool make_tmap_store_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner,
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
                        uint64_t mid_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_inner, uint32_t box_mid);
 
+// 3D view of [outer][rows][128 bytes] (contiguous), box {128 bytes, box_rows,
+// box_outer}, 128-byte swizzle: the paged cache's codes and rotary keys.
+bool make_tmap_rows128_3d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t outer, uint32_t box_rows,
+                          uint32_t box_outer);
+
 // ---- GEMM (tcgen05, TMA, persistent) --------------------------------------
 // D[b][m, n] = sum_k A[m, a_col0 + b*a_col_step + k] * Bmat(b)[n, k]
 // A is K-major.  B is either K-major ([N, K] rows, weight layout) taken from
@@ -231,6 +236,9 @@ struct PrefillAttnArgs {
   int B, T, cap;
   float scale;
   int past;                 // keys before the first query (chunked prefill), 0 otherwise
+  // sliding window (0 = none): the query at position i sees key j <= i iff
+  // i - j < window or j < sinks
+  int window = 0, sinks = 0;
 };
 cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHost& st, int num_sms,
                                      cudaStream_t stream);
@@ -278,6 +286,69 @@ cudaError_t launch_latent_attention(const LatentAttnArgs& a, const DevStatusHost
 // pos[i] = p0 + i % t for i < n (the positions of a chunk's tokens, row-major
 // over (sequence, token)).
 cudaError_t launch_chunk_positions(int* pos, int n, int t, int p0, cudaStream_t stream);
+
+// ---- paged 8-bit cache ---------------------------------------------------------
+// Pages of `page` (a power of two, 16..128) tokens; codes E4M3 [n_pages, heads,
+// page, 128], one scale per page and head, rotary keys bf16 [n_pages, page, 64],
+// table [B, max_pages].
+struct PagedCache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  __nv_bfloat16* k_pe;
+  float* k_scales;
+  float* v_scales;
+  const int* table;
+  int n_pages, max_pages, page, heads;
+};
+
+// Status words of the paged operators.  They start no memset: word 0 is
+// written by their first CTA and word kStatusExtraWord is the number of
+// further words, from word kStatusExtraFirst on, that the host ORs in (one
+// per CTA, each CTA storing its own).  Entry points that clear the region
+// leave that number zero.
+constexpr int kStatusExtraWord = 1;
+constexpr int kStatusExtraFirst = 64;
+constexpr int kMaxStatusExtra = 1024;
+
+struct PagedAppendArgs {
+  PagedCache c;
+  // source row of sequence b's token t: (cu ? cu[b] : b * T) + t; keys at
+  // k + b * k_seq + row_or_t * k_token + h * k_head, where row_or_t is the
+  // row if k_seq == 0 and t otherwise (values alike)
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long k_seq, k_token, k_head, v_seq, v_token, v_head;
+  const __nv_bfloat16* pe;     // unrotated rotary keys, row n at n * pe_token ...
+  const float* pe_f32;         // ... or in float32 (the A-projection's output); one of the two
+  long long pe_token;
+  const int* P;                // per-sequence first position (-1: idle), or null: p0 for all
+  int p0;
+  const int* cu;               // row offsets [B + 1], or null: T rows each
+  int B, T, N;
+  double inv_freq[32];
+  uint32_t* status;
+  bool status_cleared;         // the caller cleared the status region: OR into it
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+
+struct PagedAttnArgs {
+  PagedCache c;
+  const __nv_bfloat16* q;      // row b*T + t at q + row * q_row: heads x 192
+  __nv_bfloat16* o;            // row b*T + t at o + row * o_row: heads x 128
+  long long q_row, o_row;
+  const int* P;
+  int B, T, P_max, window, sinks;
+  float scale;
+  uint32_t* status;
+  bool status_cleared;
+  float* part_o;               // [2 * kPagedMaxCtas][T][4 heads][128]
+  float2* part_ml;             // [2 * kPagedMaxCtas][T][4 heads]
+  int* first_tile;             // [B + 1]: key tiles of the sequences before b
+};
+constexpr int kPagedMaxCtas = 256;
+constexpr int kPagedMaxT = 8;
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream,
+                                   int* launches);
 
 // qlat[b, h, 512:576] = q[b, h*192 + 128 : h*192 + 192]
 cudaError_t launch_copy_qpe(const __nv_bfloat16* q, __nv_bfloat16* qlat, int B, cudaStream_t stream);

@@ -1,0 +1,193 @@
+// Appending to the paged 8-bit cache.
+//
+// Per touched page and head: the new tokens' keys and values are read once
+// (a warp takes a token's 128 keys in its lower and 128 values in its upper
+// 16 lanes, 16 bytes a lane), held in registers while their largest magnitude
+// is reduced over the page's warps, and written as E4M3 codes of x * 2^-k with
+// the smallest k in [-60, 60] that keeps amax <= 448 * 2^k.  A page that
+// already holds tokens keeps max(k, old k); when k grows, its codes are
+// decoded and coded again at the new scale.  Scales are powers of two, so that
+// a code and its re-expression differ only where the larger scale drops bits.
+// The rotary keys (one per token, shared by the heads) are rotated by a
+// further row of CTAs, angles as in the RoPE table.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mla {
+
+namespace {
+
+constexpr int kFloorExp = -60, kCeilExp = 60;
+
+// Sequence b's new tokens: positions p .. p + n - 1 from source row `row` on.
+// n = 0 for an idle sequence; bad = arguments that no append can take.
+struct AppendSeq {
+  int p, n, row;
+  bool bad;
+  __device__ __forceinline__ AppendSeq(const PagedAppendArgs& a, int b) {
+    p = a.P ? a.P[b] : a.p0;
+    row = a.cu ? a.cu[b] : b * a.T;
+    n = a.cu ? a.cu[b + 1] - row : a.T;
+    const long long cap = (long long)a.c.max_pages * a.c.page;
+    bad = p < -1 || n < 0 || n > a.T || row < 0 || (long long)row + n > a.N ||
+          (p >= 0 && (long long)p + n > cap);
+    if (bad || p < 0) n = 0;
+  }
+};
+
+// The smallest k in [-60, 60] with top <= 448 * 2^k (448 = 1.75 * 2^8), top >= 0.
+__device__ __forceinline__ int block_exp(float top) {
+  const uint32_t u = __float_as_uint(top);
+  const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(kCeilExp, max(kFloorExp, k));
+}
+
+__device__ __forceinline__ float exp2_int(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+__device__ __forceinline__ uint32_t code2(float x0, float x1) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float2 decode2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 8 bf16 -> 8 codes of x * r
+__device__ __forceinline__ uint2 code8(const uint4& u, float r) {
+  const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
+  return make_uint2(code2(a.x * r, a.y * r) | code2(b.x * r, b.y * r) << 16,
+                    code2(c.x * r, c.y * r) | code2(d.x * r, d.y * r) << 16);
+}
+
+// largest |x| of 8 bf16, NaN ignored
+__device__ __forceinline__ float top8(const uint4& u) {
+  const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
+  return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+               fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+}
+
+// Grid: x = (sequence, touched page), y = head group, and one row of CTAs more
+// for the rotary keys.  W warps share a head, each holding up to 8 tokens.
+__global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs a, int pages_per_seq, int W) {
+  __shared__ float red[16][2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warps = blockDim.x >> 5;
+  const int page = a.c.page;
+
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    // every sequence and page number of the call, for the status word
+    int bad = 0;
+    for (int i = tid; i < a.B * pages_per_seq; i += blockDim.x) {
+      const int b = i / pages_per_seq, j = i - b * pages_per_seq;
+      const AppendSeq s(a, b);
+      bad |= s.bad;
+      const int pi = s.p / page + j;
+      if (s.n > 0 && pi * page < s.p + s.n) {
+        const int pid = a.c.table[(size_t)b * a.c.max_pages + pi];
+        bad |= pid < 0 || pid >= a.c.n_pages;
+      }
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+      if (!a.status_cleared) {
+        a.status[0] = bad ? kStatusBadLength : 0u;
+        a.status[kStatusExtraWord] = 0u;
+      } else if (bad) {
+        atomicOr(a.status, kStatusBadLength);
+      }
+    }
+  }
+
+  const int b = blockIdx.x / pages_per_seq, j = blockIdx.x - b * pages_per_seq;
+  const AppendSeq s(a, b);
+  const int pi = s.p / page + j;
+  const int base = pi * page;                        // the page's first position
+  if (s.n == 0 || base >= s.p + s.n) return;
+  const int pid = a.c.table[(size_t)b * a.c.max_pages + pi];
+  if (pid < 0 || pid >= a.c.n_pages) return;
+  const int slot0 = max(s.p - base, 0);              // first new slot = tokens already in the page
+  const int n = min(s.p + s.n, base + page) - (base + slot0);
+  const int t0 = base + slot0 - s.p;                 // the new token in slot0
+
+  if (blockIdx.y == gridDim.y - 1) {
+    for (int i = warp; i < n; i += warps) {
+      const long long r = (long long)(s.row + t0 + i) * a.pe_token;
+      const float x1 = a.pe ? __bfloat162float(a.pe[r + lane]) : a.pe_f32[r + lane];
+      const float x2 = a.pe ? __bfloat162float(a.pe[r + lane + 32]) : a.pe_f32[r + lane + 32];
+      const float2 cs = rope_cos_sin(base + slot0 + i, a.inv_freq[lane]);
+      __nv_bfloat16* d = a.c.k_pe + ((size_t)pid * page + slot0 + i) * 64;
+      d[lane] = __float2bfloat16_rn(x1 * cs.x - x2 * cs.y);
+      d[lane + 32] = __float2bfloat16_rn(x2 * cs.x + x1 * cs.y);
+    }
+    return;
+  }
+
+  const int h = blockIdx.y * (warps / W) + warp / W, wi = warp % W;
+  const bool live = h < a.c.heads;
+  const bool is_v = lane >= 16;
+  const int col = (lane & 15) * 8;
+  constexpr int kRows = 8;
+  uint4 u[kRows];
+  float top = 0.f;
+  float* scale_at = nullptr;
+  int k_old = kFloorExp;
+  if (live) {
+    const __nv_bfloat16* src = is_v ? a.v + b * a.v_seq + (a.v_seq ? t0 : s.row + t0) * a.v_token + h * a.v_head
+                                    : a.k + b * a.k_seq + (a.k_seq ? t0 : s.row + t0) * a.k_token + h * a.k_head;
+    const long long step = is_v ? a.v_token : a.k_token;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      u[i] = wi + i * W < n ? *reinterpret_cast<const uint4*>(src + (long long)(wi + i * W) * step + col)
+                            : make_uint4(0u, 0u, 0u, 0u);
+    scale_at = (is_v ? a.c.v_scales : a.c.k_scales) + (size_t)pid * a.c.heads + h;
+    if (slot0 > 0) k_old = min(kCeilExp, max(kFloorExp, (int)((__float_as_uint(*scale_at) >> 23) & 255) - 127));
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) top = fmaxf(top, top8(u[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  if (W > 1) {
+    if ((lane & 15) == 0) red[warp][is_v] = top;
+    __syncthreads();
+    for (int i = 0; i < W; ++i) top = fmaxf(top, red[warp - wi + i][is_v]);
+  }
+  if (!live) return;
+  const int k_new = max(k_old, block_exp(top));
+  uint8_t* dst = (is_v ? a.c.v_codes : a.c.k_codes) + ((size_t)pid * a.c.heads + h) * page * 128 + col;
+  if (slot0 > 0 && k_new > k_old) {
+    const float r = exp2_int(max(k_old - k_new, -126));
+    for (int i = wi; i < slot0; i += W) {
+      uint2* at = reinterpret_cast<uint2*>(dst + i * 128);
+      const uint2 c = *at;
+      const float2 x0 = decode2(c.x), x1 = decode2(c.x >> 16), x2 = decode2(c.y), x3 = decode2(c.y >> 16);
+      *at = make_uint2(code2(x0.x * r, x0.y * r) | code2(x1.x * r, x1.y * r) << 16,
+                       code2(x2.x * r, x2.y * r) | code2(x3.x * r, x3.y * r) << 16);
+    }
+  }
+  if (wi == 0 && (lane & 15) == 0) *scale_at = exp2_int(k_new);
+  const float r = exp2_int(-k_new);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (wi + i * W < n) *reinterpret_cast<uint2*>(dst + (slot0 + wi + i * W) * 128) = code8(u[i], r);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
+  const int pages_per_seq = (a.T - 1 + a.c.page - 1) / a.c.page + 1;
+  // 8 tokens a warp: one warp per head for a few new tokens, else page / 8
+  const int W = a.T <= 8 ? 1 : a.c.page / 8;
+  const int warps = W > 8 ? W : 8;
+  const long long gx = (long long)a.B * pages_per_seq;
+  if (gx > INT32_MAX) return cudaErrorInvalidValue;
+  const int gy = (a.c.heads * W + warps - 1) / warps + 1;
+  return launch_pdl(paged_append_kernel, dim3((unsigned)gx, gy), dim3(warps * 32), 0, stream, a, pages_per_seq, W);
+}
+
+}  // namespace mla

@@ -125,15 +125,8 @@ __global__ void __launch_bounds__(128) latent_split_kernel(const LatentArgs a) {
   reinterpret_cast<uint2*>(a.ckv + (size_t)row * 512)[tid] = ok;
   if (a.ckv_cache) reinterpret_cast<uint2*>(a.ckv_cache + ((size_t)b * a.cap + t) * 512)[tid] = ok;
   if (tid < 32) {
-    // R_t: angle (pos0 + t) * theta_i formed and reduced modulo 2 pi in double
-    // precision (Cody-Waite style, 2 pi split in two doubles), then a float
-    // sincos of the reduced angle
-    const double ang = (double)pos_row * a.inv_freq[lane];
-    const double kq = rint(ang * 0.15915494309189535);  // 1 / (2 pi)
-    const double red2 = fma(-kq, 6.283185307179586, ang) - kq * 2.4492935982947064e-16;
-    float sn, cn;
-    sincosf((float)red2, &sn, &cn);
-    const float2 cs = make_float2(cn, sn);
+    // R_t: the angle (pos0 + t) * theta_i
+    const float2 cs = rope_cos_sin(pos_row, a.inv_freq[lane]);
     if (a.pos)
       a.cs[(size_t)row * 32 + lane] = cs;  // one table row per token
     else if (b == 0)
