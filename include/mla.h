@@ -483,8 +483,8 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
  * Keys that no query of the sequence sees are not used, whatever their pages
  * hold (table entries of pages without a visible key are not looked at, so
  * pages that a window has passed can be given back).  Scores, softmax
- * statistics and sums are float32; probabilities enter the product with V as
- * two float16 parts (22 bits).
+ * statistics and sums are float32; the weights (probability times value
+ * scale) are rounded to float16 for the product with V.
  * A P[b] outside [-1, P_max] is taken as idle, a page number outside
  * [0, n_pages) is clamped, and mla_device_status then returns
  * MLA_ERR_INVALID_ARG.

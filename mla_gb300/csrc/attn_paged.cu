@@ -1,11 +1,51 @@
 // Attention of a few new tokens per sequence over the paged 8-bit cache.
 //
 // Scores s_j = scale * (kscale * (q_nope . code_j) + q_pe . kpe_j), softmax in
-// float32 over the visible keys, o = sum_j p_j vscale * code_j.  One CTA per
-// (head, query), tiles of 128 keys: a thread forms one key's score, then one
-// value dimension's sum.
+// float32 over the visible keys, o = sum_j p_j vscale * code_j: 256 bytes of
+// codes per (head, key) and 128 bytes of rotary key per key for all heads,
+// read once; about 5 flop per byte and query, so HBM bounds it as long as the
+// arithmetic on the codes keeps up.  On CUDA cores it would not (two flops a
+// code and a conversion at 6.8 TB/s are near the issue limit), so both
+// products run on mma.sync m16n8k16 with keys (then value dimensions) as the
+// 16 rows and the queries as the 8 columns: tcgen05 needs its operands in
+// shared memory in 16 bits, i.e. a written copy of every converted tile, where
+// mma.sync takes the converted codes from registers, and the tensor work is
+// small either way.
+//
+// Work: tiles of 64 keys of a group of 4 heads, flattened in (sequence, head
+// group, tile) order and cut into equal ranges, one per CTA (one CTA per SM).
+// The lengths are device data: every CTA scans them for its own range.  A
+// piece of a sequence and head group that lies in one CTA is written
+// directly; pieces that a cut separates are left as partials (at most two per
+// CTA) and merged by paged_combine_kernel, in order.
+//
+// CTA, 288 threads: warp 8 loads tiles with TMA into a 3-stage ring (4 x 64 x
+// 128 bytes of key codes, as many of value codes, 64 rotary keys, the scales;
+// 72 KB a stage, page by page from the table, whose entries it reads one tile
+// ahead).  Warps 2h and 2h + 1 take the first and last 32 keys of each tile
+// for head h of the group:
+//   * S^T = K Q^T: a thread's 16-byte loads hold 16 consecutive dimensions of
+//     one key, which are taken as the k index of four MMAs in the order in
+//     which they come (Q's fragments are laid out in the same order).  Loads
+//     hit distinct banks: rows are 128 bytes, 16-byte chunk c of row r sits at
+//     c ^ (r & 7) (TMA's 128-byte swizzle), a quad reads chunks 2t + i.
+//   * codes become float16 exactly (cvt e4m3x2 -> f16x2); q_nope is scaled by
+//     a power of two per row so that its largest element is in [1, 2) (bf16's
+//     8 bits fit float16's 11; elements below 2^-14 of the largest lose bits
+//     below 2^-24 of it).  The rotary part is a bf16 MMA with its own sum.
+//   * softmax on the accumulator fragments: a running maximum per query (moved
+//     only when it grows by more than 2^8, so that weights stay below 2^8)
+//     over log2(p) + log2(vscale), so that weights that include the value
+//     scale stay in float16's range; the sum of p is kept beside it in float32.
+//   * O^T = V^T P^T: the weights are rounded to float16 (relative 2^-11, an
+//     eighth of the output's own bf16 rounding) and transposed 8 x 8
+//     (movmatrix) into the B operand; V codes of two keys are interleaved by
+//     byte permutes into A fragments, a thread's 16 bytes being 16 rows.
+// Keys that no query sees give weight zero and their value codes are cleared
+// (they may decode to NaN).
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -15,81 +55,634 @@ namespace mla {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-__device__ __forceinline__ float decode1(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
+constexpr int kTile = 64, kStages = 3, kGroup = 4;
+constexpr int kThreads = 288;
+constexpr uint32_t kCodeBytes = kGroup * kTile * 128;
+constexpr uint32_t kVOff = kCodeBytes, kPeOff = 2 * kCodeBytes;
+constexpr uint32_t kStageBytes = 2 * kCodeBytes + kTile * 128;
+constexpr uint32_t kMergeOff = kStages * kStageBytes;
+constexpr int kMergeRows = 4;
+constexpr uint32_t kBarOff = kMergeOff + kGroup * kMergeRows * 128 * 4;
+constexpr uint32_t kSmemBytes = kBarOff + 1024 + 1024;
+static_assert(kSmemBytes <= 232448, "paged attention shared memory");
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  float scales[kStages][2][kTile / 16][kGroup];  // [k, v][page of the tile][head]
+  float2 ml[kGroup][kMergeRows];
+  int scan[kThreads / 32];
+  int first_b, first_g, first_t;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+// A sequence's keys: positions p .. p + T - 1 are its queries, keys j < len
+// with j >= w0 or j < n_first are seen by at least one of them.  Its tiles:
+// n_sink over the sinks, then those from w0 on; an idle sequence has one tile
+// without visible keys (which writes its zeros).
+struct Seq {
+  int p, len, w0, n_first, n_sink, t0, nt;
+  bool bad;
+  __device__ __forceinline__ void read(const PagedAttnArgs& a, int b) {
+    const int x = b < a.B ? a.P[b] : -1;
+    bad = x < -1 || x > a.P_max;
+    p = bad ? -1 : x;
+    len = p < 0 ? 0 : p + a.T;
+    w0 = a.window ? max(0, p - a.window + 1) : 0;
+    n_first = min(a.sinks, w0);
+    t0 = w0 / kTile;
+    n_sink = min((n_first + kTile - 1) / kTile, t0);
+    nt = p < 0 ? 1 : n_sink + (len - 1) / kTile - t0 + 1;
+  }
+  __device__ __forceinline__ int key0(int ti) const { return (ti < n_sink ? ti : ti - n_sink + t0) * kTile; }
+  // whether a query sees one of the keys j .. j + n - 1
+  __device__ __forceinline__ bool sees(int j, int n) const { return j < len && (j + n > w0 || j < n_first); }
+};
+
+struct Walk {
+  int b, grp, ti;
+  Seq s;
+  __device__ __forceinline__ void start(const PagedAttnArgs& a, const Bars* bar) {
+    b = bar->first_b;
+    grp = bar->first_g;
+    ti = bar->first_t;
+    s.read(a, b);
+  }
+  __device__ __forceinline__ void next(const PagedAttnArgs& a, int groups) {
+    if (++ti < s.nt) return;
+    ti = 0;
+    if (++grp < groups) return;
+    grp = 0;
+    s.read(a, ++b);
+  }
+};
+
+__device__ __forceinline__ long long range_start(int g, long long total, int C) { return (long long)g * total / C; }
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// four E4M3 codes -> two pairs of float16 (exact)
+__device__ __forceinline__ void decode4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 8 x 8 matrix of 16-bit elements, row r = lane / 4, columns 2 * (lane % 4) and + 1, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-__global__ void __launch_bounds__(128) paged_attn_simple(const PagedAttnArgs a) {
-  __shared__ float q[192], s[128];
-  __shared__ float red[4];
+__device__ __forceinline__ void pair_sync(int head) { 
+  switch (head) {  // barrier numbers known to the compiler
+    case 0: asm volatile("bar.sync 1, 64;" ::: "memory"); break;
+    case 1: asm volatile("bar.sync 2, 64;" ::: "memory"); break;
+    case 2: asm volatile("bar.sync 3, 64;" ::: "memory"); break;
+    default: asm volatile("bar.sync 4, 64;" ::: "memory"); break;
+  }
+ }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmPe, const PagedAttnArgs a, uint64_t wait_limit_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bar = reinterpret_cast<Bars*>(smem + kBarOff);
+  volatile int* abort_flag = &bar->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, C = gridDim.x;
+  const int groups = a.c.heads / kGroup;
+  const int tp = min(a.c.page, kTile);  // tokens of one page in a tile
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->empty[i], 8);
+    }
+    bar->abort = 0;
+    bar->first_b = bar->first_g = bar->first_t = 0;
+    fence_barrier_init();
+  }
   pdl_launch_dependents();
   pdl_wait();
-  const int h = blockIdx.x, row = blockIdx.y, b = row / a.T, t = row - b * a.T;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int p0 = a.P[b];
-  const bool idle = p0 < 0 || p0 > a.P_max;
-  bool bad = p0 < -1 || p0 > a.P_max;
-  const int qi = idle ? -1 : p0 + t;  // this query's position
-  for (int d = tid; d < 192; d += 128) q[d] = __bfloat162float(a.q[row * a.q_row + h * 192 + d]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  const int start = a.window ? max(0, qi - a.window + 1) : 0;
-  for (int k0 = 0; k0 <= qi; k0 += 128) {
-    if (a.window && k0 >= a.sinks && k0 + 127 < start) continue;
-    const int j = k0 + tid;
-    const bool seen = j <= qi && (!a.window || j >= start || j < a.sinks);
-    float x = -INFINITY;
-    if (seen) {
-      const int id = a.c.table[(size_t)b * a.c.max_pages + j / a.c.page];
-      bad |= id < 0 || id >= a.c.n_pages;
-      const int pid = min(max(id, 0), a.c.n_pages - 1);
-      const uint8_t* kc = a.c.k_codes + (((size_t)pid * a.c.heads + h) * a.c.page + j % a.c.page) * 128;
-      const __nv_bfloat16* kp = a.c.k_pe + ((size_t)pid * a.c.page + j % a.c.page) * 64;
-      float acc = 0.f, acc2 = 0.f;
-      for (int d = 0; d < 128; ++d) acc = fmaf(q[d], decode1(kc[d]), acc);
-      for (int d = 0; d < 64; ++d) acc2 = fmaf(q[128 + d], __bfloat162float(kp[d]), acc2);
-      x = (acc * a.c.k_scales[(size_t)pid * a.c.heads + h] + acc2) * (a.scale * kLog2e);
+  const DevStatus st{a.status_cleared ? a.status : a.status + kStatusExtraFirst + cta, wait_limit_ns};
+  if (tid == 0 && !a.status_cleared) {
+    *st.word = 0u;
+    if (cta == 0) {
+      a.status[0] = 0u;
+      a.status[kStatusExtraWord] = (uint32_t)C;
     }
-    float mx = warp_max(x);
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float m_new = fmaxf(m, mx), ref = m_new == -INFINITY ? 0.f : m_new;
-    s[tid] = exp2f(x - ref);
-    __syncthreads();
-    const float alpha = exp2f(m - ref);
-    m = m_new;
-    l *= alpha;
-    o *= alpha;
-    for (int i = 0; i < 128 && k0 + i <= qi; ++i) {
-      const int jj = k0 + i;
-      if (a.window && jj < start && jj >= a.sinks) continue;
-      const int id = a.c.table[(size_t)b * a.c.max_pages + jj / a.c.page];
-      const int pid = min(max(id, 0), a.c.n_pages - 1);
-      const uint8_t* vc = a.c.v_codes + (((size_t)pid * a.c.heads + h) * a.c.page + jj % a.c.page) * 128;
-      l += s[i];
-      o = fmaf(s[i] * a.c.v_scales[(size_t)pid * a.c.heads + h], decode1(vc[tid]), o);
-    }
-    __syncthreads();
   }
-  a.o[row * a.o_row + h * 128 + tid] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-  if (bad) atomicOr(a.status, kStatusBadLength);
+
+  // this CTA's range of the flattened tiles
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  int sum = 0;
+  Seq sq;
+  for (int b = b0; b < b1; ++b) {
+    sq.read(a, b);
+    sum += sq.nt;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) bar->scan[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += bar->scan[i];
+    all += bar->scan[i];
+  }
+  const long long total = (long long)all * groups;
+  const long long x0 = range_start(cta, total, C);
+  const int R = (int)(range_start(cta + 1, total, C) - x0);
+  {
+    int e = before + incl - sum;  // tiles before b0
+    const bool mine = x0 >= (long long)e * groups && x0 < (long long)(e + sum) * groups;
+    if (mine || cta == 0) {
+      for (int b = b0; b < b1; ++b) {
+        sq.read(a, b);
+        if (cta == 0) a.first_tile[b] = e;
+        if (x0 >= (long long)e * groups && x0 < (long long)(e + sq.nt) * groups) {
+          const int r = (int)(x0 - (long long)e * groups);
+          bar->first_b = b;
+          bar->first_g = r / sq.nt;
+          bar->first_t = r % sq.nt;
+        }
+        e += sq.nt;
+      }
+      if (cta == 0 && tid == 0) a.first_tile[a.B] = all;
+    }
+  }
+  __syncthreads();
+  Walk w;
+  if (R > 0) w.start(a, bar);
+  const int first_b = bar->first_b, first_g = bar->first_g;
+
+  if (warp == 8) {
+    if (lane == 0 && R > 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmPe);
+      const int n_sub = kTile / tp;
+      constexpr int kNone = INT_MIN;
+      bool bad = false;
+      int ent[kTile / 16];
+      auto fetch = [&](int (&e)[kTile / 16]) {  // page numbers of the walk's tile (kNone: no visible key there)
+        const int k0 = w.s.key0(w.ti);
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) {
+          const int j = k0 + i * tp;
+          e[i] = i < n_sub && w.s.sees(j, tp) ? a.c.table[(size_t)w.b * a.c.max_pages + j / a.c.page] : kNone;
+        }
+      };
+      fetch(ent);
+      int issued = 0;
+      for (int i = 0; i < R; ++i) {
+        const int k0 = w.s.key0(w.ti), grp = w.grp;
+        bad |= w.s.bad;
+        int nxt[kTile / 16];
+        if (i + 1 < R) {
+          w.next(a, groups);
+          fetch(nxt);
+        }
+        const int stg = i % kStages;
+        if (i >= kStages && !mbar_wait(&bar->empty[stg], (i / kStages - 1) & 1, st, abort_flag, 81)) break;
+        uint8_t* base = smem + stg * kStageBytes;
+        mbar_arrive_expect_tx(&bar->full[stg], kStageBytes + n_sub * 32);
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s) {
+          if (s < n_sub) {
+            int pid = ent[s];
+            if (pid == kNone) pid = 0;
+            bad |= pid < 0 || pid >= a.c.n_pages;
+            pid = min(max(pid, 0), a.c.n_pages - 1);
+            const int row = (k0 + s * tp) & (a.c.page - 1);
+            const int plane = pid * a.c.heads + grp * kGroup;
+            const uint32_t off = (uint32_t)(s * tp * 128);
+            tma_load_3d(base + off * kGroup, &tmK, &bar->full[stg], 0, row, plane);
+            tma_load_3d(base + kPeOff + off, &tmPe, &bar->full[stg], 0, row, pid);
+            tma_load_3d(base + kVOff + off * kGroup, &tmV, &bar->full[stg], 0, row, plane);
+            bulk_load(bar->scales[stg][0][s], a.c.k_scales + plane, 16, &bar->full[stg]);
+            bulk_load(bar->scales[stg][1][s], a.c.v_scales + plane, 16, &bar->full[stg]);
+          }
+        }
+        ++issued;
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s) ent[s] = nxt[s];
+      }
+      // no copy may still be in flight into shared memory
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        mbar_wait(&bar->full[i % kStages], (i / kStages) & 1, st, nullptr, 82);
+      if (bad) atomicOr(st.word, kStatusBadLength);
+    }
+    return;
+  }
+
+  // ---- warps 0..7: head hh of the group, keys half * 32 .. + 31 of each tile ----
+  const int hh = warp >> 1, half = warp & 1;
+  const int g = lane >> 2, t = lane & 3;
+  const float sl2 = a.scale * kLog2e;
+  float* merge = reinterpret_cast<float*>(smem + kMergeOff) + hh * kMergeRows * 128;
+  // byte offsets of the 16-key blocks of this half inside K / V (and, with one head, inside the rotary keys)
+  uint32_t off16[2], pe16[2];
+  int sub16[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    const int tok = half * 32 + ks * 16;
+    sub16[ks] = tok / tp;
+    off16[ks] = (uint32_t)((sub16[ks] * kGroup + hh) * tp + (tok & (tp - 1))) * 128;
+    pe16[ks] = (uint32_t)tok * 128;
+  }
+  uint32_t qa[8][2], qp[4][2];  // Q's row g (B operand)
+  float acc[8][4];              // O^T: dimensions 16g + 2i (+ 1 in [2], [3]), queries 2t and 2t + 1
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, qs[2] = {0.f, 0.f};  // of queries 2t and 2t + 1
+  bool ok = true;
+
+  for (int i = 0; i < R; ++i) {
+    const int stg = i % kStages;
+    const bool seg_first = i == 0 || w.ti == 0;
+    const bool seg_last = i == R - 1 || w.ti == w.s.nt - 1;
+    const int head = w.grp * kGroup + hh;
+    if (seg_first) {
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+      // Q: dimensions 32t .. 32t+31 of the nope part, 16t .. 16t+15 of the rotary part of row g
+      uint4 u[4], r[2];
+      const bool row = g < a.T && w.s.p >= 0;
+      const __nv_bfloat16* q = a.q + ((long long)w.b * a.T + g) * a.q_row + head * 192;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        u[c] = row ? reinterpret_cast<const uint4*>(q + 32 * t)[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        r[c] = row ? reinterpret_cast<const uint4*>(q + 128 + 16 * t)[c] : make_uint4(0u, 0u, 0u, 0u);
+      float top = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_bf16x2(x[e]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = min(126, max(-126, (int)(__float_as_uint(top) >> 23) - 127));
+      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + ex) << 23) * sl2;
+      qs[0] = __shfl_sync(0xffffffffu, up, 8 * t);
+      qs[1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_bf16x2(x[e]);
+          qa[c * 2 + (e >> 1)][e & 1] = pack_f16x2(f.x * down, f.y * down);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qp[2 * c][0] = r[c].x;
+        qp[2 * c][1] = r[c].y;
+        qp[2 * c + 1][0] = r[c].z;
+        qp[2 * c + 1][1] = r[c].w;
+      }
+    }
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar->full[stg], (i / kStages) & 1, st, abort_flag, 83));
+    const int a0 = w.s.key0(w.ti) + half * 32;  // this warp's first key
+    if (ok && w.s.sees(a0, 32)) {
+      const uint8_t* kb = smem + stg * kStageBytes;
+      const uint8_t* vb = kb + kVOff;
+      const uint8_t* pb = kb + kPeOff;
+      // every query of the sequence sees all 32 keys
+      const bool full = a0 + 31 <= w.s.p &&
+                        (a.window == 0 || a0 > w.s.p + a.T - 1 - a.window || a0 + 31 < a.sinks);
+      float ksc[2], vsc[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        ksc[ks] = bar->scales[stg][0][sub16[ks]][hh];
+        vsc[ks] = bar->scales[stg][1][sub16[ks]][hh];
+      }
+      // scores of 16 keys at a time: keys g ([0], [1]) and g + 8 ([2], [3]) of queries 2t and 2t + 1
+      float s[2][4];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint8_t* kr = kb + off16[ks] + (uint32_t)g * 128;
+        const uint8_t* pr = pb + pe16[ks] + (uint32_t)g * 128;
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const uint32_t chunk = (uint32_t)(((2 * t + h2) ^ g) << 4);
+          const uint4 x = *reinterpret_cast<const uint4*>(kr + chunk);
+          const uint4 x8 = *reinterpret_cast<const uint4*>(kr + 1024 + chunk);
+          const uint32_t cw[4] = {x.x, x.y, x.z, x.w}, cw8[4] = {x8.x, x8.y, x8.z, x8.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t a0, a1, a2, a3;
+            decode4(cw[e], a0, a2);
+            decode4(cw8[e], a1, a3);
+            mma_f16(c, a0, a1, a2, a3, qa[h2 * 4 + e][0], qa[h2 * 4 + e][1]);
+          }
+          const uint4 y = *reinterpret_cast<const uint4*>(pr + chunk);
+          const uint4 y8 = *reinterpret_cast<const uint4*>(pr + 1024 + chunk);
+          mma_bf16(d, y.x, y8.x, y.y, y8.y, qp[h2 * 2][0], qp[h2 * 2][1]);
+          mma_bf16(d, y.z, y8.z, y.w, y8.w, qp[h2 * 2 + 1][0], qp[h2 * 2 + 1][1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[ks][e] = fmaf(c[e], ksc[ks] * qs[e & 1], d[e] * sl2);
+      }
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int qi = w.s.p + min(2 * t + (e & 1), a.T - 1);  // the query's position
+          const int lo = a.window ? qi - a.window : -1;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const int j = a0 + ks * 16 + (e >> 1) * 8 + g;
+            if (j > qi || (j <= lo && j >= a.sinks)) s[ks][e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          if (!w.s.sees(a0 + ks * 16, 16)) vsc[ks] = 1.f;  // nothing there: its scale may be anything
+      }
+      // running maximum of log2(p * vscale) per query, over the 8 lanes of its column
+      const float lv[2] = {__log2f(vsc[0]), __log2f(vsc[1])};
+      float mx[2];
+      bool need[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(fmaxf(s[0][e], s[0][e + 2]) + lv[0], fmaxf(s[1][e], s[1][e + 2]) + lv[1]);
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+        need[e] = mx[e] > m[e] + kRescaleThreshold;
+      }
+      if (__any_sync(0xffffffffu, need[0] | need[1])) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          alpha[e] = need[e] ? ex2_approx(m[e] - mx[e]) : 1.f;
+          if (need[e]) m[e] = mx[e];
+          l[e] *= alpha[e];
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[c][e] *= alpha[e & 1];
+      }
+      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      uint32_t pb16[2][2];  // weights of keys 2t, 2t+1 (and 8 further) of query g
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = ex2_approx(s[ks][e] - ref[e & 1]);
+          l[e & 1] += p[e];
+        }
+        pb16[ks][0] = transpose8(pack_f16x2(p[0] * vsc[ks], p[1] * vsc[ks]));
+        pb16[ks][1] = transpose8(pack_f16x2(p[2] * vsc[ks], p[3] * vsc[ks]));
+      }
+      // V: keys 2t, 2t+1, 2t+8, 2t+9 of each 16, dimensions 16g .. 16g+15
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const uint8_t* vr = vb + off16[ks] + (uint32_t)(2 * t) * 128;
+        const uint32_t ce = (uint32_t)((g ^ (2 * t)) << 4), co = (uint32_t)((g ^ (2 * t + 1)) << 4);
+        uint4 x0 = *reinterpret_cast<const uint4*>(vr + ce);
+        uint4 x1 = *reinterpret_cast<const uint4*>(vr + 128 + co);
+        uint4 x2 = *reinterpret_cast<const uint4*>(vr + 1024 + ce);
+        uint4 x3 = *reinterpret_cast<const uint4*>(vr + 1152 + co);
+        if (!full) {
+          const int j = a0 + ks * 16 + 2 * t;
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+          if (!w.s.sees(j, 1)) x0 = z;
+          if (!w.s.sees(j + 1, 1)) x1 = z;
+          if (!w.s.sees(j + 8, 1)) x2 = z;
+          if (!w.s.sees(j + 9, 1)) x3 = z;
+        }
+        const uint32_t e0[4] = {x0.x, x0.y, x0.z, x0.w}, e1[4] = {x1.x, x1.y, x1.z, x1.w};
+        const uint32_t e2[4] = {x2.x, x2.y, x2.z, x2.w}, e3[4] = {x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t a0_, a1_, a2_, a3_;
+          decode4(__byte_perm(e0[e], e1[e], 0x5140), a0_, a1_);
+          decode4(__byte_perm(e2[e], e3[e], 0x5140), a2_, a3_);
+          mma_f16(acc[2 * e], a0_, a1_, a2_, a3_, pb16[ks][0], pb16[ks][1]);
+          decode4(__byte_perm(e0[e], e1[e], 0x7362), a0_, a1_);
+          decode4(__byte_perm(e2[e], e3[e], 0x7362), a2_, a3_);
+          mma_f16(acc[2 * e + 1], a0_, a1_, a2_, a3_, pb16[ks][0], pb16[ks][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->empty[stg]);
+
+    if (seg_last) {
+      // the pair's two halves become one, then the rows are written
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
+      for (int r0 = 0; r0 < a.T; r0 += kMergeRows) {
+        if (half == 1) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 2 * t + e;
+            if (row >= r0 && row < r0 + kMergeRows && row < a.T) {
+              float* at = merge + (row - r0) * 128 + 16 * g;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                reinterpret_cast<float4*>(at)[(c + (g >> 1)) & 3] =
+                    make_float4(acc[2 * c][e], acc[2 * c][e + 2], acc[2 * c + 1][e], acc[2 * c + 1][e + 2]);
+              if (g == 0) bar->ml[hh][row - r0] = make_float2(m[e], l[e]);
+            }
+          }
+        }
+        pair_sync(hh);
+        if (half == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 2 * t + e;
+            if (row >= r0 && row < r0 + kMergeRows && row < a.T) {
+              const float2 ml = bar->ml[hh][row - r0];
+              const float mm = fmaxf(m[e], ml.x), ref = mm == -INFINITY ? 0.f : mm;
+              const float f0 = ex2_approx(m[e] - ref), f1 = ex2_approx(ml.x - ref);
+              m[e] = mm;
+              l[e] = l[e] * f0 + ml.y * f1;
+              const float* at = merge + (row - r0) * 128 + 16 * g;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float4 x = reinterpret_cast<const float4*>(at)[(c + (g >> 1)) & 3];
+                acc[2 * c][e] = acc[2 * c][e] * f0 + x.x * f1;
+                acc[2 * c][e + 2] = acc[2 * c][e + 2] * f0 + x.y * f1;
+                acc[2 * c + 1][e] = acc[2 * c + 1][e] * f0 + x.z * f1;
+                acc[2 * c + 1][e + 2] = acc[2 * c + 1][e + 2] * f0 + x.w * f1;
+              }
+            }
+          }
+        }
+        pair_sync(hh);
+      }
+      if (ok && half == 0) {
+        const bool whole = w.ti == w.s.nt - 1 && i >= w.ti;  // its first tile is in this CTA too
+        const int slot = 2 * cta + (w.b == first_b && w.grp == first_g ? 0 : 1);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 2 * t + e;
+          if (row >= a.T) continue;
+          if (whole) {
+            const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+            uint4* d = reinterpret_cast<uint4*>(a.o + ((long long)w.b * a.T + row) * a.o_row + head * 128 + 16 * g);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              d[c] = make_uint4(pack_bf16x2(acc[4 * c][e] * inv, acc[4 * c][e + 2] * inv),
+                                pack_bf16x2(acc[4 * c + 1][e] * inv, acc[4 * c + 1][e + 2] * inv),
+                                pack_bf16x2(acc[4 * c + 2][e] * inv, acc[4 * c + 2][e + 2] * inv),
+                                pack_bf16x2(acc[4 * c + 3][e] * inv, acc[4 * c + 3][e + 2] * inv));
+          } else {
+            const size_t at = ((size_t)slot * a.T + row) * kGroup + hh;
+            float4* d = reinterpret_cast<float4*>(a.part_o + at * 128 + 16 * g);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              d[c] = make_float4(acc[2 * c][e], acc[2 * c][e + 2], acc[2 * c + 1][e], acc[2 * c + 1][e + 2]);
+            if (g == 0) a.part_ml[at] = make_float2(m[e], l[e]);
+          }
+        }
+      }
+    }
+    if (i + 1 < R) w.next(a, groups);
+  }
+}
+
+// Merges the pieces of the (sequence, head group) pairs that a cut between
+// CTAs separates; the others were written by paged_attn_kernel.  One warp per
+// head, 4 dimensions a lane; pieces four at a time, in order.
+__global__ void __launch_bounds__(32 * kGroup) paged_combine_kernel(const PagedAttnArgs a, int C) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int groups = a.c.heads / kGroup;
+  const int b = blockIdx.x / groups, grp = blockIdx.x - b * groups;
+  const int hh = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e = a.first_tile[b], nt = a.first_tile[b + 1] - e;
+  const long long total = (long long)a.first_tile[a.B] * groups;
+  const long long xa = (long long)e * groups + (long long)grp * nt, xb = xa + nt - 1;
+  // the CTA that holds flattened tile x: the largest g with range_start(g) <= x
+  const int g0 = (int)(((xa + 1) * C - 1) / total), g1 = (int)(((xb + 1) * C - 1) / total);
+  if (g0 == g1) return;
+  for (int t = 0; t < a.T; ++t) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = g0; k0 <= g1; k0 += 4) {
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int gg = k0 + k;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (gg > g1) continue;
+        const long long start = range_start(gg, total, C);
+        if (start == range_start(gg + 1, total, C)) continue;  // a CTA without tiles
+        const size_t at = ((size_t)(2 * gg + (start >= xa ? 0 : 1)) * a.T + t) * kGroup + hh;
+        ml[k] = a.part_ml[at];
+        x[k] = reinterpret_cast<const float4*>(a.part_o + at * 128)[lane];
+      }
+      const float mm = fmaxf(fmax3(m, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      const float f = exp2f(m - ref);
+      m = mm;
+      l *= f;
+      o.x *= f;
+      o.y *= f;
+      o.z *= f;
+      o.w *= f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float wk = exp2f(ml[k].x - ref);
+        l = fmaf(wk, ml[k].y, l);
+        o.x = fmaf(wk, x[k].x, o.x);
+        o.y = fmaf(wk, x[k].y, o.y);
+        o.z = fmaf(wk, x[k].z, o.z);
+        o.w = fmaf(wk, x[k].w, o.w);
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint2 r;
+    r.x = pack_bf16x2(o.x * inv, o.y * inv);
+    r.y = pack_bf16x2(o.z * inv, o.w * inv);
+    reinterpret_cast<uint2*>(a.o + ((long long)b * a.T + t) * a.o_row + (grp * kGroup + hh) * 128)[lane] = r;
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream,
                                    int* launches) {
-  (void)st;
-  (void)num_sms;
-  if (!a.status_cleared) {
-    const cudaError_t e = cudaMemsetAsync(a.status, 0, 256, stream);
+  const int tp = std::min(a.c.page, kTile);
+  CUtensorMap tk, tv, tpe;
+  const uint64_t planes = (uint64_t)a.c.n_pages * a.c.heads;
+  if (!make_tmap_rows128_3d(&tk, a.c.k_codes, a.c.page, planes, tp, kGroup) ||
+      !make_tmap_rows128_3d(&tv, a.c.v_codes, a.c.page, planes, tp, kGroup) ||
+      !make_tmap_rows128_3d(&tpe, a.c.k_pe, a.c.page, a.c.n_pages, tp, 1))
+    return cudaErrorInvalidValue;
+  constexpr int kMaxDevices = 64;
+  static bool attr_set[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) attr_set[dev] = true;
   }
+  // the most tiles that a sequence can have
+  long long nt = ((long long)a.P_max + a.T + kTile - 1) / kTile;
+  if (a.window)
+    nt = std::min(nt, ((long long)a.window + a.T - 2) / kTile + 2 + ((long long)a.sinks + kTile - 1) / kTile);
+  const long long most = nt * a.B * (a.c.heads / kGroup);
+  if (nt * a.B > INT32_MAX || (long long)a.B * (a.c.heads / kGroup) > INT32_MAX) return cudaErrorInvalidValue;
+  const int C = (int)std::min<long long>(most, std::min(num_sms, kPagedMaxCtas));
+  e = launch_pdl(paged_attn_kernel, dim3(C), dim3(kThreads), kSmemBytes, stream, tk, tv, tpe, a, st.wait_limit_ns);
+  if (e != cudaSuccess) return e;
   ++*launches;
-  return launch_pdl(paged_attn_simple, dim3(a.c.heads, a.B * a.T), dim3(128), 0, stream, a);
+  if (nt > 1) {  // with one tile per sequence nothing is cut
+    e = launch_pdl(paged_combine_kernel, dim3((unsigned)(a.B * (a.c.heads / kGroup))), dim3(32 * kGroup), 0, stream, a,
+                   C);
+    ++*launches;
+  }
+  return e;
 }
 
 }  // namespace mla
