@@ -386,66 +386,92 @@ def make_paged_cache(t: dict) -> MlaPagedCache:
     s = MlaPagedCache(*[t[n].data_ptr() for n in PAGED_TENSORS], t["table"].data_ptr(), n_pages, t["table"].shape[1],
                       page, heads)
     s._keep = dict(t)
+    # what every call of a decode loop looks up: read once here
+    s._ref, s._device, s._batch = ctypes.byref(s), t["table"].get_device(), t["table"].shape[0]
     return s
 
 
-def _rows(x, what: str, cols: int):
-    """Row stride of a bf16 CUDA tensor [rows, cols] whose rows are contiguous."""
-    import torch
-    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2 or x.shape[1] != cols or x.stride(1) != 1:
-        raise ValueError(f"{what}: need a bf16 CUDA tensor [rows, {cols}] with contiguous rows")
-    return x.stride(0)
+# The paged calls take a few microseconds on the GPU at decode sizes, so that
+# their argument checks are kept to one attribute each: get_device() is -1 for
+# a tensor that is not on a GPU.
+def _rows(x, what: str, cols: int, device: int) -> int:
+    """Row stride of a bf16 tensor [rows, cols] on the device whose rows are contiguous."""
+    shape, stride = x.shape, x.stride()
+    if not (x.dtype is _torch.bfloat16 and x.get_device() == device and len(shape) == 2 and shape[1] == cols and
+            stride[1] == 1):
+        raise ValueError(f"{what}: need a bf16 tensor [rows, {cols}] with contiguous rows on the current device")
+    return stride[0]
 
 
-def _head_rows(x, what: str, heads: int):
-    """Token and head strides of a bf16 CUDA tensor [rows, heads, 128] whose last dimension is contiguous."""
-    import torch
-    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != 128 or \
-            x.stride(2) != 1:
-        raise ValueError(f"{what}: need a bf16 CUDA tensor [rows, {heads}, 128] with a contiguous last dimension")
-    return x.stride(0), x.stride(1)
+def _head_rows(x, what: str, heads: int, rows: int, device: int):
+    """Token and head strides of a bf16 tensor [rows, heads, 128] on the device, its last dimension contiguous."""
+    stride = x.stride()
+    if not (x.dtype is _torch.bfloat16 and x.get_device() == device and x.shape == (rows, heads, 128) and
+            stride[2] == 1):
+        raise ValueError(f"{what}: need a bf16 tensor [{rows}, {heads}, 128] with a contiguous last dimension on the "
+                         "current device")
+    return stride[0], stride[1]
 
 
-def _ints(x, what: str, n: int):
-    import torch
-    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or x.dim() != 1 or x.numel() != n:
-        raise ValueError(f"{what}: need a contiguous int32 CUDA tensor of {n} elements")
+def _ints(x, what: str, n: int, device: int) -> int:
+    if not (x.dtype is _torch.int32 and x.get_device() == device and x.shape == (n,) and x.is_contiguous()):
+        raise ValueError(f"{what}: need a contiguous int32 tensor of {n} elements on the current device")
+    return x.data_ptr()
+
+
+def _bytes(x, device: int) -> int:
+    if x.get_device() != device or not x.is_contiguous():
+        raise ValueError("workspace: need a contiguous tensor on the current device")
+    return x.data_ptr()
+
+
+def _stream_on(device: int, stream) -> int:
+    """The stream's handle (the current one of the device if None); the device has to be the current one."""
+    global _torch
+    if _torch is None:
+        import torch as _torch
+    if device < 0 or _torch.cuda.current_device() != device:
+        raise ValueError("the tensors are not on the current CUDA device")
+    return stream.cuda_stream if stream is not None else _torch._C._cuda_getCurrentRawStream(device)
+
+
+_torch = None
 
 
 def mla_paged_append(cache: MlaPagedCache, k, v, k_pe, P, T: int, workspace, cu=None,
                      params: MlaParams | None = None, stream=None):
-    """k, v: bf16 [N, heads, 128] (views of a kv_b product are fine); k_pe: bf16 [N, 64], unrotated; P: int32 CUDA
-    [B], position of each sequence's first new token (-1: idle); T tokens each, or with cu (int32 CUDA [B + 1],
-    row offsets) at most T; workspace of MODE_PAGED_APPEND."""
-    B, N = cache._keep["table"].shape[0], k.shape[0]
-    k_token, k_head = _head_rows(k, "k", cache.heads)
-    v_token, v_head = _head_rows(v, "v", cache.heads)
-    pe_token = _rows(k_pe, "k_pe", QK_ROPE)
-    _ints(P, "P", B)
-    if cu is not None:
-        _ints(cu, "cu", B + 1)
-    if v.shape[0] != N or k_pe.shape[0] != N:
-        raise ValueError("k, v and k_pe: need the same number of rows")
-    rc = lib().mla_paged_append(ctypes.byref(cache), None if params is None else ctypes.byref(params), k.data_ptr(),
-                                k_token, k_head, v.data_ptr(), v_token, v_head, k_pe.data_ptr(), pe_token,
-                                P.data_ptr(), None if cu is None else cu.data_ptr(), B, T, N, workspace.data_ptr(),
-                                workspace.numel(), _stream(stream))
+    """k, v: bf16 [N, heads, 128] (views of a kv_b product are fine); k_pe: bf16 [N, 64], unrotated; P: int32 [B],
+    position of each sequence's first new token (-1: idle); T tokens each, or with cu (int32 [B + 1], row offsets)
+    at most T; workspace of MODE_PAGED_APPEND."""
+    dev, B = cache._device, cache._batch
+    s = _stream_on(dev, stream)
+    N = k.shape[0]
+    k_token, k_head = _head_rows(k, "k", cache.heads, N, dev)
+    v_token, v_head = _head_rows(v, "v", cache.heads, N, dev)
+    pe_token = _rows(k_pe, "k_pe", QK_ROPE, dev)
+    if k_pe.shape[0] != N:
+        raise ValueError("k_pe: need as many rows as k and v")
+    rc = lib().mla_paged_append(cache._ref, None if params is None else ctypes.byref(params), k.data_ptr(), k_token,
+                                k_head, v.data_ptr(), v_token, v_head, k_pe.data_ptr(), pe_token,
+                                _ints(P, "P", B, dev), None if cu is None else _ints(cu, "cu", B + 1, dev), B, T, N,
+                                _bytes(workspace, dev), workspace.nbytes, s)
     _check(rc, "mla_paged_append")
 
 
 def mla_paged_attention(cache: MlaPagedCache, q, P, P_max: int, out, workspace, window: int = 0, sinks: int = 0,
                         params: MlaParams | None = None, stream=None):
-    """q: bf16 [B * T, heads * 192] (rotated); out: bf16 [B * T, heads * 128]; P: int32 CUDA [B], position of each
+    """q: bf16 [B * T, heads * 192] (rotated); out: bf16 [B * T, heads * 128]; P: int32 [B], position of each
     sequence's first query (-1: idle, its rows become zeros), at most P_max; window 0 = every key, else the last
     `window` keys and the first `sinks`; workspace of MODE_PAGED_ATTN."""
-    B = cache._keep["table"].shape[0]
-    q_row, out_row = _rows(q, "q", cache.heads * QK), _rows(out, "out", cache.heads * V)
-    _ints(P, "P", B)
-    if q.shape[0] % B or out.shape[0] != q.shape[0]:
+    dev, B = cache._device, cache._batch
+    s = _stream_on(dev, stream)
+    q_row, out_row = _rows(q, "q", cache.heads * QK, dev), _rows(out, "out", cache.heads * V, dev)
+    n = q.shape[0]
+    if n % B or out.shape[0] != n:
         raise ValueError("q and out: need the same number of rows, T for each sequence of the table")
-    rc = lib().mla_paged_attention(ctypes.byref(cache), None if params is None else ctypes.byref(params),
-                                   q.data_ptr(), q_row, B, q.shape[0] // B, P.data_ptr(), P_max, window, sinks,
-                                   out.data_ptr(), out_row, workspace.data_ptr(), workspace.numel(), _stream(stream))
+    rc = lib().mla_paged_attention(cache._ref, None if params is None else ctypes.byref(params), q.data_ptr(), q_row,
+                                   B, n // B, _ints(P, "P", B, dev), P_max, window, sinks, out.data_ptr(), out_row,
+                                   _bytes(workspace, dev), workspace.nbytes, s)
     _check(rc, "mla_paged_attention")
 
 
@@ -454,15 +480,16 @@ def mla_window_attention(q, P0: int, k_cache, v_cache, out, workspace, window: i
     """q: bf16 [B, T, 64 * 192] at positions P0..P0+T-1; k_cache [B, 64, cap, 192], v_cache [B, 64, cap, 128];
     out: bf16 [B, T, 64 * 128]; a query sees the last `window` keys up to its own and the first `sinks`;
     workspace of MODE_WINDOW_ATTN."""
-    import torch
+    dev = q.get_device()
+    s = _stream_on(dev, stream)
     B, T, cap = q.shape[0], q.shape[1], k_cache.shape[2]
     for x, what, shape in ((q, "q", (B, T, HEADS * QK)), (k_cache, "k_cache", (B, HEADS, cap, QK)),
                            (v_cache, "v_cache", (B, HEADS, cap, V)), (out, "out", (B, T, HEADS * V))):
-        if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != shape:
-            raise ValueError(f"{what}: need a contiguous bf16 CUDA tensor of shape {shape}")
-    rc = lib().mla_window_attention(None if params is None else ctypes.byref(params), _ptr(q), B, T, P0,
-                                    _ptr(k_cache), _ptr(v_cache), cap, window, sinks, _ptr(out), _ptr(workspace),
-                                    workspace.numel(), _stream(stream))
+        if not (x.dtype is _torch.bfloat16 and x.get_device() == dev and x.is_contiguous() and x.shape == shape):
+            raise ValueError(f"{what}: need a contiguous bf16 tensor of shape {shape} on the current device")
+    rc = lib().mla_window_attention(None if params is None else ctypes.byref(params), q.data_ptr(), B, T, P0,
+                                    k_cache.data_ptr(), v_cache.data_ptr(), cap, window, sinks, out.data_ptr(),
+                                    _bytes(workspace, dev), workspace.nbytes, s)
     _check(rc, "mla_window_attention")
 
 

@@ -19,11 +19,14 @@
 // directly; pieces that a cut separates are left as partials (at most two per
 // CTA) and merged by paged_combine_kernel, in order.
 //
-// CTA, 288 threads: warp 8 loads tiles with TMA into a 3-stage ring (4 x 64 x
-// 128 bytes of key codes, as many of value codes, 64 rotary keys, the scales;
-// 72 KB a stage, page by page from the table, whose entries it reads one tile
-// ahead).  Warps 2h and 2h + 1 take the first and last 32 keys of each tile
-// for head h of the group:
+// CTA, 384 threads: warps 8..11 fill a 3-stage ring (72 KB a stage) with tiles,
+// page by page from the table, whose entries they read ahead: warp 8 the key
+// codes (4 x 64 x 128 bytes), 9 the value codes, 10 the 64 rotary keys (TMA),
+// 11 the scales (plain loads).  One thread issuing all of a tile's copies was
+// the limit with 16-token pages, 20 copies a tile: 32 sequences of up to 8192
+// keys 463 us, with four warps 382 us.  Warps 2h and 2h + 1 take the first and
+// last 32 keys of each tile for head h of the group (against every second tile
+// each, which holds a stage for longer: 64 x 1001 keys 169 us against 177 us):
 //   * S^T = K Q^T: a thread's 16-byte loads hold 16 consecutive dimensions of
 //     one key, which are taken as the k index of four MMAs in the order in
 //     which they come (Q's fragments are laid out in the same order).  Loads
@@ -58,7 +61,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 constexpr int kTile = 64, kStages = 3, kGroup = 4;
-constexpr int kThreads = 288;
+constexpr int kThreads = 384;
 constexpr uint32_t kCodeBytes = kGroup * kTile * 128;
 constexpr uint32_t kVOff = kCodeBytes, kPeOff = 2 * kCodeBytes;
 constexpr uint32_t kStageBytes = 2 * kCodeBytes + kTile * 128;
@@ -178,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bar->full[i], 1);
-      mbar_init(&bar->empty[i], 8);
+      mbar_init(&bar->full[i], 4);
+      mbar_init(&bar->empty[i], 2 * kGroup);
     }
     bar->abort = 0;
     bar->first_b = bar->first_g = bar->first_t = 0;
@@ -245,62 +248,88 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (R > 0) w.start(a, bar);
   const int first_b = bar->first_b, first_g = bar->first_g;
 
-  if (warp == 8) {
-    if (lane == 0 && R > 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmPe);
-      const int n_sub = kTile / tp;
-      constexpr int kNone = INT_MIN;
-      bool bad = false;
-      int ent[kTile / 16];
-      auto fetch = [&](int (&e)[kTile / 16]) {  // page numbers of the walk's tile (kNone: no visible key there)
-        const int k0 = w.s.key0(w.ti);
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i) {
-          const int j = k0 + i * tp;
-          e[i] = i < n_sub && w.s.sees(j, tp) ? a.c.table[(size_t)w.b * a.c.max_pages + j / a.c.page] : kNone;
-        }
-      };
-      fetch(ent);
-      int issued = 0;
-      for (int i = 0; i < R; ++i) {
-        const int k0 = w.s.key0(w.ti), grp = w.grp;
-        bad |= w.s.bad;
-        int nxt[kTile / 16];
-        if (i + 1 < R) {
-          w.next(a, groups);
-          fetch(nxt);
-        }
-        const int stg = i % kStages;
-        if (i >= kStages && !mbar_wait(&bar->empty[stg], (i / kStages - 1) & 1, st, abort_flag, 81)) break;
-        uint8_t* base = smem + stg * kStageBytes;
-        mbar_arrive_expect_tx(&bar->full[stg], kStageBytes + n_sub * 32);
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s) {
-          if (s < n_sub) {
-            int pid = ent[s];
-            if (pid == kNone) pid = 0;
-            bad |= pid < 0 || pid >= a.c.n_pages;
-            pid = min(max(pid, 0), a.c.n_pages - 1);
-            const int row = (k0 + s * tp) & (a.c.page - 1);
-            const int plane = pid * a.c.heads + grp * kGroup;
-            const uint32_t off = (uint32_t)(s * tp * 128);
-            tma_load_3d(base + off * kGroup, &tmK, &bar->full[stg], 0, row, plane);
-            tma_load_3d(base + kPeOff + off, &tmPe, &bar->full[stg], 0, row, pid);
-            tma_load_3d(base + kVOff + off * kGroup, &tmV, &bar->full[stg], 0, row, plane);
-            bulk_load(bar->scales[stg][0][s], a.c.k_scales + plane, 16, &bar->full[stg]);
-            bulk_load(bar->scales[stg][1][s], a.c.v_scales + plane, 16, &bar->full[stg]);
-          }
-        }
-        ++issued;
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s) ent[s] = nxt[s];
+  const int n_sub = kTile / tp;  // pages in a tile
+  constexpr int kNone = INT_MIN;
+  // page number of part `sub` of the walk's tile (kNone: no visible key there)
+  auto entry = [&](int sub) {
+    const int j = w.s.key0(w.ti) + sub * tp;
+    return sub < n_sub && w.s.sees(j, tp) ? a.c.table[(size_t)w.b * a.c.max_pages + j / a.c.page] : kNone;
+  };
+  auto page_of = [&](int ent) { return ent == kNone ? 0 : min(max(ent, 0), a.c.n_pages - 1); };
+
+  if (warp >= 8 && warp < 11) {
+    // ---- TMA: key codes, value codes, rotary keys ----
+    if (R == 0) return;
+    const CUtensorMap* map = warp == 8 ? &tmK : warp == 9 ? &tmV : &tmPe;
+    const bool codes = warp < 10;
+    const uint32_t at = warp == 8 ? 0 : warp == 9 ? kVOff : kPeOff;
+    const uint32_t bytes = codes ? kCodeBytes : kTile * 128;
+    if (lane == 0) tma_prefetch_desc(map);
+    bool bad = false;
+    int ent = entry(lane);  // lane i: part i of the tile
+    int issued = 0;
+    for (int i = 0; i < R; ++i) {
+      const int k0 = w.s.key0(w.ti), grp = w.grp, e = ent;
+      bad |= w.s.bad || (e != kNone && (e < 0 || e >= a.c.n_pages));
+      const int pid = page_of(e);
+      if (i + 1 < R) {
+        w.next(a, groups);
+        ent = entry(lane);
       }
-      // no copy may still be in flight into shared memory
-      for (int i = max(0, issued - kStages); i < issued; ++i)
-        mbar_wait(&bar->full[i % kStages], (i / kStages) & 1, st, nullptr, 82);
-      if (bad) atomicOr(st.word, kStatusBadLength);
+      const int stg = i % kStages;
+      if (i >= kStages &&
+          !__all_sync(0xffffffffu, mbar_wait(&bar->empty[stg], (i / kStages - 1) & 1, st, abort_flag, 81)))
+        break;
+      if (lane == 0) mbar_arrive_expect_tx(&bar->full[stg], bytes);
+      uint8_t* dst = smem + stg * kStageBytes + at;
+      for (int sub = 0; sub < n_sub; ++sub) {
+        const int id = __shfl_sync(0xffffffffu, pid, sub);
+        const int row = (k0 + sub * tp) & (a.c.page - 1);
+        if (lane == 0) {
+          if (codes)
+            tma_load_3d(dst + sub * tp * 128 * kGroup, map, &bar->full[stg], 0, row, id * a.c.heads + grp * kGroup);
+          else
+            tma_load_3d(dst + sub * tp * 128, map, &bar->full[stg], 0, row, id);
+        }
+      }
+      ++issued;
+    }
+    // no copy may still be in flight into shared memory
+    for (int i = max(0, issued - kStages); i < issued; ++i)
+      mbar_wait(&bar->full[i % kStages], (i / kStages) & 1, st, nullptr, 82);
+    if (warp == 8 && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(st.word, kStatusBadLength);
+    return;
+  }
+  if (warp == 11) {
+    // ---- scales: lane = (part of the tile, key or value, head); entries two tiles ahead, scales one ----
+    if (R == 0) return;
+    const int sub = lane >> 3;
+    const float* src = (lane & 4) ? a.c.v_scales : a.c.k_scales;
+    auto scale_of = [&](int ent, int grp) {
+      return ent == kNone ? 1.f : src[(size_t)page_of(ent) * a.c.heads + grp * kGroup + (lane & 3)];
+    };
+    float val = scale_of(entry(sub), w.grp);  // of tile i
+    int ent = kNone, grp = 0;                 // of tile i + 1
+    if (R > 1) {
+      w.next(a, groups);
+      ent = entry(sub);
+      grp = w.grp;
+    }
+    for (int i = 0; i < R; ++i) {
+      const float cur = val;
+      if (i + 1 < R) val = scale_of(ent, grp);
+      if (i + 2 < R) {
+        w.next(a, groups);
+        ent = entry(sub);
+        grp = w.grp;
+      }
+      const int stg = i % kStages;
+      if (i >= kStages &&
+          !__all_sync(0xffffffffu, mbar_wait(&bar->empty[stg], (i / kStages - 1) & 1, st, abort_flag, 84)))
+        break;
+      (&bar->scales[stg][0][0][0])[(lane & 4 ? kTile / 16 * kGroup : 0) + sub * kGroup + (lane & 3)] = cur;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->full[stg]);
     }
     return;
   }
@@ -310,15 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, t = lane & 3;
   const float sl2 = a.scale * kLog2e;
   float* merge = reinterpret_cast<float*>(smem + kMergeOff) + hh * kMergeRows * 128;
-  // byte offsets of the 16-key blocks of this half inside K / V (and, with one head, inside the rotary keys)
-  uint32_t off16[2], pe16[2];
-  int sub16[2];
+  constexpr int kKeys = kTile / 2, kBlocks = kKeys / 16;
+  uint32_t off16[kBlocks];  // byte offset of this head's 16-key blocks in the tile's K and V
+  int sub16[kBlocks];       // and their page of the tile
 #pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    const int tok = half * 32 + ks * 16;
+  for (int ks = 0; ks < kBlocks; ++ks) {
+    const int tok = half * kKeys + ks * 16;
     sub16[ks] = tok / tp;
     off16[ks] = (uint32_t)((sub16[ks] * kGroup + hh) * tp + (tok & (tp - 1))) * 128;
-    pe16[ks] = (uint32_t)tok * 128;
   }
   uint32_t qa[8][2], qp[4][2];  // Q's row g (B operand)
   float acc[8][4];              // O^T: dimensions 16g + 2i (+ 1 in [2], [3]), queries 2t and 2t + 1
@@ -380,129 +408,127 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar->full[stg], (i / kStages) & 1, st, abort_flag, 83));
-    const int a0 = w.s.key0(w.ti) + half * 32;  // this warp's first key
-    if (ok && w.s.sees(a0, 32)) {
-      const uint8_t* kb = smem + stg * kStageBytes;
-      const uint8_t* vb = kb + kVOff;
-      const uint8_t* pb = kb + kPeOff;
-      // every query of the sequence sees all 32 keys
-      const bool full = a0 + 31 <= w.s.p &&
-                        (a.window == 0 || a0 > w.s.p + a.T - 1 - a.window || a0 + 31 < a.sinks);
-      float ksc[2], vsc[2];
+    {
+      const int a0 = w.s.key0(w.ti) + half * kKeys;  // this warp's first key
+      if (ok && w.s.sees(a0, kKeys)) {
+        const uint8_t* kb = smem + stg * kStageBytes;
+        const uint8_t* vb = kb + kVOff;
+        const uint8_t* pb = kb + kPeOff;
+        // every query of the sequence sees all of these keys
+        const bool full = a0 + kKeys - 1 <= w.s.p &&
+                          (a.window == 0 || a0 > w.s.p + a.T - 1 - a.window || a0 + kKeys - 1 < a.sinks);
+        float vsc[kBlocks];
+        // scores of 16 keys at a time: keys g ([0], [1]) and g + 8 ([2], [3]) of queries 2t and 2t + 1
+        float s[kBlocks][4];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        ksc[ks] = bar->scales[stg][0][sub16[ks]][hh];
-        vsc[ks] = bar->scales[stg][1][sub16[ks]][hh];
-      }
-      // scores of 16 keys at a time: keys g ([0], [1]) and g + 8 ([2], [3]) of queries 2t and 2t + 1
-      float s[2][4];
+        for (int ks = 0; ks < kBlocks; ++ks) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+          const float ksc = bar->scales[stg][0][sub16[ks]][hh];
+          vsc[ks] = bar->scales[stg][1][sub16[ks]][hh];
+          const uint8_t* kr = kb + off16[ks] + (uint32_t)g * 128;
+          const uint8_t* pr = pb + (uint32_t)(half * kKeys + ks * 16 + g) * 128;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint8_t* kr = kb + off16[ks] + (uint32_t)g * 128;
-        const uint8_t* pr = pb + pe16[ks] + (uint32_t)g * 128;
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const uint32_t chunk = (uint32_t)(((2 * t + h2) ^ g) << 4);
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + chunk);
+            const uint4 x8 = *reinterpret_cast<const uint4*>(kr + 1024 + chunk);
+            const uint32_t cw[4] = {x.x, x.y, x.z, x.w}, cw8[4] = {x8.x, x8.y, x8.z, x8.w};
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const uint32_t chunk = (uint32_t)(((2 * t + h2) ^ g) << 4);
-          const uint4 x = *reinterpret_cast<const uint4*>(kr + chunk);
-          const uint4 x8 = *reinterpret_cast<const uint4*>(kr + 1024 + chunk);
-          const uint32_t cw[4] = {x.x, x.y, x.z, x.w}, cw8[4] = {x8.x, x8.y, x8.z, x8.w};
+            for (int e = 0; e < 4; ++e) {
+              uint32_t b0, b1, b2, b3;
+              decode4(cw[e], b0, b2);
+              decode4(cw8[e], b1, b3);
+              mma_f16(c, b0, b1, b2, b3, qa[h2 * 4 + e][0], qa[h2 * 4 + e][1]);
+            }
+            const uint4 y = *reinterpret_cast<const uint4*>(pr + chunk);
+            const uint4 y8 = *reinterpret_cast<const uint4*>(pr + 1024 + chunk);
+            mma_bf16(d, y.x, y8.x, y.y, y8.y, qp[h2 * 2][0], qp[h2 * 2][1]);
+            mma_bf16(d, y.z, y8.z, y.w, y8.w, qp[h2 * 2 + 1][0], qp[h2 * 2 + 1][1]);
+          }
+          const float kq[2] = {ksc * qs[0], ksc * qs[1]};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[ks][e] = fmaf(c[e], kq[e & 1], d[e] * sl2);
+        }
+        if (!full) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t a0, a1, a2, a3;
-            decode4(cw[e], a0, a2);
-            decode4(cw8[e], a1, a3);
-            mma_f16(c, a0, a1, a2, a3, qa[h2 * 4 + e][0], qa[h2 * 4 + e][1]);
-          }
-          const uint4 y = *reinterpret_cast<const uint4*>(pr + chunk);
-          const uint4 y8 = *reinterpret_cast<const uint4*>(pr + 1024 + chunk);
-          mma_bf16(d, y.x, y8.x, y.y, y8.y, qp[h2 * 2][0], qp[h2 * 2][1]);
-          mma_bf16(d, y.z, y8.z, y.w, y8.w, qp[h2 * 2 + 1][0], qp[h2 * 2 + 1][1]);
-        }
+            const int qi = w.s.p + min(2 * t + (e & 1), a.T - 1);  // the query's position
+            const int lo = a.window ? qi - a.window : -1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[ks][e] = fmaf(c[e], ksc[ks] * qs[e & 1], d[e] * sl2);
-      }
-      if (!full) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int qi = w.s.p + min(2 * t + (e & 1), a.T - 1);  // the query's position
-          const int lo = a.window ? qi - a.window : -1;
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const int j = a0 + ks * 16 + (e >> 1) * 8 + g;
-            if (j > qi || (j <= lo && j >= a.sinks)) s[ks][e] = -INFINITY;
+            for (int ks = 0; ks < kBlocks; ++ks) {
+              const int j = a0 + ks * 16 + (e >> 1) * 8 + g;
+              if (j > qi || (j <= lo && j >= a.sinks)) s[ks][e] = -INFINITY;
+            }
           }
         }
+        // running maximum of log2(p * vscale) per query, over the 8 lanes of its column
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-          if (!w.s.sees(a0 + ks * 16, 16)) vsc[ks] = 1.f;  // nothing there: its scale may be anything
-      }
-      // running maximum of log2(p * vscale) per query, over the 8 lanes of its column
-      const float lv[2] = {__log2f(vsc[0]), __log2f(vsc[1])};
-      float mx[2];
-      bool need[2];
+        for (int ks = 0; ks < kBlocks; ++ks) {
+          const float lv = __log2f(vsc[ks]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(fmaxf(s[0][e], s[0][e + 2]) + lv[0], fmaxf(s[1][e], s[1][e + 2]) + lv[1]);
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
-        need[e] = mx[e] > m[e] + kRescaleThreshold;
-      }
-      if (__any_sync(0xffffffffu, need[0] | need[1])) {
-        float alpha[2];
+          for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[ks][e], s[ks][e + 2]) + lv);
+        }
+        bool need[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          alpha[e] = need[e] ? ex2_approx(m[e] - mx[e]) : 1.f;
-          if (need[e]) m[e] = mx[e];
-          l[e] *= alpha[e];
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+          need[e] = mx[e] > m[e] + kRescaleThreshold;
         }
+        if (__any_sync(0xffffffffu, need[0] | need[1])) {
+          float alpha[2];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+          for (int e = 0; e < 2; ++e) {
+            alpha[e] = need[e] ? ex2_approx(m[e] - mx[e]) : 1.f;
+            if (need[e]) m[e] = mx[e];
+            l[e] *= alpha[e];
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[c][e] *= alpha[e & 1];
-      }
-      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-      uint32_t pb16[2][2];  // weights of keys 2t, 2t+1 (and 8 further) of query g
+          for (int c = 0; c < 8; ++c)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2_approx(s[ks][e] - ref[e & 1]);
-          l[e & 1] += p[e];
+            for (int e = 0; e < 4; ++e) acc[c][e] *= alpha[e & 1];
         }
-        pb16[ks][0] = transpose8(pack_f16x2(p[0] * vsc[ks], p[1] * vsc[ks]));
-        pb16[ks][1] = transpose8(pack_f16x2(p[2] * vsc[ks], p[3] * vsc[ks]));
-      }
-      // V: keys 2t, 2t+1, 2t+8, 2t+9 of each 16, dimensions 16g .. 16g+15
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const uint8_t* vr = vb + off16[ks] + (uint32_t)(2 * t) * 128;
-        const uint32_t ce = (uint32_t)((g ^ (2 * t)) << 4), co = (uint32_t)((g ^ (2 * t + 1)) << 4);
-        uint4 x0 = *reinterpret_cast<const uint4*>(vr + ce);
-        uint4 x1 = *reinterpret_cast<const uint4*>(vr + 128 + co);
-        uint4 x2 = *reinterpret_cast<const uint4*>(vr + 1024 + ce);
-        uint4 x3 = *reinterpret_cast<const uint4*>(vr + 1152 + co);
-        if (!full) {
-          const int j = a0 + ks * 16 + 2 * t;
-          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-          if (!w.s.sees(j, 1)) x0 = z;
-          if (!w.s.sees(j + 1, 1)) x1 = z;
-          if (!w.s.sees(j + 8, 1)) x2 = z;
-          if (!w.s.sees(j + 9, 1)) x3 = z;
-        }
-        const uint32_t e0[4] = {x0.x, x0.y, x0.z, x0.w}, e1[4] = {x1.x, x1.y, x1.z, x1.w};
-        const uint32_t e2[4] = {x2.x, x2.y, x2.z, x2.w}, e3[4] = {x3.x, x3.y, x3.z, x3.w};
+        for (int ks = 0; ks < kBlocks; ++ks) {
+          float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t a0_, a1_, a2_, a3_;
-          decode4(__byte_perm(e0[e], e1[e], 0x5140), a0_, a1_);
-          decode4(__byte_perm(e2[e], e3[e], 0x5140), a2_, a3_);
-          mma_f16(acc[2 * e], a0_, a1_, a2_, a3_, pb16[ks][0], pb16[ks][1]);
-          decode4(__byte_perm(e0[e], e1[e], 0x7362), a0_, a1_);
-          decode4(__byte_perm(e2[e], e3[e], 0x7362), a2_, a3_);
-          mma_f16(acc[2 * e + 1], a0_, a1_, a2_, a3_, pb16[ks][0], pb16[ks][1]);
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2_approx(s[ks][e] - ref[e & 1]);
+            l[e & 1] += p[e];
+          }
+          // weights of keys 2t, 2t+1 (and 8 further) of query g
+          const uint32_t p0 = transpose8(pack_f16x2(p[0] * vsc[ks], p[1] * vsc[ks]));
+          const uint32_t p1 = transpose8(pack_f16x2(p[2] * vsc[ks], p[3] * vsc[ks]));
+          // V: keys 2t, 2t+1, 2t+8, 2t+9 of the 16, dimensions 16g .. 16g+15
+          const uint8_t* vr = vb + off16[ks] + (uint32_t)(2 * t) * 128;
+          const uint32_t ce = (uint32_t)((g ^ (2 * t)) << 4), co = (uint32_t)((g ^ (2 * t + 1)) << 4);
+          uint4 x0 = *reinterpret_cast<const uint4*>(vr + ce);
+          uint4 x1 = *reinterpret_cast<const uint4*>(vr + 128 + co);
+          uint4 x2 = *reinterpret_cast<const uint4*>(vr + 1024 + ce);
+          uint4 x3 = *reinterpret_cast<const uint4*>(vr + 1152 + co);
+          if (!full) {
+            const int j = a0 + ks * 16 + 2 * t;
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            if (!w.s.sees(j, 1)) x0 = z;
+            if (!w.s.sees(j + 1, 1)) x1 = z;
+            if (!w.s.sees(j + 8, 1)) x2 = z;
+            if (!w.s.sees(j + 9, 1)) x3 = z;
+          }
+          const uint32_t e0[4] = {x0.x, x0.y, x0.z, x0.w}, e1[4] = {x1.x, x1.y, x1.z, x1.w};
+          const uint32_t e2[4] = {x2.x, x2.y, x2.z, x2.w}, e3[4] = {x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0, b1, b2, b3;
+            decode4(__byte_perm(e0[e], e1[e], 0x5140), b0, b1);
+            decode4(__byte_perm(e2[e], e3[e], 0x5140), b2, b3);
+            mma_f16(acc[2 * e], b0, b1, b2, b3, p0, p1);
+            decode4(__byte_perm(e0[e], e1[e], 0x7362), b0, b1);
+            decode4(__byte_perm(e2[e], e3[e], 0x7362), b2, b3);
+            mma_f16(acc[2 * e + 1], b0, b1, b2, b3, p0, p1);
+          }
         }
       }
     }
@@ -593,7 +619,7 @@ __global__ void __launch_bounds__(32 * kGroup) paged_combine_kernel(const PagedA
   pdl_launch_dependents();
   pdl_wait();
   const int groups = a.c.heads / kGroup;
-  const int b = blockIdx.x / groups, grp = blockIdx.x - b * groups;
+  const int t = blockIdx.y, b = blockIdx.x / groups, grp = blockIdx.x - b * groups;
   const int hh = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e = a.first_tile[b], nt = a.first_tile[b + 1] - e;
   const long long total = (long long)a.first_tile[a.B] * groups;
@@ -601,49 +627,47 @@ __global__ void __launch_bounds__(32 * kGroup) paged_combine_kernel(const PagedA
   // the CTA that holds flattened tile x: the largest g with range_start(g) <= x
   const int g0 = (int)(((xa + 1) * C - 1) / total), g1 = (int)(((xb + 1) * C - 1) / total);
   if (g0 == g1) return;
-  for (int t = 0; t < a.T; ++t) {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = g0; k0 <= g1; k0 += 4) {
-      float2 ml[4];
-      float4 x[4];
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = g0; k0 <= g1; k0 += 4) {
+    float2 ml[4];
+    float4 x[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int gg = k0 + k;
-        ml[k] = make_float2(-INFINITY, 0.f);
-        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (gg > g1) continue;
-        const long long start = range_start(gg, total, C);
-        if (start == range_start(gg + 1, total, C)) continue;  // a CTA without tiles
-        const size_t at = ((size_t)(2 * gg + (start >= xa ? 0 : 1)) * a.T + t) * kGroup + hh;
-        ml[k] = a.part_ml[at];
-        x[k] = reinterpret_cast<const float4*>(a.part_o + at * 128)[lane];
-      }
-      const float mm = fmaxf(fmax3(m, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-      const float ref = mm == -INFINITY ? 0.f : mm;
-      const float f = exp2f(m - ref);
-      m = mm;
-      l *= f;
-      o.x *= f;
-      o.y *= f;
-      o.z *= f;
-      o.w *= f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float wk = exp2f(ml[k].x - ref);
-        l = fmaf(wk, ml[k].y, l);
-        o.x = fmaf(wk, x[k].x, o.x);
-        o.y = fmaf(wk, x[k].y, o.y);
-        o.z = fmaf(wk, x[k].z, o.z);
-        o.w = fmaf(wk, x[k].w, o.w);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int gg = k0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (gg > g1) continue;
+      const long long start = range_start(gg, total, C);
+      if (start == range_start(gg + 1, total, C)) continue;  // a CTA without tiles
+      const size_t at = ((size_t)(2 * gg + (start >= xa ? 0 : 1)) * a.T + t) * kGroup + hh;
+      ml[k] = a.part_ml[at];
+      x[k] = reinterpret_cast<const float4*>(a.part_o + at * 128)[lane];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2 r;
-    r.x = pack_bf16x2(o.x * inv, o.y * inv);
-    r.y = pack_bf16x2(o.z * inv, o.w * inv);
-    reinterpret_cast<uint2*>(a.o + ((long long)b * a.T + t) * a.o_row + (grp * kGroup + hh) * 128)[lane] = r;
+    const float mm = fmaxf(fmax3(m, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    const float f = exp2f(m - ref);
+    m = mm;
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float wk = exp2f(ml[k].x - ref);
+      l = fmaf(wk, ml[k].y, l);
+      o.x = fmaf(wk, x[k].x, o.x);
+      o.y = fmaf(wk, x[k].y, o.y);
+      o.z = fmaf(wk, x[k].z, o.z);
+      o.w = fmaf(wk, x[k].w, o.w);
+    }
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint2 r;
+  r.x = pack_bf16x2(o.x * inv, o.y * inv);
+  r.y = pack_bf16x2(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(a.o + ((long long)b * a.T + t) * a.o_row + (grp * kGroup + hh) * 128)[lane] = r;
 }
 
 }  // namespace
@@ -678,7 +702,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
   if (e != cudaSuccess) return e;
   ++*launches;
   if (nt > 1) {  // with one tile per sequence nothing is cut
-    e = launch_pdl(paged_combine_kernel, dim3((unsigned)(a.B * (a.c.heads / kGroup))), dim3(32 * kGroup), 0, stream, a,
+    e = launch_pdl(paged_combine_kernel, dim3((unsigned)(a.B * (a.c.heads / kGroup)), a.T), dim3(32 * kGroup), 0, stream, a,
                    C);
     ++*launches;
   }

@@ -132,11 +132,45 @@ def test_binding_refuses_wrong_tensors():
     t["table"] = torch.zeros((1, 2), dtype=torch.int32)
     with pytest.raises(ValueError):
         m.make_paged_cache(t)  # not CUDA tensors
+    m.make_params()
     x = torch.zeros((3, 4, 128), dtype=torch.bfloat16)
-    for f in (lambda: m._rows(x[:, 0], "q", 128), lambda: m._head_rows(x, "k", 4),
-              lambda: m._ints(torch.zeros(3, dtype=torch.int32), "P", 3)):
+    c = fake_cache(heads=4, page=16)
+    c._ref, c._device, c._batch = ctypes.byref(c), x.get_device(), 1
+    for f in (lambda: m.mla_paged_append(c, x, x, x[:, 0, :64], x, 3, x),
+              lambda: m.mla_paged_attention(c, x, x, 0, x, x),
+              lambda: m.mla_window_attention(x, 0, x, x, x, x, 4)):
         with pytest.raises(ValueError):
-            f()
+            f()  # CPU tensors
+
+
+@gpu
+def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
+    import torch
+    t = new_cache(4, 16, 4, [[0, 1], [2, 3]], 1, garbage=False)
+    for n, bad in (("k_codes", t["k_codes"].to(torch.int8)), ("k_pe", t["k_pe"][:, :8]), ("table", t["table"][0]),
+                   ("v_scales", t["v_scales"].cpu()), ("table", t["table"].long())):
+        with pytest.raises(ValueError):
+            m.make_paged_cache({**t, n: bad})
+    c = m.make_paged_cache(t)
+    k, pe, P, cu = normal(1, 6, 4, 128), normal(2, 6, 64), ints([0, 0]), ints([0, 2, 6])
+    ws = m.alloc_workspace(m.MODE_PAGED_ATTN, 2, 4)
+    good = dict(k=k, v=k, k_pe=pe, P=P, T=4, workspace=ws, cu=cu)
+    m.mla_paged_append(c, **good)
+    for over in (dict(k=k[:5]), dict(k=k.float()), dict(v=k[:, :3]), dict(v=k.cpu()), dict(k_pe=pe[:5]),
+                 dict(k_pe=pe[:, :32]), dict(P=P.long()), dict(P=P[:1]), dict(cu=cu[:2]), dict(P=P.cpu()),
+                 dict(workspace=ws.cpu()), dict(v=k.transpose(1, 2)), dict(P=ints([0, 0, 0, 0])[::2])):
+        with pytest.raises(ValueError):
+            m.mla_paged_append(c, **{**good, **over})
+    q, out = normal(3, 2, 4 * 192), normal(4, 2, 4 * 128)
+    good = dict(q=q, P=P, P_max=5, out=out, workspace=ws)
+    m.mla_paged_attention(c, **good)
+    for over in (dict(q=q[:1]), dict(q=q.half()), dict(q=q[:, :-8]), dict(out=out[:1]), dict(out=out.t()),
+                 dict(out=out.cpu()), dict(P=P.float()), dict(workspace=ws[::2])):
+        with pytest.raises(ValueError):
+            m.mla_paged_attention(c, **{**good, **over})
+    with pytest.raises(m.MlaError) as e:
+        m.mla_paged_attention(c, q, P, 32, out, ws)
+    assert e.value.status == -1
 
 
 # ---- references -------------------------------------------------------------------------------------------
