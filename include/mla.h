@@ -85,6 +85,8 @@ extern "C" {
 #define MLA_MODE_PAGED_APPEND 8
 #define MLA_MODE_PAGED_ATTN 9
 #define MLA_MODE_WINDOW_ATTN 10
+#define MLA_MODE_DECODE_PAGED 11
+#define MLA_MODE_PREFILL_PAGED 12
 
 /* Weights of one MLA sublayer: device pointers to bf16, nn.Linear [out, in].
  * Key-value compression page, MLA __init__ excerpt, for the projections;
@@ -159,6 +161,10 @@ typedef struct {
  *                                  t_or_p new tokens (`cap` ignored).
  *   mode = MLA_MODE_WINDOW_ATTN:   mla_window_attention, B sequences of
  *                                  t_or_p queries (`cap` ignored).
+ *   mode = MLA_MODE_DECODE_PAGED:  mla_decode_paged, B sequences, P_max = t_or_p.
+ *   mode = MLA_MODE_PREFILL_PAGED: mla_prefill_paged, B sequences of T = t_or_p
+ *                                  tokens, cap = P0 + T (or more): it holds
+ *                                  those positions' keys and values in bf16.
  * Returns 0 when the arguments are out of range. */
 size_t mla_workspace_size(int mode, int B, int t_or_p, int cap);
 
@@ -510,6 +516,35 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
 int mla_window_attention(const mla_params_t* params, const void* q, int B, int T, int P0, const void* k_cache,
                          const void* v_cache, int cap, int window, int sinks, void* out, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* One decode step of the sublayer against the paged 8-bit cache (64 heads):
+ * sequence b's new token at position P[b] is appended to its pages (as
+ * mla_paged_append) and attends to keys 0..P[b] (as mla_paged_attention with
+ * T = 1, its own key as the cache holds it), window and sinks as there.
+ *   x, out   [B, 7168]      (out may alias x exactly); idle rows (P[b] = -1)
+ *                           append nothing and get out = x
+ *   P        int [B] in DEVICE memory, -1 .. P_max; P_max + 1 <= max_pages * page
+ *   workspace mla_workspace_size(MLA_MODE_DECODE_PAGED, B, P_max, 0)
+ * The kv_b product is rounded to bf16 before it is quantized.
+ * Errors: those of mla_decode_varlen and of the cache (UNSUPPORTED unless
+ * heads = 64); device-side reports as mla_paged_attention. */
+int mla_decode_paged(const mla_weights_t* w, const mla_params_t* params, const void* x, int B, const int* P,
+                     int P_max, const mla_paged_cache_t* cache, int window, int sinks, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Prefill of T new tokens per sequence at positions P0..P0+T-1 into the paged
+ * 8-bit cache (64 heads): their keys and values are appended to the pages, and
+ * the tokens attend to the P0 cached positions (as the pages hold them) and to
+ * each other (as computed, not quantized), causally, with window > 0 only to
+ * the last `window` keys and the first `sinks`.  P0 = 0, window = 0 computes
+ * the out of mla_prefill.
+ *   x, out   [B, T, 7168]  (out may alias x exactly)
+ *   workspace mla_workspace_size(MLA_MODE_PREFILL_PAGED, B, T, P0 + T)
+ * Requires P0 >= 0 and P0 + T <= max_pages * page.
+ * Errors: INVALID_ARG, UNSUPPORTED (cache), ALIGNMENT, WORKSPACE, CUDA. */
+int mla_prefill_paged(const mla_weights_t* w, const mla_params_t* params, const void* x, int B, int T, int P0,
+                      const mla_paged_cache_t* cache, int window, int sinks, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream` and reads the device status word the last call on
  * this workspace left: MLA_OK, MLA_ERR_TIMEOUT if a bounded device wait

@@ -18,7 +18,7 @@ D, HEADS, Q_LORA, KV_LORA, QK_NOPE, QK_ROPE, QK, V = 7168, 64, 1536, 512, 128, 6
 FFN_INTER = 18432
 MODE_PREFILL, MODE_DECODE, MODE_DECODE_LATENT, MODE_FFN, MODE_CHUNK_LATENT, MODE_CHUNK_ABSORBED = 0, 1, 2, 3, 4, 5
 MODE_FOLD = 6
-MODE_PAGED_APPEND, MODE_PAGED_ATTN, MODE_WINDOW_ATTN = 8, 9, 10
+MODE_PAGED_APPEND, MODE_PAGED_ATTN, MODE_WINDOW_ATTN, MODE_DECODE_PAGED, MODE_PREFILL_PAGED = 8, 9, 10, 11, 12
 STAGES = ["input_norm", "a_proj", "latent", "q_b", "kv_b", "attn", "combine", "absorb_q", "absorb_o", "o_proj",
           "ffn_norm", "gate_up", "down"]
 MAX_STAGES = len(STAGES)
@@ -109,6 +109,10 @@ _SIGS = {
                                  _I, _I, _VP, _LL, _VP, _SZ, _VP]),
     "mla_window_attention": (_I, [ctypes.POINTER(MlaParams), _VP, _I, _I, _I, _VP, _VP, _I, _I, _I, _VP, _VP, _SZ,
                                   _VP]),
+    "mla_decode_paged": (_I, [ctypes.POINTER(MlaWeights), ctypes.POINTER(MlaParams), _VP, _I, _VP, _I,
+                              ctypes.POINTER(MlaPagedCache), _I, _I, _VP, _VP, _SZ, _VP]),
+    "mla_prefill_paged": (_I, [ctypes.POINTER(MlaWeights), ctypes.POINTER(MlaParams), _VP, _I, _I, _I,
+                               ctypes.POINTER(MlaPagedCache), _I, _I, _VP, _VP, _SZ, _VP]),
     "mla_device_status": (_I, [_VP, _VP]),
     "mla_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -491,6 +495,36 @@ def mla_window_attention(q, P0: int, k_cache, v_cache, out, workspace, window: i
                                     k_cache.data_ptr(), v_cache.data_ptr(), cap, window, sinks, out.data_ptr(),
                                     _bytes(workspace, dev), workspace.nbytes, s)
     _check(rc, "mla_window_attention")
+
+
+def mla_decode_paged(weights: MlaWeights, x, P, P_max: int, cache: MlaPagedCache, out, workspace, window: int = 0,
+                     sinks: int = 0, params: MlaParams | None = None, stream=None):
+    """x, out: bf16 [B, 7168]; P: int32 [B], positions of the new tokens (-1: idle), at most P_max; the cache has one
+    table row per sequence; workspace of MODE_DECODE_PAGED sized with P_max."""
+    dev, B = cache._device, cache._batch
+    s = _stream_on(dev, stream)
+    for t, what in ((x, "x"), (out, "out")):
+        if _rows(t, what, D, dev) != D or t.shape[0] != B:
+            raise ValueError(f"{what}: need a contiguous bf16 tensor [{B}, {D}], one row for each row of the table")
+    rc = lib().mla_decode_paged(ctypes.byref(weights), None if params is None else ctypes.byref(params), x.data_ptr(), B,
+                                _ints(P, "P", B, dev), P_max, cache._ref, window, sinks, out.data_ptr(),
+                                _bytes(workspace, dev), workspace.nbytes, s)
+    _check(rc, "mla_decode_paged")
+
+
+def mla_prefill_paged(weights: MlaWeights, x, P0: int, cache: MlaPagedCache, out, workspace, window: int = 0,
+                      sinks: int = 0, params: MlaParams | None = None, stream=None):
+    """x, out: bf16 [B, T, 7168], tokens at positions P0..P0+T-1, appended to the pages; the cache has one table row
+    per sequence; workspace of MODE_PREFILL_PAGED sized with T and cap = P0 + T."""
+    dev, B, T = cache._device, cache._batch, x.shape[1]
+    s = _stream_on(dev, stream)
+    for t, what in ((x, "x"), (out, "out")):
+        if t.dtype is not _torch.bfloat16 or t.get_device() != dev or not t.is_contiguous() or t.shape != (B, T, D):
+            raise ValueError(f"{what}: need a contiguous bf16 tensor [{B}, {T}, {D}], a sequence for each row of the table")
+    rc = lib().mla_prefill_paged(ctypes.byref(weights), None if params is None else ctypes.byref(params), x.data_ptr(),
+                                 B, T, P0, cache._ref, window, sinks, out.data_ptr(), _bytes(workspace, dev),
+                                 workspace.nbytes, s)
+    _check(rc, "mla_prefill_paged")
 
 
 def mla_device_status(workspace, stream=None) -> int:

@@ -20,7 +20,7 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // Workspace carve-up.  Offsets are computed identically by the size query
 // and by the entry points.
 struct Layout {
-  size_t status, cs, xn, ca, cq, ckv, kpe, q, o, kscr, vscr, qlat, olat, part_o, part_ml, split, h, plan, pos, total;
+  size_t status, cs, xn, ca, cq, ckv, kpe, q, o, kscr, vscr, qlat, olat, part_o, part_ml, split, h, plan, pos, kv, total;
   size_t split_bytes;  // split-K partial slots (decode modes), 0 = none
 };
 
@@ -40,7 +40,9 @@ void take_paged(Layout& L, int B, int T, Take& take) {
 
 Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
   Layout L{};
-  const bool pre = mode == MLA_MODE_PREFILL || mode == MLA_MODE_CHUNK_LATENT;
+  // K/V scratch for every position up to cap: rebuilt from the latent cache, or taken from the pages
+  const bool scratch_cap = mode == MLA_MODE_CHUNK_LATENT || mode == MLA_MODE_PREFILL_PAGED;
+  const bool pre = mode == MLA_MODE_PREFILL || scratch_cap;
   // absorbed chunk: one latent decode row per (sequence, new token)
   const bool absorbed = mode == MLA_MODE_CHUNK_ABSORBED;
   const size_t n = (pre || absorbed) ? (size_t)B * t_or_p : (size_t)B;
@@ -87,10 +89,13 @@ Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
   if (!pre) L.cs = L.o;
   if (pre) {
     // K/V scratch: the chunk's positions (prefill without caches), or every
-    // position up to cap rebuilt from the latent cache (latent chunk)
-    const size_t pos = mode == MLA_MODE_CHUNK_LATENT ? (size_t)cap : (size_t)t_or_p;
+    // position up to cap (latent and paged chunk)
+    const size_t pos = scratch_cap ? (size_t)cap : (size_t)t_or_p;
     L.kscr = take((size_t)B * MLA_HEADS * pos * MLA_QK * 2);
     L.vscr = take((size_t)B * MLA_HEADS * pos * MLA_V * 2);
+  } else if (mode == MLA_MODE_DECODE_PAGED) {
+    L.kv = take(n * MLA_HEADS * (MLA_QK_NOPE + MLA_V) * 2);  // the kv_b product
+    take_paged(L, B, 1, take);
   } else if (mode == MLA_MODE_DECODE) {
     const int s = decode_splits(B, t_or_p + 1, num_sms);
     L.part_o = take((size_t)B * MLA_HEADS * s * MLA_V * sizeof(float));
@@ -232,7 +237,7 @@ int front_end(const mla_weights_t* w, const Params& p, const void* x, int n_tok,
               int t_mod, int t_off, __nv_bfloat16* ckv_cache, __nv_bfloat16* kpe_cache, int cap, void* ws,
               const Layout& L, const DevStatusHost& st, int sms, cudaStream_t stream, Stager& sg,
               int* launches, bool with_q = true, const int* pos = nullptr, int pos_max = 0,
-              const mla_weights_fp8_t* f8 = nullptr, __nv_bfloat16* qpe_out = nullptr) {
+              const mla_weights_fp8_t* f8 = nullptr, __nv_bfloat16* qpe_out = nullptr, bool idle_ok = false) {
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   (void)n_pos;
   sg.start(MLA_STAGE_INPUT_NORM);
@@ -284,6 +289,7 @@ int front_end(const mla_weights_t* w, const Params& p, const void* x, int n_tok,
     la.pos = pos;
     la.pos_max = pos_max;
     la.status = st.word;
+    la.idle_ok = idle_ok;
     MLA_TRY(launch_latent_split(la, stream));
     *launches += 1;
   }
@@ -459,10 +465,10 @@ size_t mla_workspace_size(int mode, int B, int t_or_p, int cap) {
   if (B < 1) return 0;
   if (mode == MLA_MODE_PREFILL) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
-  } else if (mode == MLA_MODE_CHUNK_LATENT) {
+  } else if (mode == MLA_MODE_CHUNK_LATENT || mode == MLA_MODE_PREFILL_PAGED) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens || cap < t_or_p || (int64_t)B * cap > (int64_t)1 << 26)
       return 0;
-  } else if (mode == MLA_MODE_DECODE || mode == MLA_MODE_DECODE_LATENT) {
+  } else if (mode == MLA_MODE_DECODE || mode == MLA_MODE_DECODE_LATENT || mode == MLA_MODE_DECODE_PAGED) {
     if (t_or_p < 0 || B > kMaxTokens || t_or_p >= (1 << 24)) return 0;
   } else if (mode == MLA_MODE_FFN) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
@@ -1117,6 +1123,7 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
   a.pe = static_cast<const __nv_bfloat16*>(k_pe);
   a.pe_token = pe_token;
   a.P = P;
+  a.p_max = INT32_MAX;
   a.cu = cu;
   a.B = B;
   a.T = T;
@@ -1191,6 +1198,213 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
                     static_cast<const __nv_bfloat16*>(v_cache), static_cast<__nv_bfloat16*>(out), B, T, cap,
                     p.scale, P0, window, sinks};
   return launch_prefill_attention(a, st, sms, stream_) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---- the sublayer over the paged cache ---------------------------------------
+namespace {
+
+// kv_b of n rows into kv [n, 64 * 256], then the append of the rows' keys and
+// values (rotary keys from the A-projection's float32 output).
+int kv_b_append(const mla_weights_t* w, const Params& p, const mla_paged_cache_t* cache, int B, const int* P,
+                int P_max, void* ws, const Layout& L, const DevStatusHost& st, int sms, cudaStream_t stream, bool split_ok,
+                int* launches) {
+  GemmShape s{B, MLA_HEADS * 256, MLA_KV_LORA, 1, 0, 0, 0, 0, MLA_HEADS * 256};
+  GemmOperands op{at<__nv_bfloat16>(ws, L.ckv), MLA_KV_LORA, B,
+                  static_cast<const __nv_bfloat16*>(w->w_kv_b), MLA_KV_LORA, MLA_HEADS * 256,
+                  nullptr, 0, 0, false};
+  EpiArgs ea{};
+  ea.out = at<__nv_bfloat16>(ws, L.kv);
+  ea.ldo = MLA_HEADS * 256;
+  if (split_ok) set_split(ea, ws, L);
+  MLA_TRY(launch_gemm(s, op, Epi::kStoreBf16, ea, st, sms, stream));
+  *launches += 1;
+  PagedAppendArgs a{};
+  a.c = device_cache(cache);
+  a.k = at<__nv_bfloat16>(ws, L.kv);
+  a.v = a.k + MLA_QK_NOPE;
+  a.k_token = a.v_token = MLA_HEADS * 256;
+  a.k_head = a.v_head = 256;
+  a.pe_f32 = at<float>(ws, L.ca) + MLA_Q_LORA + MLA_KV_LORA;
+  a.pe_token = 2112;
+  a.P = P;
+  a.p_max = P_max;
+  a.B = a.N = B;
+  a.T = 1;
+  for (int i = 0; i < 32; ++i) a.inv_freq[i] = pow((double)p.base, -2.0 * i / 64.0);
+  a.status = st.word;
+  a.status_cleared = true;
+  MLA_TRY(launch_paged_append(a, stream));
+  *launches += 1;
+  return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_decode_paged(const mla_weights_t* w, const mla_params_t* params, const void* x, int B, const int* P,
+                     int P_max, const mla_paged_cache_t* cache, int window, int sinks, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const Params p = resolve(params);
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (cache->heads != MLA_HEADS) return MLA_ERR_UNSUPPORTED;
+  if (!P || B < 1 || B > kMaxTokens || P_max < 0 || P_max >= (1 << 24) || window < 0 || sinks < 0 ||
+      (int64_t)P_max + 1 > (int64_t)cache->max_pages * cache->page)
+    return MLA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(P) & 3) return MLA_ERR_ALIGNMENT;
+  rc = common_checks(w, p, x, out, (size_t)B, workspace, workspace_bytes,
+                     make_layout(MLA_MODE_DECODE_PAGED, B, P_max, kMaxSmsForSizing).total);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  const Layout L = make_layout(MLA_MODE_DECODE_PAGED, B, P_max, kMaxSmsForSizing);
+
+  cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  const DevStatusHost st{at<uint32_t>(workspace, L.status), kDefaultWaitLimitNs};
+  Stager sg{p.timing, stream_};
+  int launches = 0;
+  if (cudaMemsetAsync(st.word, 0, kStatusRegion, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+  SideStream* side = B <= kForkMaxRows ? side_stream(stream_) : nullptr;
+  rc = front_end(w, p, x, B, 1, P_max, 1, P_max, nullptr, nullptr, 0, workspace, L, st, sms, stream_, sg, &launches,
+                 side == nullptr, P, P_max, nullptr, nullptr, true);
+  if (rc) return rc;
+  // kv_b and the append beside q_b (as kv_b_beside: their split-K slots are q_b's)
+  cudaStream_t kvs = stream_;
+  if (side) {
+    MLA_TRY(cudaEventRecord(side->fork, stream_));
+    MLA_TRY(cudaStreamWaitEvent(side->s, side->fork, 0));
+    kvs = side->s;
+  }
+  Stager sk{p.timing, kvs};
+  sk.start(MLA_STAGE_KV_B);
+  rc = kv_b_append(w, p, cache, B, P, P_max, workspace, L, st, sms, kvs, side == nullptr, &launches);
+  if (rc) return rc;
+  sk.stop(MLA_STAGE_KV_B);
+  if (side) {
+    sg.start(MLA_STAGE_Q_B);
+    rc = q_b_stage(w, B, 1, P, nullptr, nullptr, workspace, L, st, sms, stream_, &launches);
+    if (rc) return rc;
+    sg.stop(MLA_STAGE_Q_B);
+    rc = join_side(side, stream_);
+    if (rc) return rc;
+  }
+
+  sg.start(MLA_STAGE_ATTN);
+  {
+    PagedAttnArgs a{};
+    a.c = device_cache(cache);
+    a.q = at<__nv_bfloat16>(workspace, L.q);
+    a.o = at<__nv_bfloat16>(workspace, L.o);
+    a.q_row = MLA_HEADS * MLA_QK;
+    a.o_row = MLA_HEADS * MLA_V;
+    a.P = P;
+    a.B = B;
+    a.T = 1;
+    a.P_max = P_max;
+    a.window = window;
+    a.sinks = window ? sinks : 0;
+    a.scale = p.scale;
+    a.status = st.word;
+    a.status_cleared = true;
+    a.part_o = at<float>(workspace, L.part_o);
+    a.part_ml = at<float2>(workspace, L.part_ml);
+    a.first_tile = at<int>(workspace, L.plan);
+    if (launch_paged_attention(a, st, sms, stream_, &launches) != cudaSuccess) return MLA_ERR_CUDA;
+  }
+  sg.stop(MLA_STAGE_ATTN);
+
+  sg.start(MLA_STAGE_O_PROJ);
+  rc = o_proj_stage(w, p, x, out, B, workspace, L, st, sms, stream_, &launches);
+  if (rc) return rc;
+  sg.stop(MLA_STAGE_O_PROJ);
+  if (p.timing) p.timing->n_launches = launches;
+  return MLA_OK;
+}
+
+int mla_prefill_paged(const mla_weights_t* w, const mla_params_t* params, const void* x, int B, int T, int P0,
+                      const mla_paged_cache_t* cache, int window, int sinks, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const Params p = resolve(params);
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (cache->heads != MLA_HEADS) return MLA_ERR_UNSUPPORTED;
+  if (B < 1 || T < 1 || P0 < 0 || (int64_t)B * T > kMaxTokens || window < 0 || sinks < 0 ||
+      (int64_t)P0 + T > (int64_t)cache->max_pages * cache->page ||
+      (int64_t)B * ((int64_t)P0 + T) > (int64_t)1 << 26)
+    return MLA_ERR_INVALID_ARG;
+  const size_t n_tok = (size_t)B * T;
+  const int cap = P0 + T;  // positions of the scratch K/V
+  rc = common_checks(w, p, x, out, n_tok, workspace, workspace_bytes,
+                     make_layout(MLA_MODE_PREFILL_PAGED, B, T, kMaxSmsForSizing, cap).total);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  const Layout L = make_layout(MLA_MODE_PREFILL_PAGED, B, T, kMaxSmsForSizing, cap);
+
+  cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  const DevStatusHost st{at<uint32_t>(workspace, L.status), kDefaultWaitLimitNs};
+  Stager sg{p.timing, stream_};
+  int launches = 0;
+  if (cudaMemsetAsync(st.word, 0, kStatusRegion, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+  rc = front_end(w, p, x, (int)n_tok, T, P0, T, P0, nullptr, nullptr, cap, workspace, L, st, sms, stream_, sg,
+                 &launches);
+  if (rc) return rc;
+
+  __nv_bfloat16* kc = at<__nv_bfloat16>(workspace, L.kscr);
+  __nv_bfloat16* vc = at<__nv_bfloat16>(workspace, L.vscr);
+  sg.start(MLA_STAGE_KV_B);
+  if (P0 > 0) {  // the cached positions that a query of the chunk sees
+    const int from = window ? (P0 - window + 1 > 0 ? P0 - window + 1 : 0) : 0;
+    PagedGatherArgs ga{device_cache(cache), kc, vc, B, P0, cap, from, sinks < from ? sinks : from, st.word};
+    MLA_TRY(launch_paged_gather(ga, stream_));
+    launches += 1;
+  }
+  rc = kv_b_stage(w, (int)n_tok, T, P0, kc, vc, cap, workspace, L, st, sms, stream_, &launches);
+  if (rc) return rc;
+  {
+    // the new rows of the scratch K/V into the pages
+    PagedAppendArgs a{};
+    a.c = device_cache(cache);
+    a.k = kc + (size_t)P0 * MLA_QK;
+    a.v = vc + (size_t)P0 * MLA_V;
+    a.k_seq = (long long)MLA_HEADS * cap * MLA_QK;
+    a.k_head = (long long)cap * MLA_QK;
+    a.k_token = MLA_QK;
+    a.v_seq = (long long)MLA_HEADS * cap * MLA_V;
+    a.v_head = (long long)cap * MLA_V;
+    a.v_token = MLA_V;
+    a.pe_f32 = at<float>(workspace, L.ca) + MLA_Q_LORA + MLA_KV_LORA;
+    a.pe_token = 2112;
+    a.p0 = a.p_max = P0;
+    a.B = B;
+    a.T = T;
+    a.N = (int)n_tok;
+    for (int i = 0; i < 32; ++i) a.inv_freq[i] = pow((double)p.base, -2.0 * i / 64.0);
+    a.status = st.word;
+    a.status_cleared = true;
+    MLA_TRY(launch_paged_append(a, stream_));
+    launches += 1;
+  }
+  sg.stop(MLA_STAGE_KV_B);
+
+  sg.start(MLA_STAGE_ATTN);
+  {
+    PrefillAttnArgs a{at<__nv_bfloat16>(workspace, L.q), kc, vc, at<__nv_bfloat16>(workspace, L.o), B, T, cap,
+                      p.scale, P0, window, window ? sinks : 0};
+    if (launch_prefill_attention(a, st, sms, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+    launches += 1;
+  }
+  sg.stop(MLA_STAGE_ATTN);
+
+  sg.start(MLA_STAGE_O_PROJ);
+  rc = o_proj_stage(w, p, x, out, (int)n_tok, workspace, L, st, sms, stream_, &launches);
+  if (rc) return rc;
+  sg.stop(MLA_STAGE_O_PROJ);
+  if (p.timing) p.timing->n_launches = launches;
+  return MLA_OK;
 }
 
 }  // extern "C"

@@ -224,6 +224,7 @@ struct LatentArgs {
   const int* pos;
   int pos_max;
   uint32_t* status;
+  bool idle_ok;            // pos[r] = -1 marks an idle row (taken as position 0, not reported)
 };
 cudaError_t launch_latent_split(const LatentArgs& a, cudaStream_t stream);
 
@@ -321,8 +322,8 @@ struct PagedAppendArgs {
   const __nv_bfloat16* pe;     // unrotated rotary keys, row n at n * pe_token ...
   const float* pe_f32;         // ... or in float32 (the A-projection's output); one of the two
   long long pe_token;
-  const int* P;                // per-sequence first position (-1: idle), or null: p0 for all
-  int p0;
+  const int* P;                // per-sequence first position (-1: idle, at most p_max), or null: p0 for all
+  int p0, p_max;
   const int* cu;               // row offsets [B + 1], or null: T rows each
   int B, T, N;
   double inv_freq[32];
@@ -330,6 +331,18 @@ struct PagedAppendArgs {
   bool status_cleared;         // the caller cleared the status region: OR into it
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+
+// Positions of the dense caches K [B, heads, cap, 192], V [B, heads, cap, 128]
+// filled with the paged ones' values (code * scale, exact in bf16): positions
+// j < P with j >= from or j < first, of every sequence.
+struct PagedGatherArgs {
+  PagedCache c;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int B, P, cap, from, first;
+  uint32_t* status;            // cleared by the caller
+};
+cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream);
 
 struct PagedAttnArgs {
   PagedCache c;

@@ -32,7 +32,7 @@ struct AppendSeq {
     row = a.cu ? a.cu[b] : b * a.T;
     n = a.cu ? a.cu[b + 1] - row : a.T;
     const long long cap = (long long)a.c.max_pages * a.c.page;
-    bad = p < -1 || n < 0 || n > a.T || row < 0 || (long long)row + n > a.N ||
+    bad = p < -1 || p > a.p_max || n < 0 || n > a.T || row < 0 || (long long)row + n > a.N ||
           (p >= 0 && (long long)p + n > cap);
     if (bad || p < 0) n = 0;
   }
@@ -177,7 +177,51 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
     if (wi + i * W < n) *reinterpret_cast<uint2*>(dst + (slot0 + wi + i * W) * 128) = code8(u[i], r);
 }
 
+// Grid: x = (sequence, page of 16 positions), y = head: a warp per 2
+// positions, 16 codes a lane and step.  The rotary key of a position is
+// copied into each head's row.
+__global__ void __launch_bounds__(256) paged_gather_kernel(const PagedGatherArgs a, int blocks) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x / blocks, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j0 = (blockIdx.x - b * blocks) * 16;
+  if (j0 + 16 <= a.from && j0 >= a.first) return;
+  const int id = a.c.table[(size_t)b * a.c.max_pages + j0 / a.c.page];
+  const bool bad = id < 0 || id >= a.c.n_pages;
+  if (bad && threadIdx.x == 0 && h == 0) atomicOr(a.status, kStatusBadLength);
+  const int pid = bad ? 0 : id;
+  const float ks = a.c.k_scales[(size_t)pid * a.c.heads + h], vs = a.c.v_scales[(size_t)pid * a.c.heads + h];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = j0 + warp * 2 + i;
+    if (j >= a.P || (j < a.from && j >= a.first)) continue;
+    const int slot = j & (a.c.page - 1);
+    const size_t row = (((size_t)pid * a.c.heads + h) * a.c.page + slot) * 128;
+    const size_t dst = ((size_t)b * a.c.heads + h) * a.cap + j;
+    // lanes 0..15: 8 key codes each, 16..31: 8 value codes; then the 64 rotary values
+    const bool is_v = lane >= 16;
+    const int col = (lane & 15) * 8;
+    const uint2 c = *reinterpret_cast<const uint2*>((is_v ? a.c.v_codes : a.c.k_codes) + row + col);
+    const float s = is_v ? vs : ks;
+    const float2 x0 = decode2(c.x), x1 = decode2(c.x >> 16), x2 = decode2(c.y), x3 = decode2(c.y >> 16);
+    const uint4 u = make_uint4(pack_bf16x2(x0.x * s, x0.y * s), pack_bf16x2(x1.x * s, x1.y * s),
+                               pack_bf16x2(x2.x * s, x2.y * s), pack_bf16x2(x3.x * s, x3.y * s));
+    *reinterpret_cast<uint4*>((is_v ? a.v + dst * 128 : a.k + dst * 192) + col) = u;
+    if (lane < 8)
+      *reinterpret_cast<uint4*>(a.k + dst * 192 + 128 + lane * 8) =
+          *reinterpret_cast<const uint4*>(a.c.k_pe + ((size_t)pid * a.c.page + slot) * 64 + lane * 8);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream) {
+  const int blocks = (a.P + 15) / 16;
+  const long long gx = (long long)a.B * blocks;
+  if (gx > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(paged_gather_kernel, dim3((unsigned)gx, a.c.heads), dim3(256), 0, stream, a, blocks);
+}
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   const int pages_per_seq = (a.T - 1 + a.c.page - 1) / a.c.page + 1;

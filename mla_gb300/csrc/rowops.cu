@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(128) latent_split_kernel(const LatentArgs a) {
   int pos_row = a.pos0 + tm, t = a.t_off + tm;
   if (a.pos) {
     const int p = a.pos[row];
-    if ((p < 0 || p > a.pos_max) && tid == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+    if ((p < 0 || p > a.pos_max) && !(a.idle_ok && p == -1) && tid == 0 && a.status) atomicOr(a.status, kStatusBadLength);
     pos_row = t = clamp_pos(p, a.pos_max);
   }
   // c^Q-hat = RMSNorm(c^Q); c^KV-hat = RMSNorm(c^KV) (also the latent cache row)
