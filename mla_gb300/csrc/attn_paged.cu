@@ -17,7 +17,9 @@
 // The lengths are device data: every CTA scans them for its own range.  A
 // piece of a sequence and head group that lies in one CTA is written
 // directly; pieces that a cut separates are left as partials (at most two per
-// CTA) and merged by paged_combine_kernel, in order.
+// CTA) and merged by paged_combine_kernel, in order.  (Merging in the last of
+// the CTAs to arrive instead, counted by atomics, took as long: 93 against 95
+// us at one sequence of 32,818 keys, 391 against 381 at 32 ragged ones.)
 //
 // CTA, 384 threads: warps 8..11 fill a 3-stage ring (72 KB a stage) with tiles,
 // page by page from the table, whose entries they read ahead: warp 8 the key
@@ -126,7 +128,7 @@ __device__ __forceinline__ long long range_start(int g, long long total, int C) 
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -134,7 +136,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -154,19 +156,44 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // 8 x 8 matrix of 16-bit elements, row r = lane / 4, columns 2 * (lane % 4) and + 1, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-__device__ __forceinline__ void pair_sync(int head) { 
-  switch (head) {  // barrier numbers known to the compiler
-    case 0: asm volatile("bar.sync 1, 64;" ::: "memory"); break;
-    case 1: asm volatile("bar.sync 2, 64;" ::: "memory"); break;
-    case 2: asm volatile("bar.sync 3, 64;" ::: "memory"); break;
-    default: asm volatile("bar.sync 4, 64;" ::: "memory"); break;
+// The merge of a pair's halves: the second warp fills the pair's buffer, the
+// first one reads it.  Named barriers 1 + head (filled) and 5 + head (read);
+// each has 32 arrivals that do not wait and 32 that do.
+template <int ID>
+__device__ __forceinline__ void bar_arrive64() { asm volatile("bar.arrive %0, 64;" ::"n"(ID) : "memory"); }
+template <int ID>
+__device__ __forceinline__ void bar_sync64() { asm volatile("bar.sync %0, 64;" ::"n"(ID) : "memory"); }
+__device__ __forceinline__ void pair_arrive(int k) {
+  switch (k) {
+    case 0: bar_arrive64<1>(); break;
+    case 1: bar_arrive64<2>(); break;
+    case 2: bar_arrive64<3>(); break;
+    case 3: bar_arrive64<4>(); break;
+    case 4: bar_arrive64<5>(); break;
+    case 5: bar_arrive64<6>(); break;
+    case 6: bar_arrive64<7>(); break;
+    default: bar_arrive64<8>(); break;
   }
- }
+}
+__device__ __forceinline__ void pair_wait(int k) {
+  switch (k) {
+    case 0: bar_sync64<1>(); break;
+    case 1: bar_sync64<2>(); break;
+    case 2: bar_sync64<3>(); break;
+    case 3: bar_sync64<4>(); break;
+    case 4: bar_sync64<5>(); break;
+    case 5: bar_sync64<6>(); break;
+    case 6: bar_sync64<7>(); break;
+    default: bar_sync64<8>(); break;
+  }
+}
 
+// ONE: one query per sequence (a fragment's second column is not there)
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmPe, const PagedAttnArgs a, uint64_t wait_limit_ns) {
@@ -250,10 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int n_sub = kTile / tp;  // pages in a tile
   constexpr int kNone = INT_MIN;
+  const int page_log = 31 - __clz(a.c.page);
   // page number of part `sub` of the walk's tile (kNone: no visible key there)
   auto entry = [&](int sub) {
     const int j = w.s.key0(w.ti) + sub * tp;
-    return sub < n_sub && w.s.sees(j, tp) ? a.c.table[(size_t)w.b * a.c.max_pages + j / a.c.page] : kNone;
+    return sub < n_sub && w.s.sees(j, tp) ? a.c.table[(size_t)w.b * a.c.max_pages + (j >> page_log)] : kNone;
   };
   auto page_of = [&](int ent) { return ent == kNone ? 0 : min(max(ent, 0), a.c.n_pages - 1); };
 
@@ -308,12 +336,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto scale_of = [&](int ent, int grp) {
       return ent == kNone ? 1.f : src[(size_t)page_of(ent) * a.c.heads + grp * kGroup + (lane & 3)];
     };
+    // The queries of the walk's next piece into L1 (its rows are not read for
+    // anything else, so the warps that need them would wait for HBM).
+    auto touch_q = [&]() {
+      if (w.ti != 0 || w.s.p < 0) return;
+      for (int k = lane; k < a.T * 12; k += 32) {  // 4 heads x 384 bytes a row
+        const int row = k / 12;
+        const char* at = reinterpret_cast<const char*>(a.q + ((long long)w.b * a.T + row) * a.q_row +
+                                                       w.grp * kGroup * 192) + (k - row * 12) * 128;
+        uint32_t sink;
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(sink) : "l"(at));
+      }
+    };
     float val = scale_of(entry(sub), w.grp);  // of tile i
     int ent = kNone, grp = 0;                 // of tile i + 1
     if (R > 1) {
       w.next(a, groups);
       ent = entry(sub);
       grp = w.grp;
+      touch_q();
     }
     for (int i = 0; i < R; ++i) {
       const float cur = val;
@@ -322,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.next(a, groups);
         ent = entry(sub);
         grp = w.grp;
+        touch_q();
       }
       const int stg = i % kStages;
       if (i >= kStages &&
@@ -339,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, t = lane & 3;
   const float sl2 = a.scale * kLog2e;
   float* merge = reinterpret_cast<float*>(smem + kMergeOff) + hh * kMergeRows * 128;
-  constexpr int kKeys = kTile / 2, kBlocks = kKeys / 16;
+  constexpr int kKeys = kTile / 2, kBlocks = kKeys / 16, NE = ONE ? 1 : 2;
   uint32_t off16[kBlocks];  // byte offset of this head's 16-key blocks in the tile's K and V
   int sub16[kBlocks];       // and their page of the tile
 #pragma unroll
@@ -352,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float acc[8][4];              // O^T: dimensions 16g + 2i (+ 1 in [2], [3]), queries 2t and 2t + 1
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, qs[2] = {0.f, 0.f};  // of queries 2t and 2t + 1
   bool ok = true;
+  if (R > 0 && half == 0) pair_arrive(4 + hh);  // the pair's buffer is free
 
   for (int i = 0; i < R; ++i) {
     const int stg = i % kStages;
@@ -422,36 +465,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s[kBlocks][4];
 #pragma unroll
         for (int ks = 0; ks < kBlocks; ++ks) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+          // a chain of dependent MMAs for each 64 dimensions of the nope part and each 32 of the rotary one
+          float c[2][4] = {}, d[2][4] = {};
           const float ksc = bar->scales[stg][0][sub16[ks]][hh];
           vsc[ks] = bar->scales[stg][1][sub16[ks]][hh];
           const uint8_t* kr = kb + off16[ks] + (uint32_t)g * 128;
           const uint8_t* pr = pb + (uint32_t)(half * kKeys + ks * 16 + g) * 128;
+          uint4 x[2], x8[2], y[2], y8[2];
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const uint32_t chunk = (uint32_t)(((2 * t + h2) ^ g) << 4);
-            const uint4 x = *reinterpret_cast<const uint4*>(kr + chunk);
-            const uint4 x8 = *reinterpret_cast<const uint4*>(kr + 1024 + chunk);
-            const uint32_t cw[4] = {x.x, x.y, x.z, x.w}, cw8[4] = {x8.x, x8.y, x8.z, x8.w};
+            x[h2] = *reinterpret_cast<const uint4*>(kr + chunk);
+            x8[h2] = *reinterpret_cast<const uint4*>(kr + 1024 + chunk);
+            y[h2] = *reinterpret_cast<const uint4*>(pr + chunk);
+            y8[h2] = *reinterpret_cast<const uint4*>(pr + 1024 + chunk);
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const uint32_t cw = e == 0 ? x[h2].x : e == 1 ? x[h2].y : e == 2 ? x[h2].z : x[h2].w;
+              const uint32_t cw8 = e == 0 ? x8[h2].x : e == 1 ? x8[h2].y : e == 2 ? x8[h2].z : x8[h2].w;
               uint32_t b0, b1, b2, b3;
-              decode4(cw[e], b0, b2);
-              decode4(cw8[e], b1, b3);
-              mma_f16(c, b0, b1, b2, b3, qa[h2 * 4 + e][0], qa[h2 * 4 + e][1]);
+              decode4(cw, b0, b2);
+              decode4(cw8, b1, b3);
+              mma_f16(c[h2], b0, b1, b2, b3, qa[h2 * 4 + e][0], qa[h2 * 4 + e][1]);
+              if (e == 0) mma_bf16(d[h2], y[h2].x, y8[h2].x, y[h2].y, y8[h2].y, qp[h2 * 2][0], qp[h2 * 2][1]);
+              if (e == 2) mma_bf16(d[h2], y[h2].z, y8[h2].z, y[h2].w, y8[h2].w, qp[h2 * 2 + 1][0], qp[h2 * 2 + 1][1]);
             }
-            const uint4 y = *reinterpret_cast<const uint4*>(pr + chunk);
-            const uint4 y8 = *reinterpret_cast<const uint4*>(pr + 1024 + chunk);
-            mma_bf16(d, y.x, y8.x, y.y, y8.y, qp[h2 * 2][0], qp[h2 * 2][1]);
-            mma_bf16(d, y.z, y8.z, y.w, y8.w, qp[h2 * 2 + 1][0], qp[h2 * 2 + 1][1]);
           }
           const float kq[2] = {ksc * qs[0], ksc * qs[1]};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[ks][e] = fmaf(c[e], kq[e & 1], d[e] * sl2);
+          for (int e = 0; e < 4; ++e)
+            if ((e & 1) < NE) s[ks][e] = fmaf(c[0][e] + c[1][e], kq[e & 1], (d[0][e] + d[1][e]) * sl2);
         }
         if (!full) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            if ((e & 1) >= NE) continue;
             const int qi = w.s.p + min(2 * t + (e & 1), a.T - 1);  // the query's position
             const int lo = a.window ? qi - a.window : -1;
 #pragma unroll
@@ -467,11 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ks = 0; ks < kBlocks; ++ks) {
           const float lv = __log2f(vsc[ks]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[ks][e], s[ks][e + 2]) + lv);
+          for (int e = 0; e < NE; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[ks][e], s[ks][e + 2]) + lv);
         }
-        bool need[2];
+        bool need[2] = {false, false};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < NE; ++e) {
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
@@ -481,6 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            if (e >= NE) {
+              alpha[e] = 1.f;
+              continue;
+            }
             alpha[e] = need[e] ? ex2_approx(m[e] - mx[e]) : 1.f;
             if (need[e]) m[e] = mx[e];
             l[e] *= alpha[e];
@@ -493,9 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
         for (int ks = 0; ks < kBlocks; ++ks) {
-          float p[4];
+          float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            if ((e & 1) >= NE) continue;
             p[e] = ex2_approx(s[ks][e] - ref[e & 1]);
             l[e & 1] += p[e];
           }
@@ -538,13 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (seg_last) {
       // the pair's two halves become one, then the rows are written
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < NE; ++e)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
       for (int r0 = 0; r0 < a.T; r0 += kMergeRows) {
         if (half == 1) {
+          pair_wait(4 + hh);  // the partner has read what was there
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < NE; ++e) {
             const int row = 2 * t + e;
             if (row >= r0 && row < r0 + kMergeRows && row < a.T) {
               float* at = merge + (row - r0) * 128 + 16 * g;
@@ -555,11 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (g == 0) bar->ml[hh][row - r0] = make_float2(m[e], l[e]);
             }
           }
-        }
-        pair_sync(hh);
-        if (half == 0) {
+          pair_arrive(hh);
+        } else {
+          pair_wait(hh);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < NE; ++e) {
             const int row = 2 * t + e;
             if (row >= r0 && row < r0 + kMergeRows && row < a.T) {
               const float2 ml = bar->ml[hh][row - r0];
@@ -578,14 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          pair_arrive(4 + hh);
         }
-        pair_sync(hh);
       }
       if (ok && half == 0) {
         const bool whole = w.ti == w.s.nt - 1 && i >= w.ti;  // its first tile is in this CTA too
         const int slot = 2 * cta + (w.b == first_b && w.grp == first_g ? 0 : 1);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < NE; ++e) {
           const int row = 2 * t + e;
           if (row >= a.T) continue;
           if (whole) {
@@ -610,41 +667,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (i + 1 < R) w.next(a, groups);
   }
+  if (R > 0 && half == 1) pair_wait(4 + hh);  // the last arrival
 }
 
 // Merges the pieces of the (sequence, head group) pairs that a cut between
 // CTAs separates; the others were written by paged_attn_kernel.  One warp per
-// head, 4 dimensions a lane; pieces four at a time, in order.
+// head and query, 4 dimensions a lane; pieces eight at a time, in order.
 __global__ void __launch_bounds__(32 * kGroup) paged_combine_kernel(const PagedAttnArgs a, int C) {
   pdl_launch_dependents();
   pdl_wait();
   const int groups = a.c.heads / kGroup;
   const int t = blockIdx.y, b = blockIdx.x / groups, grp = blockIdx.x - b * groups;
   const int hh = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e = a.first_tile[b], nt = a.first_tile[b + 1] - e;
-  const long long total = (long long)a.first_tile[a.B] * groups;
-  const long long xa = (long long)e * groups + (long long)grp * nt, xb = xa + nt - 1;
+  const int e = a.first_tile[b], nt = a.first_tile[b + 1] - e, all = a.first_tile[a.B];
+  const long long total = (long long)all * groups;
+  const long long xa = (long long)e * groups + (long long)grp * nt;
   // the CTA that holds flattened tile x: the largest g with range_start(g) <= x
-  const int g0 = (int)(((xa + 1) * C - 1) / total), g1 = (int)(((xb + 1) * C - 1) / total);
+  auto cta_of = [&](long long x) {
+    const long long n = (x + 1) * C - 1;
+    return total * C <= INT_MAX ? (int)((uint32_t)n / (uint32_t)total) : (int)(n / total);
+  };
+  const int g0 = cta_of(xa), g1 = cta_of(xa + nt - 1);
   if (g0 == g1) return;
+  // a CTA's first piece is in its slot 0; only g0 can have begun before this pair
+  const int slot0 = 2 * g0 + (range_start(g0, total, C) >= xa ? 0 : 1);
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = g0; k0 <= g1; k0 += 4) {
-    float2 ml[4];
-    float4 x[4];
+  for (int k0 = g0; k0 <= g1; k0 += 8) {
+    float2 ml[8];
+    float4 x[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const int gg = k0 + k;
       ml[k] = make_float2(-INFINITY, 0.f);
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (gg > g1) continue;
-      const long long start = range_start(gg, total, C);
-      if (start == range_start(gg + 1, total, C)) continue;  // a CTA without tiles
-      const size_t at = ((size_t)(2 * gg + (start >= xa ? 0 : 1)) * a.T + t) * kGroup + hh;
+      // with fewer tiles than CTAs some of them have none
+      if (total < C && range_start(gg, total, C) == range_start(gg + 1, total, C)) continue;
+      const size_t at = ((size_t)(gg == g0 ? slot0 : 2 * gg) * a.T + t) * kGroup + hh;
       ml[k] = a.part_ml[at];
       x[k] = reinterpret_cast<const float4*>(a.part_o + at * 128)[lane];
     }
-    const float mm = fmaxf(fmax3(m, ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    float mm = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mm = fmaxf(mm, ml[k].x);
     const float ref = mm == -INFINITY ? 0.f : mm;
     const float f = exp2f(m - ref);
     m = mm;
@@ -654,7 +720,7 @@ __global__ void __launch_bounds__(32 * kGroup) paged_combine_kernel(const PagedA
     o.z *= f;
     o.w *= f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const float wk = exp2f(ml[k].x - ref);
       l = fmaf(wk, ml[k].y, l);
       o.x = fmaf(wk, x[k].x, o.x);
@@ -681,15 +747,17 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
       !make_tmap_rows128_3d(&tv, a.c.v_codes, a.c.page, planes, tp, kGroup) ||
       !make_tmap_rows128_3d(&tpe, a.c.k_pe, a.c.page, a.c.n_pages, tp, 1))
     return cudaErrorInvalidValue;
+  const bool one = a.T == 1;
+  auto kern = one ? paged_attn_kernel<true> : paged_attn_kernel<false>;
   constexpr int kMaxDevices = 64;
-  static bool attr_set[kMaxDevices] = {};
+  static bool attr_set[kMaxDevices][2] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= kMaxDevices || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (dev >= kMaxDevices || !attr_set[dev][one]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices) attr_set[dev] = true;
+    if (dev < kMaxDevices) attr_set[dev][one] = true;
   }
   // the most tiles that a sequence can have
   long long nt = ((long long)a.P_max + a.T + kTile - 1) / kTile;
@@ -698,7 +766,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
   const long long most = nt * a.B * (a.c.heads / kGroup);
   if (nt * a.B > INT32_MAX || (long long)a.B * (a.c.heads / kGroup) > INT32_MAX) return cudaErrorInvalidValue;
   const int C = (int)std::min<long long>(most, std::min(num_sms, kPagedMaxCtas));
-  e = launch_pdl(paged_attn_kernel, dim3(C), dim3(kThreads), kSmemBytes, stream, tk, tv, tpe, a, st.wait_limit_ns);
+  e = launch_pdl(kern, dim3(C), dim3(kThreads), kSmemBytes, stream, tk, tv, tpe, a, st.wait_limit_ns);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (nt > 1) {  // with one tile per sequence nothing is cut
