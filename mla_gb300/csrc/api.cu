@@ -30,7 +30,7 @@ struct Layout {
 constexpr size_t kStatusRegion = 256 + kMaxSplitCounters * sizeof(int);
 
 // Regions of the paged attention: partials of up to two pieces per CTA, and
-// the number of key tiles before each sequence.
+// the units of work before each sequence.
 template <class Take>
 void take_paged(Layout& L, int B, int T, Take& take) {
   L.part_o = take((size_t)2 * kPagedMaxCtas * T * 4 * MLA_V * sizeof(float));
@@ -59,7 +59,7 @@ Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
     L.total = off;
     return L;
   }
-  if (mode == MLA_MODE_PAGED_ATTN) {  // two partial pieces per CTA, and the sequences' first tiles
+  if (mode == MLA_MODE_PAGED_ATTN) {  // two partial pieces per CTA, and the sequences' first units
     take_paged(L, B, t_or_p, take);
     L.total = off;
     return L;
@@ -1170,7 +1170,7 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
   a.status = at<uint32_t>(workspace, L.status);
   a.part_o = at<float>(workspace, L.part_o);
   a.part_ml = at<float2>(workspace, L.part_ml);
-  a.first_tile = at<int>(workspace, L.plan);
+  a.first_unit = at<int>(workspace, L.plan);
   const DevStatusHost st{a.status, kDefaultWaitLimitNs};
   int launches = 0;
   return launch_paged_attention(a, st, sms, static_cast<cudaStream_t>(stream), &launches) == cudaSuccess
@@ -1311,7 +1311,7 @@ int mla_decode_paged(const mla_weights_t* w, const mla_params_t* params, const v
     a.status_cleared = true;
     a.part_o = at<float>(workspace, L.part_o);
     a.part_ml = at<float2>(workspace, L.part_ml);
-    a.first_tile = at<int>(workspace, L.plan);
+    a.first_unit = at<int>(workspace, L.plan);
     if (launch_paged_attention(a, st, sms, stream_, &launches) != cudaSuccess) return MLA_ERR_CUDA;
   }
   sg.stop(MLA_STAGE_ATTN);

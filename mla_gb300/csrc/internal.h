@@ -356,7 +356,7 @@ struct PagedAttnArgs {
   bool status_cleared;
   float* part_o;               // [2 * kPagedMaxCtas][T][4 heads][128]
   float2* part_ml;             // [2 * kPagedMaxCtas][T][4 heads]
-  int* first_tile;             // [B + 1]: key tiles of the sequences before b
+  int* first_unit;             // [B + 1]: units of work of the sequences before b, one head group
 };
 constexpr int kPagedMaxCtas = 256;
 constexpr int kPagedMaxT = 8;
