@@ -1087,6 +1087,18 @@ int check_workspace(const void* ws, size_t bytes, int mode, int B, int T) {
   return bytes < make_layout(mode, B, T, kMaxSmsForSizing).total ? MLA_ERR_WORKSPACE : MLA_OK;
 }
 
+// theta_i = base^(-2i/64).  The powers of the last base are kept: 32 calls of
+// pow are a third of the host time of an append.
+void rope_frequencies(float base, double (&f)[32]) {
+  thread_local float last = 0.f;
+  thread_local double theta[32];
+  if (base != last) {
+    for (int i = 0; i < 32; ++i) theta[i] = pow((double)base, -2.0 * i / 64.0);
+    last = base;
+  }
+  memcpy(f, theta, sizeof(theta));
+}
+
 // strides in elements whose rows stay 16-byte aligned
 bool good_stride(long long s) { return s >= 0 && s % 8 == 0; }
 
@@ -1128,7 +1140,7 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
   a.B = B;
   a.T = T;
   a.N = N;
-  for (int i = 0; i < 32; ++i) a.inv_freq[i] = pow((double)p.base, -2.0 * i / 64.0);
+  rope_frequencies(p.base, a.inv_freq);
   a.status = static_cast<uint32_t*>(workspace);
   return launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -1232,7 +1244,7 @@ int kv_b_append(const mla_weights_t* w, const Params& p, const mla_paged_cache_t
   a.p_max = P_max;
   a.B = a.N = B;
   a.T = 1;
-  for (int i = 0; i < 32; ++i) a.inv_freq[i] = pow((double)p.base, -2.0 * i / 64.0);
+  rope_frequencies(p.base, a.inv_freq);
   a.status = st.word;
   a.status_cleared = true;
   MLA_TRY(launch_paged_append(a, stream));
@@ -1382,7 +1394,7 @@ int mla_prefill_paged(const mla_weights_t* w, const mla_params_t* params, const 
     a.B = B;
     a.T = T;
     a.N = (int)n_tok;
-    for (int i = 0; i < 32; ++i) a.inv_freq[i] = pow((double)p.base, -2.0 * i / 64.0);
+    rope_frequencies(p.base, a.inv_freq);
     a.status = st.word;
     a.status_cleared = true;
     MLA_TRY(launch_paged_append(a, stream_));

@@ -63,22 +63,21 @@ __device__ __forceinline__ uint2 code8(const uint4& u, float r) {
                     code2(c.x * r, c.y * r) | code2(d.x * r, d.y * r) << 16);
 }
 
-// largest |x| of 8 bf16, NaN ignored
-__device__ __forceinline__ float top8(const uint4& u) {
-  const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
-  return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
-               fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+// larger |x| of two pairs of bf16, element by element, NaN ignored
+__device__ __forceinline__ __nv_bfloat162 top_pair(__nv_bfloat162 m, uint32_t u) {
+  const uint32_t a = u & 0x7fff7fffu;
+  return __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&a));
 }
 
 // Grid: x = (sequence, touched page), y = head group, and one row of CTAs more
-// for the rotary keys.  W warps share a head, each holding up to 8 tokens.
-__global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs a, int pages_per_seq, int W) {
+// for the rotary keys.  2^w_log warps share a head, each holding up to 8 tokens.
+__global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs a, int pages_per_seq, int w_log) {
   __shared__ float red[16][2];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int warps = blockDim.x >> 5;
-  const int page = a.c.page;
+  const int page = a.c.page, page_log = 31 - __clz(page);
 
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     // every sequence and page number of the call, for the status word
@@ -87,7 +86,7 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
       const int b = i / pages_per_seq, j = i - b * pages_per_seq;
       const AppendSeq s(a, b);
       bad |= s.bad;
-      const int pi = s.p / page + j;
+      const int pi = (s.p >> page_log) + j;
       if (s.n > 0 && pi * page < s.p + s.n) {
         const int pid = a.c.table[(size_t)b * a.c.max_pages + pi];
         bad |= pid < 0 || pid >= a.c.n_pages;
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
 
   const int b = blockIdx.x / pages_per_seq, j = blockIdx.x - b * pages_per_seq;
   const AppendSeq s(a, b);
-  const int pi = s.p / page + j;
+  const int pi = (s.p >> page_log) + j;
   const int base = pi * page;                        // the page's first position
   if (s.n == 0 || base >= s.p + s.n) return;
   const int pid = a.c.table[(size_t)b * a.c.max_pages + pi];
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
     return;
   }
 
-  const int h = blockIdx.y * (warps / W) + warp / W, wi = warp % W;
+  const int h = blockIdx.y * (warps >> w_log) + (warp >> w_log), W = 1 << w_log, wi = warp & (W - 1);
   const bool live = h < a.c.heads;
   const bool is_v = lane >= 16;
   const int col = (lane & 15) * 8;
@@ -137,18 +136,28 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
   float top = 0.f;
   float* scale_at = nullptr;
   int k_old = kFloorExp;
+  const int mine = (n - wi + W - 1) >> w_log;  // this warp's tokens: wi, wi + W, ..
   if (live) {
     const __nv_bfloat16* src = is_v ? a.v + b * a.v_seq + (a.v_seq ? t0 : s.row + t0) * a.v_token + h * a.v_head
                                     : a.k + b * a.k_seq + (a.k_seq ? t0 : s.row + t0) * a.k_token + h * a.k_head;
-    const long long step = is_v ? a.v_token : a.k_token;
+    const long long token = is_v ? a.v_token : a.k_token;
+    const __nv_bfloat16* at = src + wi * token + col;
+    const long long step = token << w_log;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      u[i] = wi + i * W < n ? *reinterpret_cast<const uint4*>(src + (long long)(wi + i * W) * step + col)
-                            : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kRows; ++i) {
+      u[i] = i < mine ? *reinterpret_cast<const uint4*>(at) : make_uint4(0u, 0u, 0u, 0u);
+      at += step;
+    }
     scale_at = (is_v ? a.c.v_scales : a.c.k_scales) + (size_t)pid * a.c.heads + h;
     if (slot0 > 0) k_old = min(kCeilExp, max(kFloorExp, (int)((__float_as_uint(*scale_at) >> 23) & 255) - 127));
+    __nv_bfloat162 m0 = __floats2bfloat162_rn(0.f, 0.f), m1 = m0;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) top = fmaxf(top, top8(u[i]));
+    for (int i = 0; i < kRows; ++i) {
+      m0 = top_pair(top_pair(m0, u[i].x), u[i].y);
+      m1 = top_pair(top_pair(m1, u[i].z), u[i].w);
+    }
+    const float2 f = __bfloat1622float2(__hmax2(m0, m1));
+    top = fmaxf(f.x, f.y);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
@@ -159,7 +168,7 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
   }
   if (!live) return;
   const int k_new = max(k_old, block_exp(top));
-  uint8_t* dst = (is_v ? a.c.v_codes : a.c.k_codes) + ((size_t)pid * a.c.heads + h) * page * 128 + col;
+  uint8_t* dst = (is_v ? a.c.v_codes : a.c.k_codes) + (((size_t)pid * a.c.heads + h) << page_log) * 128 + col;
   if (slot0 > 0 && k_new > k_old) {
     const float r = exp2_int(max(k_old - k_new, -126));
     for (int i = wi; i < slot0; i += W) {
@@ -172,9 +181,12 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
   }
   if (wi == 0 && (lane & 15) == 0) *scale_at = exp2_int(k_new);
   const float r = exp2_int(-k_new);
+  uint8_t* at = dst + (slot0 + wi) * 128;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (wi + i * W < n) *reinterpret_cast<uint2*>(dst + (slot0 + wi + i * W) * 128) = code8(u[i], r);
+  for (int i = 0; i < kRows; ++i) {
+    if (i < mine) *reinterpret_cast<uint2*>(at) = code8(u[i], r);
+    at += 128 << w_log;
+  }
 }
 
 // Grid: x = (sequence, page of 16 positions), y = head: a warp per 2
@@ -226,12 +238,13 @@ cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream) {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   const int pages_per_seq = (a.T - 1 + a.c.page - 1) / a.c.page + 1;
   // 8 tokens a warp: one warp per head for a few new tokens, else page / 8
-  const int W = a.T <= 8 ? 1 : a.c.page / 8;
-  const int warps = W > 8 ? W : 8;
+  const int w_log = a.T <= 8 ? 0 : a.c.page == 16 ? 1 : a.c.page == 32 ? 2 : a.c.page == 64 ? 3 : 4;
+  const int W = 1 << w_log, warps = W > 8 ? W : 8;
   const long long gx = (long long)a.B * pages_per_seq;
   if (gx > INT32_MAX) return cudaErrorInvalidValue;
   const int gy = (a.c.heads * W + warps - 1) / warps + 1;
-  return launch_pdl(paged_append_kernel, dim3((unsigned)gx, gy), dim3(warps * 32), 0, stream, a, pages_per_seq, W);
+  return launch_pdl(paged_append_kernel, dim3((unsigned)gx, gy), dim3(warps * 32), 0, stream, a,
+                    pages_per_seq, w_log);
 }
 
 }  // namespace mla
