@@ -142,6 +142,19 @@ __device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, const DevSt
   return true;
 }
 
+// What computed l and p stays ahead of what follows (the wait for the previous
+// P.V): the compiler is free to move arithmetic behind a wait's assembly, and
+// did (B=8 T=4096 causal 1977 -> 1874 us with this and P packed ahead of the
+// wait; B=2 T=4096 under a window of 1,024 with 128 sinks 358 -> 348 us).
+__device__ __forceinline__ void keep_order(float& l, uint32_t (&p)[64]) {
+  asm volatile("" : "+f"(l) : : "memory");
+#pragma unroll
+  for (int c = 0; c < 64; c += 16)
+    asm volatile("" : "+r"(p[c]), "+r"(p[c + 1]), "+r"(p[c + 2]), "+r"(p[c + 3]), "+r"(p[c + 4]), "+r"(p[c + 5]),
+                 "+r"(p[c + 6]), "+r"(p[c + 7]), "+r"(p[c + 8]), "+r"(p[c + 9]), "+r"(p[c + 10]), "+r"(p[c + 11]),
+                 "+r"(p[c + 12]), "+r"(p[c + 13]), "+r"(p[c + 14]), "+r"(p[c + 15]));
+}
+
 template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -492,6 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
         l = l * alpha + sum;
         m = m_new;
+        // P_j as bf16 pairs (low half = even key), all of it ahead of the wait
+        uint32_t pk[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+        keep_order(l, pk);
         // the previous P.V (this CTA's tile gt-1) has read P and added into O:
         // P may be rewritten and O rescaled
         if (gt > 0) {
@@ -512,11 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        // P_j (bf16 pairs, low half = even key) into the P buffer
+        // P_j into the P buffer
         {
-          uint32_t pk[64];
-#pragma unroll
-          for (int c = 0; c < 64; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
           const uint32_t tp = tmem + lane_addr + kTmP;
 #pragma unroll
           for (int c = 0; c < 64; c += 16) tmem_st16(tp + c, &pk[c]);
