@@ -130,7 +130,10 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ long long range_start(int g, long long total, int C) { return (long long)g * total / C; }
+__device__ __forceinline__ long long range_start(int g, long long total, int C) {
+  const long long x = g * total;
+  return x <= UINT32_MAX ? (long long)((uint32_t)x / (uint32_t)C) : x / C;  // (a 64-bit division is a few hundred cycles)
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -221,6 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar->first_b = bar->first_g = bar->first_t = 0;
     bar->tiles[0] = bar->tiles[1] = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmPe);
   }
   pdl_launch_dependents();
   pdl_wait();
@@ -309,7 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool codes = warp < 10;
     const uint32_t at = warp == 8 ? 0 : warp == 9 ? kVOff : kPeOff;
     const uint32_t bytes = codes ? kCodeBytes : kTile * 128;
-    if (lane == 0) tma_prefetch_desc(map);
     bool bad = false;
     int ent = entry(lane);  // lane i: part i of the tile
     int issued = 0;
@@ -781,7 +786,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
   if (a.window)
     nt = std::min(nt, ((long long)a.window + a.T - 2) / kTile + 2 + ((long long)a.sinks + kTile - 1) / kTile);
   const long long most = nt * a.B * (a.c.heads / kGroup);
-  if (nt * a.B > INT32_MAX || (long long)a.B * (a.c.heads / kGroup) > INT32_MAX) return cudaErrorInvalidValue;
+  if ((nt + kPieceCost) * a.B > INT32_MAX || (long long)a.B * (a.c.heads / kGroup) > INT32_MAX) return cudaErrorInvalidValue;
   const int C = (int)std::min<long long>(most, std::min(num_sms, kPagedMaxCtas));
   e = launch_pdl(kern, dim3(C), dim3(kThreads), kSmemBytes, stream, tk, tv, tpe, a, st.wait_limit_ns);
   if (e != cudaSuccess) return e;

@@ -591,6 +591,45 @@ def test_append_then_attention_graph_and_streams(gpu_available):
         assert all(torch.equal(a, b) for a, b in zip(res[k], outs))
 
 
+@gpu
+def test_pages_past_32_bit_offsets(gpu_available):
+    """A cache of more than 2^32 bytes of codes: its last pages against the same tokens in the first ones."""
+    import torch
+    heads, page, P, T = 64, 128, [299, 130], 1
+    n_pages = 4400  # 1 MiB of key codes each
+    ids = [[n_pages - 1, n_pages - 7, n_pages - 3], [n_pages - 4, n_pages - 2, -1]]
+    tables = [ids, [[0, 3, 2], [4, 1, -1]]]
+    t = new_cache(n_pages, page, heads, tables[0], 1, garbage=False)
+    outs, pages = [], []
+    lengths = [p + T for p in P]
+    kv, pe, q = normal(1, sum(lengths), heads, 256), normal(2, sum(lengths), 64), normal(3, 2, heads * 192)
+    for table in tables:
+        t["table"] = ints(table)
+        cache = m.make_paged_cache(t)
+        ws = m.alloc_workspace(m.MODE_PAGED_APPEND, 2, max(lengths))
+        m.mla_paged_append(cache, kv[..., :128], kv[..., 128:], pe, ints([0, 0]), max(lengths), ws,
+                           cu=ints([0, lengths[0], sum(lengths)]))
+        assert m.mla_device_status(ws) == 0
+        outs.append(_again(cache, q, P, 0, 0, T))
+        at = t["table"].flatten().clamp_min(0).long()[:5]
+        pages.append([t[n][at].clone() for n in m.PAGED_TENSORS])
+    assert torch.equal(outs[0], outs[1]) and bool(outs[0].abs().sum() > 0)
+    assert all(torch.equal(a, b) for a, b in zip(*pages))
+    assert bool((t["k_codes"][100:n_pages - 100] == 0).all()), "pages that belong to nobody"
+
+
+@gpu
+def test_many_short_sequences_and_few_tiles(gpu_available):
+    """More sequences than threads of a block, one tile each; and fewer tiles than SMs, some of them cut."""
+    import torch
+    for P, heads, window in (([i % 7 - 1 for i in range(900)], 4, 0), ([70, -1, 3, 200], 4, 0), ([63] * 3, 8, 9)):
+        t, cache = filled(P, 1, 16, heads, 5)
+        q = normal(7, len(P), heads * 192)
+        out = _again(cache, q, P, window, 0, 1)
+        ref, vmax = ref_attend(t, q, P, 1, window, 0)
+        check_out(out, ref, vmax, f"{len(P)} sequences")
+
+
 # ---- window attention over the dense caches ----------------------------------------------------------------
 @gpu
 @pytest.mark.parametrize("B,T,P0,window,sinks", [

@@ -240,6 +240,35 @@ def test_decode_paged_parity(W, P, page, window, sinks):
 
 
 @gpu
+@pytest.mark.parametrize("B", [65, 130, 300])
+def test_decode_paged_larger_batches(W, B):
+    """More rows than one tile of the small products: each row as in a batch of its own sequences alone."""
+    import torch
+    page = 16
+    P = [(7 * i) % 33 - 1 for i in range(B)]
+    past = synth.tensor_cuda(11, "cache_x", (B, 33, 7168), synth.X_DIST)
+    x = synth.tensor_cuda(12, "new_x", (B, 7168), synth.X_DIST)
+    t, cache = pages(B, 34, page, 4)
+    run_prefill(W, t, cache, past, 0)
+    first = {n: t[n].clone() for n in m.PAGED_TENSORS}
+    out, delta = torch.empty_like(x), torch.empty((B, 7168), dtype=torch.float32, device="cuda")
+    ws = m.alloc_workspace(m.MODE_DECODE_PAGED, B, 32)
+    pos = torch.tensor(P, dtype=torch.int32, device="cuda")
+    m.mla_decode_paged(W[0], x, pos, 32, cache, out, ws, params=m.make_params(delta_out=delta))
+    assert m.mla_device_status(ws) == 0
+    for n in m.PAGED_TENSORS:
+        t[n].copy_(first[n])
+    for lo in range(0, B, 50):
+        n = min(50, B - lo)
+        part = m.make_paged_cache({**{k: t[k] for k in m.PAGED_TENSORS}, "table": t["table"][lo:lo + n].contiguous()})
+        o2, d2 = torch.empty_like(x[:n]), torch.empty((n, 7168), dtype=torch.float32, device="cuda")
+        m.mla_decode_paged(W[0], x[lo:lo + n].contiguous(), pos[lo:lo + n].contiguous(), 32, part, o2,
+                           m.alloc_workspace(m.MODE_DECODE_PAGED, n, 32), params=m.make_params(delta_out=d2))
+        # other tile shapes and K splits: float32 sums in another order, bf16 roundings that may fall the other way
+        parity(cuda_to_f64(delta[lo:lo + n]), cuda_to_f64(d2), f"rows from {lo}")
+
+
+@gpu
 def test_decode_paged_steps_equal_their_parts_and_capture(W):
     """Steps of mla_decode_paged, eager and replayed from one captured graph, give the same pages and outputs; a bad
     position is reported and changes nothing."""
