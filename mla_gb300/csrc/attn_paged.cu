@@ -162,6 +162,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ void lds128(uint4& v, uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+}
 // 8 x 8 matrix of 16-bit elements, row r = lane / 4, columns 2 * (lane % 4) and + 1, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -521,6 +524,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e)
             if ((e & 1) < NE) s[ks][e] = fmaf(c[0][e] + c[1][e], kq[e & 1], (d[0][e] + d[1][e]) * sl2);
         }
+        // V: keys 2t, 2t+1, 2t+8, 2t+9 of each 16, dimensions 16g .. 16g+15, loaded
+        // ahead of the softmax (its shuffles would hold the loads back: 190 -> 184
+        // us at 64 sequences under a window of 1,024)
+        uint4 xv[kBlocks][4];
+        {
+          const uint32_t ce = (uint32_t)((g ^ (2 * t)) << 4), co = (uint32_t)((g ^ (2 * t + 1)) << 4);
+#pragma unroll
+          for (int ks = 0; ks < kBlocks; ++ks) {
+            const uint32_t vr = smem_u32(vb) + off16[ks] + (uint32_t)(2 * t) * 128;
+            lds128(xv[ks][0], vr + ce);
+            lds128(xv[ks][1], vr + 128 + co);
+            lds128(xv[ks][2], vr + 1024 + ce);
+            lds128(xv[ks][3], vr + 1152 + co);
+            if (!full) {
+              const int j = a0 + ks * 16 + 2 * t;
+              const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+              if (!w.s.sees(j, 1)) xv[ks][0] = z;
+              if (!w.s.sees(j + 1, 1)) xv[ks][1] = z;
+              if (!w.s.sees(j + 8, 1)) xv[ks][2] = z;
+              if (!w.s.sees(j + 9, 1)) xv[ks][3] = z;
+            }
+          }
+        }
         if (!full) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -580,21 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // weights of keys 2t, 2t+1 (and 8 further) of query g
           const uint32_t p0 = transpose8(pack_f16x2(p[0] * vsc[ks], p[1] * vsc[ks]));
           const uint32_t p1 = transpose8(pack_f16x2(p[2] * vsc[ks], p[3] * vsc[ks]));
-          // V: keys 2t, 2t+1, 2t+8, 2t+9 of the 16, dimensions 16g .. 16g+15
-          const uint8_t* vr = vb + off16[ks] + (uint32_t)(2 * t) * 128;
-          const uint32_t ce = (uint32_t)((g ^ (2 * t)) << 4), co = (uint32_t)((g ^ (2 * t + 1)) << 4);
-          uint4 x0 = *reinterpret_cast<const uint4*>(vr + ce);
-          uint4 x1 = *reinterpret_cast<const uint4*>(vr + 128 + co);
-          uint4 x2 = *reinterpret_cast<const uint4*>(vr + 1024 + ce);
-          uint4 x3 = *reinterpret_cast<const uint4*>(vr + 1152 + co);
-          if (!full) {
-            const int j = a0 + ks * 16 + 2 * t;
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            if (!w.s.sees(j, 1)) x0 = z;
-            if (!w.s.sees(j + 1, 1)) x1 = z;
-            if (!w.s.sees(j + 8, 1)) x2 = z;
-            if (!w.s.sees(j + 9, 1)) x3 = z;
-          }
+          const uint4 x0 = xv[ks][0], x1 = xv[ks][1], x2 = xv[ks][2], x3 = xv[ks][3];
           const uint32_t e0[4] = {x0.x, x0.y, x0.z, x0.w}, e1[4] = {x1.x, x1.y, x1.z, x1.w};
           const uint32_t e2[4] = {x2.x, x2.y, x2.z, x2.w}, e3[4] = {x3.x, x3.y, x3.z, x3.w};
 #pragma unroll
