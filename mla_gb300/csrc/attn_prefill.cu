@@ -45,8 +45,12 @@
 //            running max with lazy rescaling (O is rescaled in TMEM only when
 //            the max grows by more than 2^8, so P stays <= 256), P_j as bf16
 //            into the P buffer (once the previous P.V has read it), and at
-//            the end O / l to global memory (after the next item's Q has
-//            been copied, so its first scores overlap).
+//            the end O / l (after the next item's Q has been copied, so its
+//            first scores overlap) through the staging tile that the copy has
+//            emptied and a TMA store.  (Each thread storing its own row, 16
+//            bytes at a time, took 3,300 cycles an item, now 1,350: B=2 T=4096
+//            under a window of 1,024 with 128 sinks 348 -> 337 us, causal B=8
+//            T=4096 1874 -> 1829 us.)
 // Layout: Q [B*T, 64*192], K/V caches [B, 64, cap, 192|128] (TMA 3D views
 // whose position extent is T, so keys >= T read as zeros), O [B*T, 64*128].
 #include "common.cuh"
@@ -142,6 +146,28 @@ __device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, const DevSt
   return true;
 }
 
+// s[c] = -inf for the key columns c of the row above hi, or below lo.  The
+// bounds of a warp's rows are `lane` apart: a block of 32 columns that all of
+// them see is decided once (hi_w, lo_w: the first row's bounds).
+__device__ __forceinline__ void mask_above(uint32_t (&s)[128], int hi, int hi_w) {
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    if (c0 + 31 <= hi_w) continue;
+#pragma unroll
+    for (int c = c0; c < c0 + 32; ++c)
+      if (c > hi) s[c] = __float_as_uint(-INFINITY);
+  }
+}
+__device__ __forceinline__ void mask_below(uint32_t (&s)[128], int lo, int lo_w) {
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    if (c0 >= lo_w + 31) continue;
+#pragma unroll
+    for (int c = c0; c < c0 + 32; ++c)
+      if (c < lo) s[c] = __float_as_uint(-INFINITY);
+  }
+}
+
 // What computed l and p stays ahead of what follows (the wait for the previous
 // P.V): the compiler is free to move arithmetic behind a wait's assembly, and
 // did (B=8 T=4096 causal 1977 -> 1874 us with this and P packed ahead of the
@@ -159,7 +185,7 @@ template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVsink,
-                    __nv_bfloat16* __restrict__ o, int T, int n_qt, int n_items, float sl2, int past, int head_group,
+                    const __grid_constant__ CUtensorMap tmO, int T, int n_qt, int n_items, float sl2, int past, int head_group,
                     int window, int sinks, int* __restrict__ work, const DevStatus st) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
     mbar_init(&bar->q_tmem, 128);
-    mbar_init(&bar->qn_empty, 128);
+    mbar_init(&bar->qn_empty, 4);
     mbar_init(&bar->qpe_empty[0], 1);
     mbar_init(&bar->qpe_empty[1], 1);
     mbar_init(&bar->p_full, 128);
@@ -402,30 +428,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar->q_tmem);
-        mbar_arrive(&bar->qn_empty);
       }
       if (prev_last >= 0) {
-        // epilogue of the previous item: O / l once its last P.V is done
+        // epilogue of the previous item: O / l once its last P.V is done, through
+        // this row of the staging atoms, whose Q this thread has copied, and a TMA
+        // store (rows from T on are clipped)
         ok = __all_sync(0xffffffffu, mbar_wait(&bar->pv_done, prev_last & 1, st, abort_flag, 52));
         if (!ok) break;
         tc_fence_after();
         const float inv = 1.f / prev_l;
         const uint32_t ta = tmem + lane_addr + kTmO;
-        __nv_bfloat16* dst = o + ((size_t)prev_b * T + prev_qpos) * 8192 + prev_h * 128;
+        uint8_t* orow = smem + kQOff + row * 128;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
           tmem_ld32(ta + c, r);
           tmem_wait_ld();
-          if (prev_qpos < T) {
-            uint4* d4 = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              d4[q] = make_uint4(pack_bf16x2(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
-                                 pack_bf16x2(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
-                                 pack_bf16x2(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
-                                 pack_bf16x2(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(orow + (c >> 6) * kAtom + ((((c & 32) >> 3) + q) ^ (row & 7)) * 16) = make_uint4(
+                pack_bf16x2(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
+                pack_bf16x2(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
+                pack_bf16x2(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
+                pack_bf16x2(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const uint8_t* rows = smem + kQOff + quarter * 32 * 128;
+          const int first = prev_qpos - lane;  // this warp's first query
+          if (first < T) {
+            tma_store_3d(&tmO, rows, prev_h * 128, first, prev_b);
+            tma_store_3d(&tmO, rows + kAtom, prev_h * 128 + 64, first, prev_b);
           }
+          bulk_commit();
         }
         prev_last = -1;
       }
@@ -457,24 +493,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         // max of the raw scores (the scale is positive), causal mask (key k
         // visible to query position past + qpos iff k <= past + qpos) on the
         // tiles that reach beyond the tile's first query
-        if (k0 + 127 > past + t.q0) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (k0 + c > past + qpos) s[c] = __float_as_uint(-INFINITY);
-        }
         if constexpr (WIN) {
+          const int hi = past + qpos - k0, hi_w = past + t.q0 + quarter * 32 - k0;  // last visible column
           if (j < t.n_sink) {  // sinks before the window: every query sees them
             if (k0 + 127 >= t.n_first) {
 #pragma unroll
               for (int c = 0; c < 128; ++c)
                 if (k0 + c >= t.n_first) s[c] = __float_as_uint(-INFINITY);
             }
-          } else if (past + t.q0 + 127 - k0 >= window) {  // keys that the tile's later queries have passed
-            const int lo = past + qpos - window;  // the last key behind this query's window
+          } else {
+            // keys behind the later queries' windows, unless they are sinks, and keys ahead
+            if (past + t.q0 + 127 - k0 >= window) {
+              if (k0 >= sinks) {
+                mask_below(s, hi - window + 1, hi_w - window + 1);
+              } else {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (k0 + c <= lo && k0 + c >= sinks) s[c] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < 128; ++c)
+                  if (c <= hi - window && k0 + c >= sinks) s[c] = __float_as_uint(-INFINITY);
+              }
+            }
+            if (k0 + 127 > past + t.q0) mask_above(s, hi, hi_w);
           }
+        } else if (k0 + 127 > past + t.q0) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (k0 + c > past + qpos) s[c] = __float_as_uint(-INFINITY);
         }
         // eight independent partial maxima / sums keep the reductions off a
         // single serial dependency chain; three-input maxima and two-lane
@@ -539,6 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&bar->p_full);
+        if (j == 0 && lane == 0) {  // the staging atoms may take the next Q
+          bulk_wait_read<0>();
+          mbar_arrive(&bar->qn_empty);
+        }
       }
       prev_qpos = qpos;
       prev_h = t.h;
@@ -546,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prev_l = l;
       prev_last = gt - 1;
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -566,7 +614,10 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
       !make_tmap_bf16_3d(&tv, a.v, 128, n_keys, (uint64_t)a.B * 64, 256, (uint64_t)a.cap * 256, 64, 128))
     return cudaErrorInvalidValue;
   const bool win = a.window > 0;
-  CUtensorMap tvs = tv;
+  const int window = (uint64_t)a.window < n_keys ? a.window : (int)n_keys;  // (positions minus it stay in range)
+  CUtensorMap tvs = tv, to;
+  if (!make_tmap_store_bf16_3d(&to, a.o, 8192, a.T, a.B, 8192ull * 2, (uint64_t)a.T * 8192 * 2))
+    return cudaErrorInvalidValue;
   if (win && a.sinks > 0 &&
       !make_tmap_bf16_3d(&tvs, a.v, 128, (uint64_t)a.sinks < n_keys ? (uint64_t)a.sinks : n_keys, (uint64_t)a.B * 64,
                          256, (uint64_t)a.cap * 256, 64, 128))
@@ -595,7 +646,7 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   long long heavy = past_t + n_qt + 1;
   long long per_head = (long long)n_qt * past_t + (long long)n_qt * (n_qt + 1) / 2 + n_qt;
   if (win) {  // no tile takes more than the window's and the sinks' key tiles
-    heavy = std::min(heavy, ((long long)a.window + 254) / 128 + ((long long)a.sinks + 127) / 128 + 1);
+    heavy = std::min(heavy, ((long long)window + 254) / 128 + ((long long)a.sinks + 127) / 128 + 1);
     per_head = std::min(per_head, n_qt * heavy);
   }
   const long long need = (3 * (long long)grid * heavy + 2 * per_head - 1) / (2 * per_head);
@@ -606,8 +657,8 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   // the work counter: an int of the status region (cleared before every call)
   int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
   DevStatus dst{st.word, st.wait_limit_ns};
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, tvs, a.o, a.T, n_qt, n_items,
-                    a.scale * 1.4426950408889634f, a.past, G, a.window, a.sinks, work, dst);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, tvs, to, a.T, n_qt, n_items,
+                    a.scale * 1.4426950408889634f, a.past, G, window, a.sinks, work, dst);
 }
 
 }  // namespace mla
