@@ -424,7 +424,8 @@ int mla_ffn(const mla_ffn_weights_t* w, const mla_params_t* params, const void* 
  *   page   16, 32, 64 or 128
  *   heads  a multiple of 4, at most 128 (the sublayer's entry points need 64;
  *          a shard of the heads has fewer)
- * n_pages * heads and n_pages * page must fit a 31-bit int. */
+ * n_pages * heads and n_pages * page must fit a 31-bit int, and a sequence has
+ * at most 2^30 positions (max_pages * page). */
 typedef struct {
   void* k_codes;
   void* v_codes;
@@ -488,7 +489,9 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
  *            calls that may run concurrently, or by two captured graphs that may
  * Keys that no query of the sequence sees are not used, whatever their pages
  * hold (table entries of pages without a visible key are not looked at, so
- * pages that a window has passed can be given back).  Scores, softmax
+ * pages that a window has passed can be given back).  A key that one query
+ * sees has weight zero for the others; a NaN among its values reaches those
+ * of its call too.  Scores, softmax
  * statistics and sums are float32; the weights (probability times value
  * scale) are rounded to float16 for the product with V.
  * A P[b] outside [-1, P_max] is taken as idle, a page number outside
@@ -512,6 +515,9 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
  *   params   softmax_scale (the others are not used)
  *   workspace mla_workspace_size(MLA_MODE_WINDOW_ATTN, B, T, 0)
  * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
+ * A NaN among a key's values may also reach queries that do not see the key
+ * but share a tile with one that does (weight zero times NaN): those less than
+ * 256 positions short of it, or past the end of its window.
  * Errors: INVALID_ARG (null pointer, sizes), ALIGNMENT, WORKSPACE, CUDA. */
 int mla_window_attention(const mla_params_t* params, const void* q, int B, int T, int P0, const void* k_cache,
                          const void* v_cache, int cap, int window, int sinks, void* out, void* workspace,

@@ -1070,7 +1070,9 @@ int check_cache(const mla_paged_cache_t* c) {
   if (reinterpret_cast<uintptr_t>(c->table) & 3) return MLA_ERR_ALIGNMENT;
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MLA_ERR_UNSUPPORTED;
   if (c->heads < 4 || c->heads > 128 || c->heads % 4) return MLA_ERR_UNSUPPORTED;
-  if ((int64_t)c->n_pages * c->heads > INT32_MAX || (int64_t)c->n_pages * c->page > INT32_MAX)
+  // (a position, a call's tokens and a page behind them stay in 31 bits)
+  if ((int64_t)c->n_pages * c->heads > INT32_MAX || (int64_t)c->n_pages * c->page > INT32_MAX ||
+      (int64_t)c->max_pages * c->page > (int64_t)1 << 30)
     return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }

@@ -75,6 +75,14 @@ def test_bad_caches_are_refused(over, rc):
     assert attend(fake_cache(**over)) == rc
 
 
+def test_tables_that_pass_31_bits_are_refused():
+    """positions (and a call's tokens behind the last one) are counted in 32-bit ints"""
+    for over in (dict(max_pages=(1 << 24) + 1), dict(max_pages=(1 << 27) + 1, page=16), dict(max_pages=(1 << 31) - 1)):
+        assert append(fake_cache(**over)) == -4
+        assert attend(fake_cache(**over)) == -4
+    assert append(fake_cache(max_pages=1 << 24), wsb=16) == -3  # 2^30 positions: the next check speaks
+
+
 def test_append_refusals():
     L = m.lib()
     for kw in (dict(k=None), dict(v=None), dict(pe=None), dict(P=None), dict(B=0), dict(T=0), dict(N=0), dict(N=5),
