@@ -16,10 +16,18 @@
 // scores overlap the previous item's last P.V and epilogue.
 // Sliding window (WIN): an item's key tiles are those of the sinks and of the
 // keys its queries see, so the work of a query tile is bounded by the window.
+// With so few key tiles an item, its Q copy, its masked tiles and its epilogue
+// are half of its time, so two threads share a row there (warps 8..11 take the
+// second half of every tile's, of Q's and of O's columns; the two maxima, and
+// at the end the two sums, go through shared memory): B=2 T=4096, a window of
+// 1,024 with 128 sinks 325 -> 308 us, of 256 with 4 sinks 218 -> 185 us, of 64
+// 157 -> 135 us.  The causal kernel keeps one thread a row: the tensor pipe and
+// the exponentials (the same number a scheduler either way) set its pace, and
+// its sums keep their order.
 // Chunked prefill: the queries sit at positions past..past+T-1 and attend to
 // keys 0..past+T-1 of the cache (the chunk's own keys written after the
 // cached ones), the causal mask offset by past.
-// Warp roles (256 threads):
+// Warp roles (256 threads; 384 under a window):
 //   warp 0   work scheduler (atomic counter -> a 4-slot ring of item
 //            indices in shared memory that every role reads), then TMA: the
 //            item's Q tile, then its K tiles into a 2-slot ring
@@ -62,7 +70,6 @@ namespace mla {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kAtom = 128 * 128;            // 128 rows x 64 bf16
 constexpr uint32_t kQOff = 0;                    // Q dims 0-127: 2 atoms (staging)
 constexpr uint32_t kQpeOff = 2 * kAtom;          // Q dims 128-191: 2 slots x 1 atom
@@ -72,12 +79,19 @@ constexpr uint32_t kBarOff = 14 * kAtom;
 // tensor memory columns: S_0, S_1 (fp32), O (fp32), P (bf16 pairs, 128 keys),
 // Q dims 0-127 (bf16 pairs)
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = 384, kTmQ = 448;
-constexpr uint32_t kSmemBytes = kBarOff + 512 + 1024;
-static_assert(kSmemBytes <= 232448, "prefill attention shared memory");
+constexpr uint32_t kXchOff = kBarOff + 512;      // WIN: a row's two partial maxima (or sums), 2 x 2 x 128 fp32
+// WIN: two threads a row, each with half of a key tile's (and of O's) columns
+template <bool WIN>
+struct Shape {
+  static constexpr int kHalves = WIN ? 2 : 1;
+  static constexpr int kThreads = 128 + 128 * kHalves;
+  static constexpr int kCols = 128 / kHalves;
+  static constexpr uint32_t kSmemBytes = WIN ? kXchOff + 2048 : kXchOff;  // (1,024-byte aligned)
+};
+static_assert(Shape<true>::kSmemBytes <= 232448, "prefill attention shared memory");
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 
 constexpr int kItemRing = 4;
-constexpr int kItemReaders = 3 + 128;  // V producer, S issuer, P.V issuer, softmax threads
 
 struct Bars {
   uint64_t q_full, q_tmem, qn_empty, qpe_empty[2];
@@ -87,6 +101,7 @@ struct Bars {
   uint64_t s_full[2], s_free[2];
   uint64_t p_full, pv_done;
   uint64_t drain_s, drain_pv;
+  uint64_t xch[4];  // WIN: per quarter of the rows
   uint32_t tmem_slot;
   int abort;
   int item[kItemRing];
@@ -149,18 +164,20 @@ __device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, const DevSt
 // s[c] = -inf for the key columns c of the row above hi, or below lo.  The
 // bounds of a warp's rows are `lane` apart: a block of 32 columns that all of
 // them see is decided once (hi_w, lo_w: the first row's bounds).
-__device__ __forceinline__ void mask_above(uint32_t (&s)[128], int hi, int hi_w) {
+template <int N>
+__device__ __forceinline__ void mask_above(uint32_t (&s)[N], int hi, int hi_w) {
 #pragma unroll
-  for (int c0 = 0; c0 < 128; c0 += 32) {
+  for (int c0 = 0; c0 < N; c0 += 32) {
     if (c0 + 31 <= hi_w) continue;
 #pragma unroll
     for (int c = c0; c < c0 + 32; ++c)
       if (c > hi) s[c] = __float_as_uint(-INFINITY);
   }
 }
-__device__ __forceinline__ void mask_below(uint32_t (&s)[128], int lo, int lo_w) {
+template <int N>
+__device__ __forceinline__ void mask_below(uint32_t (&s)[N], int lo, int lo_w) {
 #pragma unroll
-  for (int c0 = 0; c0 < 128; c0 += 32) {
+  for (int c0 = 0; c0 < N; c0 += 32) {
     if (c0 >= lo_w + 31) continue;
 #pragma unroll
     for (int c = c0; c < c0 + 32; ++c)
@@ -172,23 +189,25 @@ __device__ __forceinline__ void mask_below(uint32_t (&s)[128], int lo, int lo_w)
 // P.V): the compiler is free to move arithmetic behind a wait's assembly, and
 // did (B=8 T=4096 causal 1977 -> 1874 us with this and P packed ahead of the
 // wait; B=2 T=4096 under a window of 1,024 with 128 sinks 358 -> 348 us).
-__device__ __forceinline__ void keep_order(float& l, uint32_t (&p)[64]) {
+template <int N>
+__device__ __forceinline__ void keep_order(float& l, uint32_t (&p)[N]) {
   asm volatile("" : "+f"(l) : : "memory");
 #pragma unroll
-  for (int c = 0; c < 64; c += 16)
+  for (int c = 0; c < N; c += 16)
     asm volatile("" : "+r"(p[c]), "+r"(p[c + 1]), "+r"(p[c + 2]), "+r"(p[c + 3]), "+r"(p[c + 4]), "+r"(p[c + 5]),
                  "+r"(p[c + 6]), "+r"(p[c + 7]), "+r"(p[c + 8]), "+r"(p[c + 9]), "+r"(p[c + 10]), "+r"(p[c + 11]),
                  "+r"(p[c + 12]), "+r"(p[c + 13]), "+r"(p[c + 14]), "+r"(p[c + 15]));
 }
 
 template <bool WIN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<WIN>::kThreads, 1)
     prefill_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVsink,
                     const __grid_constant__ CUtensorMap tmO, int T, int n_qt, int n_items, float sl2, int past, int head_group,
                     int window, int sinks, int* __restrict__ work, const DevStatus st) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kHalves = Shape<WIN>::kHalves, kCols = Shape<WIN>::kCols;
+  constexpr int kItemReaders = 3 + 128 * kHalves;  // V producer, S issuer, P.V issuer, softmax threads
   Bars* bar = reinterpret_cast<Bars*>(smem + kBarOff);
   volatile int* abort_flag = &bar->abort;
   const int warp = threadIdx.x >> 5;
@@ -196,11 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
-    mbar_init(&bar->q_tmem, 128);
-    mbar_init(&bar->qn_empty, 4);
+    mbar_init(&bar->q_tmem, 128 * kHalves);
+    mbar_init(&bar->qn_empty, 4 * kHalves);
     mbar_init(&bar->qpe_empty[0], 1);
     mbar_init(&bar->qpe_empty[1], 1);
-    mbar_init(&bar->p_full, 128);
+    mbar_init(&bar->p_full, 128 * kHalves);
     mbar_init(&bar->pv_done, 1);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&bar->item_full[i], 1);
@@ -212,8 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar->v_full[i], 1);
       mbar_init(&bar->v_empty[i], 1);
       mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->s_free[i], 128);
+      mbar_init(&bar->s_free[i], 128 * kHalves);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&bar->xch[i], 64);
     mbar_init(&bar->drain_s, 1);
     mbar_init(&bar->drain_pv, 1);
     bar->abort = 0;
@@ -391,12 +411,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&bar->drain_pv, 0, st, nullptr, 49);
     }
   } else {
-    // ---- softmax / correction / epilogue: warps 2..5, one thread per query row ----
+    // ---- softmax / correction / epilogue: warps 2..5, one thread per query row
+    // (WIN: and warps 8..11, for the second half of the columns) ----
+    const int half = WIN ? warp >> 3 : 0;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     bool ok = true;
     int gt = 0;
+    // WIN: the two threads of a row tell each other x; the other one's value
+    float* const xch = reinterpret_cast<float*>(smem + kXchOff) + row;
+    int n_xch = 0;
+    auto exchange = [&](float x, float& y) -> bool {
+      float* at = xch + (n_xch & 1) * 256;
+      at[half * 128] = x;
+      mbar_arrive(&bar->xch[quarter]);
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&bar->xch[quarter], n_xch & 1, st, abort_flag, 55));
+      ++n_xch;
+      y = at[(half ^ 1) * 128];
+      return got;
+    };
     // the previous item, whose O is written out once the next item's Q is in place
     int prev_qpos = -1, prev_h = 0, prev_b = 0, prev_last = -1;
     float prev_l = 1.f;
@@ -413,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const uint8_t* qrow = smem + kQOff + row * 128;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 2 / kHalves; ++i) {
+          const int c = half + i;
           uint32_t v[32];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -440,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ta = tmem + lane_addr + kTmO;
         uint8_t* orow = smem + kQOff + row * 128;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = half * kCols; c < half * kCols + kCols; c += 32) {
           uint32_t r[32];
           tmem_ld32(ta + c, r);
           tmem_wait_ld();
@@ -458,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint8_t* rows = smem + kQOff + quarter * 32 * 128;
           const int first = prev_qpos - lane;  // this warp's first query
           if (first < T) {
-            tma_store_3d(&tmO, rows, prev_h * 128, first, prev_b);
-            tma_store_3d(&tmO, rows + kAtom, prev_h * 128 + 64, first, prev_b);
+            for (int c = half; c < half + 2 / kHalves; ++c)
+              tma_store_3d(&tmO, rows + c * kAtom, prev_h * 128 + 64 * c, first, prev_b);
           }
           bulk_commit();
         }
@@ -474,31 +509,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&bar->s_full[sb], (gt >> 1) & 1, st, abort_flag, 50));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[128];
+        uint32_t s[kCols];
         {
-          uint32_t (&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
-          uint32_t (&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32]);
-          uint32_t (&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[64]);
-          uint32_t (&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[96]);
-          const uint32_t ta = tmem + lane_addr + kTmS + sb * 128;
-          tmem_ld32(ta, s0);
-          tmem_ld32(ta + 32, s1);
-          tmem_ld32(ta + 64, s2);
-          tmem_ld32(ta + 96, s3);
+          const uint32_t ta = tmem + lane_addr + kTmS + sb * 128 + half * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) tmem_ld32(ta + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
           tmem_wait_ld();
         }
         tc_fence_before();
         mbar_arrive(&bar->s_free[sb]);  // the score buffer may take S_{j+2}
-        const int k0 = t.key0(j);
+        const int k0 = t.key0(j) + half * kCols;  // the key of this thread's first column
         // max of the raw scores (the scale is positive), causal mask (key k
         // visible to query position past + qpos iff k <= past + qpos) on the
         // tiles that reach beyond the tile's first query
         if constexpr (WIN) {
           const int hi = past + qpos - k0, hi_w = past + t.q0 + quarter * 32 - k0;  // last visible column
           if (j < t.n_sink) {  // sinks before the window: every query sees them
-            if (k0 + 127 >= t.n_first) {
+            if (k0 + kCols - 1 >= t.n_first) {
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
+              for (int c = 0; c < kCols; ++c)
                 if (k0 + c >= t.n_first) s[c] = __float_as_uint(-INFINITY);
             }
           } else {
@@ -508,15 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mask_below(s, hi - window + 1, hi_w - window + 1);
               } else {
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
+                for (int c = 0; c < kCols; ++c)
                   if (c <= hi - window && k0 + c >= sinks) s[c] = __float_as_uint(-INFINITY);
               }
             }
-            if (k0 + 127 > past + t.q0) mask_above(s, hi, hi_w);
+            if (k0 + kCols - 1 > past + t.q0) mask_above(s, hi, hi_w);
           }
         } else if (k0 + 127 > past + t.q0) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < kCols; ++c)
             if (k0 + c > past + qpos) s[c] = __float_as_uint(-INFINITY);
         }
         // eight independent partial maxima / sums keep the reductions off a
@@ -527,17 +556,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) mp[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 8]));
 #pragma unroll
-        for (int c = 16; c < 128; c += 16)
+        for (int c = 16; c < kCols; c += 16)
 #pragma unroll
           for (int i = 0; i < 8; ++i) mp[i] = fmax3(mp[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
         float mx = fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], fmax3(mp[5], mp[6], mp[7])));
+        if constexpr (WIN) {
+          float other;
+          ok = exchange(mx, other);
+          if (!ok) break;
+          mx = fmaxf(mx, other);
+        }
         mx *= sl2;  // log2 units
         const bool need = mx > m + kRescaleThreshold;
         const float m_new = need ? mx : m;
         const float alpha = need ? ex2_approx(m - m_new) : 1.f;
         float sp[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
+        for (int c = 0; c < kCols; c += 2) {
           float x0, x1;
           fma_x2(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, -m_new, -m_new);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -549,9 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * alpha + sum;
         m = m_new;
         // P_j as bf16 pairs (low half = even key), all of it ahead of the wait
-        uint32_t pk[64];
+        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+        for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
         keep_order(l, pk);
         // the previous P.V (this CTA's tile gt-1) has read P and added into O:
         // P may be rewritten and O rescaled
@@ -563,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j > 0 && __any_sync(0xffffffffu, need)) {
           const uint32_t ta = tmem + lane_addr + kTmO;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = half * kCols; c < half * kCols + kCols; c += 32) {
             uint32_t r[32];
             tmem_ld32(ta + c, r);
             tmem_wait_ld();
@@ -575,9 +610,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // P_j into the P buffer
         {
-          const uint32_t tp = tmem + lane_addr + kTmP;
+          const uint32_t tp = tmem + lane_addr + kTmP + half * (kCols / 2);
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) tmem_st16(tp + c, &pk[c]);
+          for (int c = 0; c < kCols / 2; c += 16) tmem_st16(tp + c, &pk[c]);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -586,6 +621,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           bulk_wait_read<0>();
           mbar_arrive(&bar->qn_empty);
         }
+      }
+      if (!ok) break;
+      if constexpr (WIN) {
+        float other;
+        ok = exchange(l, other);
+        if (!ok) break;
+        l += other;
       }
       prev_qpos = qpos;
       prev_h = t.h;
@@ -623,9 +665,11 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
                          256, (uint64_t)a.cap * 256, 64, 128))
     return cudaErrorInvalidValue;
   auto kern = win ? prefill_attn_tc<true> : prefill_attn_tc<false>;
+  const uint32_t smem_bytes = win ? Shape<true>::kSmemBytes : Shape<false>::kSmemBytes;
+  const int threads = win ? Shape<true>::kThreads : Shape<false>::kThreads;
   static bool attr_set[2] = {false, false};
   if (!attr_set[win]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes);
     if (e != cudaSuccess) return e;
     attr_set[win] = true;
   }
@@ -657,7 +701,7 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   // the work counter: an int of the status region (cleared before every call)
   int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
   DevStatus dst{st.word, st.wait_limit_ns};
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, tvs, to, a.T, n_qt, n_items,
+  return launch_pdl(kern, dim3(grid), dim3(threads), smem_bytes, stream, tq, tk, tv, tvs, to, a.T, n_qt, n_items,
                     a.scale * 1.4426950408889634f, a.past, G, window, a.sinks, work, dst);
 }
 
