@@ -161,29 +161,8 @@ __device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, const DevSt
   return true;
 }
 
-// s[c] = -inf for the key columns c of the row above hi, or below lo.  The
-// bounds of a warp's rows are `lane` apart: a block of 32 columns that all of
-// them see is decided once (hi_w, lo_w: the first row's bounds).
-template <int N>
-__device__ __forceinline__ void mask_above(uint32_t (&s)[N], int hi, int hi_w) {
-#pragma unroll
-  for (int c0 = 0; c0 < N; c0 += 32) {
-    if (c0 + 31 <= hi_w) continue;
-#pragma unroll
-    for (int c = c0; c < c0 + 32; ++c)
-      if (c > hi) s[c] = __float_as_uint(-INFINITY);
-  }
-}
-template <int N>
-__device__ __forceinline__ void mask_below(uint32_t (&s)[N], int lo, int lo_w) {
-#pragma unroll
-  for (int c0 = 0; c0 < N; c0 += 32) {
-    if (c0 >= lo_w + 31) continue;
-#pragma unroll
-    for (int c = c0; c < c0 + 32; ++c)
-      if (c < lo) s[c] = __float_as_uint(-INFINITY);
-  }
-}
+// the lowest n bits of 32 (none for n < 0, all for n > 32)
+__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 // What computed l and p stays ahead of what follows (the wait for the previous
 // P.V): the compiler is free to move arithmetic behind a wait's assembly, and
@@ -523,25 +502,26 @@ __global__ void __launch_bounds__(Shape<WIN>::kThreads, 1)
         // visible to query position past + qpos iff k <= past + qpos) on the
         // tiles that reach beyond the tile's first query
         if constexpr (WIN) {
-          const int hi = past + qpos - k0, hi_w = past + t.q0 + quarter * 32 - k0;  // last visible column
-          if (j < t.n_sink) {  // sinks before the window: every query sees them
-            if (k0 + kCols - 1 >= t.n_first) {
+          // tiles that some query of the item sees a part of: 32 columns at a time,
+          // the visible ones of this thread's row as bits (one short piece of code for
+          // every mask: with a loop of comparisons for each, a window of 1,024 with
+          // 128 sinks took 310 us where it takes 295, one of 4,096 at T=8192 729
+          // where it takes 693, much of it waits for instructions)
+          const bool in_sinks = j < t.n_sink;
+          if (in_sinks ? k0 + kCols > t.n_first
+                       : past + t.q0 + 127 - k0 >= window || k0 + kCols - 1 > past + t.q0) {
 #pragma unroll
-              for (int c = 0; c < kCols; ++c)
-                if (k0 + c >= t.n_first) s[c] = __float_as_uint(-INFINITY);
-            }
-          } else {
-            // keys behind the later queries' windows, unless they are sinks, and keys ahead
-            if (past + t.q0 + 127 - k0 >= window) {
-              if (k0 >= sinks) {
-                mask_below(s, hi - window + 1, hi_w - window + 1);
-              } else {
+            for (int c0 = 0; c0 < kCols; c0 += 32) {
+              const int kw = k0 + c0, i = past + qpos;
+              const uint32_t seen = in_sinks ? first_bits(t.n_first - kw)  // (every query sees the sinks)
+                                             : first_bits(i + 1 - kw) & (~first_bits(i + 1 - window - kw) |
+                                                                         first_bits(sinks - kw));
+              if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                  if (c <= hi - window && k0 + c >= sinks) s[c] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < 32; ++c)
+                  if (!(seen & (1u << c))) s[c0 + c] = __float_as_uint(-INFINITY);
               }
             }
-            if (k0 + kCols - 1 > past + t.q0) mask_above(s, hi, hi_w);
           }
         } else if (k0 + 127 > past + t.q0) {
 #pragma unroll
