@@ -404,7 +404,7 @@ def _rows(x, what: str, cols: int, device: int) -> int:
     if not (x.dtype is _torch.bfloat16 and x.get_device() == device and len(shape) == 2 and shape[1] == cols and
             stride[1] == 1):
         raise ValueError(f"{what}: need a bf16 tensor [rows, {cols}] with contiguous rows on the current device")
-    return stride[0]
+    return stride[0] if shape[0] > 1 else cols  # (the stride of a single row is arbitrary)
 
 
 def _head_rows(x, what: str, heads: int, rows: int, device: int):
@@ -414,7 +414,7 @@ def _head_rows(x, what: str, heads: int, rows: int, device: int):
             stride[2] == 1):
         raise ValueError(f"{what}: need a bf16 tensor [{rows}, {heads}, 128] with a contiguous last dimension on the "
                          "current device")
-    return stride[0], stride[1]
+    return stride[0] if rows > 1 else 0, stride[1]
 
 
 def _ints(x, what: str, n: int, device: int) -> int:

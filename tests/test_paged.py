@@ -684,3 +684,29 @@ def test_window_that_holds_every_key_equals_the_causal_attention(gpu_available):
         m.mla_window_attention(q, 0, k, v, out, ws, window=window, sinks=sinks)
         outs.append(out)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.gpu
+def test_single_rows_with_any_row_stride():
+    """the stride of a tensor's only row says nothing: every view of it is taken, with the same results"""
+    import torch
+
+    heads, page = 4, 16
+    torch.manual_seed(5)
+    k, v = (torch.randn(1, heads, 128, device="cuda").bfloat16() for _ in range(2))
+    pe, q = torch.randn(1, 64, device="cuda").bfloat16(), torch.randn(1, heads * 192, device="cuda").bfloat16()
+    P = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = []
+    for row in (None, 1, 3):
+        def view(x):
+            return x if row is None else x.as_strided(x.shape, (row,) + x.stride()[1:])
+        t = m.alloc_paged_cache(1, page, heads)
+        t["table"] = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+        c = m.make_paged_cache(t)
+        m.mla_paged_append(c, view(k), view(v), view(pe), P, 1, m.alloc_workspace(m.MODE_PAGED_APPEND, 1, 1))
+        out = torch.empty(1, heads * 128, dtype=torch.bfloat16, device="cuda")
+        m.mla_paged_attention(c, view(q), P, 0, view(out), m.alloc_workspace(m.MODE_PAGED_ATTN, 1, 1))
+        got.append(torch.cat([out.view(-1).view(torch.int16).int(), t["k_codes"].view(-1).int(),
+                              t["v_codes"].view(-1).int(), t["k_pe"].view(-1).view(torch.int16).int()]))
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    assert got[0].any()
