@@ -710,3 +710,86 @@ def test_single_rows_with_any_row_stride():
                               t["v_codes"].view(-1).int(), t["k_pe"].view(-1).view(torch.int16).int()]))
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
     assert got[0].any()
+
+
+@gpu
+@pytest.mark.parametrize("order", ["growing", "falling", "spikes"])
+def test_window_attention_moving_maxima(gpu_available, order):
+    """Scores whose maximum moves by far more than the rescale threshold from key tile to key tile, in the first or
+    the second half of a tile; more items than SMs, so that every CTA takes several."""
+    import torch
+    B, T, P0, window, sinks, cap = 1, 700, 130, 300, 9, 830
+    L = P0 + T
+    q, k, v = normal(1, B, T, 64 * 192), normal(2, B, 64, cap, 192), normal(3, B, 64, cap, 128)
+    u = normal(4, 192).sign()
+    q = (q * 0.25 + u.repeat(64)).bfloat16()  # every query has a part along u
+    j = torch.arange(cap, device="cuda")
+    along = {"growing": j * 0.02, "falling": (cap - j) * 0.02,
+             "spikes": ((j % 97 == 0) * 7.0 + (j % 64 == 63) * 4.0)}[order]
+    k = (k * 0.25 + along[None, None, :, None] * u).bfloat16()
+    out = torch.full((B, T, 64 * 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = m.alloc_workspace(m.MODE_WINDOW_ATTN, B, T)
+    m.mla_window_attention(q, P0, k, v, out, ws, window=window, sinks=sinks)
+    assert m.mla_device_status(ws) == 0
+    got, qn, kr, vr = f64(out).reshape(T, 64, 128), f64(q).reshape(T, 64, 192), f64(k)[0], f64(v)[0]
+    i, jj = np.arange(P0, L)[:, None], np.arange(L)[None, :]
+    seen = (jj <= i) & ((i - jj < window) | (jj < sinks))
+    for h in (0, 2, 40, 63):
+        s = np.where(seen, qn[:, h] @ kr[h, :L].T / math.sqrt(192), -np.inf)
+        w = np.exp(s - s.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        ref, mass = w @ vr[h, :L], w @ np.abs(vr[h, :L])
+        # a score: 192 products summed in float32, then scaled and shifted by a maximum of the same size: at most
+        # 200 roundings of 2^-24 of the sum of the products' magnitudes, for a key and for the row's sum
+        ds = 2 * 200 * 2.0 ** -24 * (np.abs(qn[:, h]) @ np.abs(kr[h, :L]).T).max() / math.sqrt(192)
+        d = np.abs(got[:, h] - ref)
+        # output 2^-8 |ref|, probabilities 2^-8 of the weighted |v|, the scores' errors on all of it; 1 % for the
+        # products of these and the exponential's own 2^-22
+        assert np.all(d <= 1.01 * (2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + math.expm1(ds)) * mass)), (h, d.max())
+
+
+@gpu
+def test_window_attention_captured_and_on_two_streams(gpu_available):
+    """A captured call replayed with new inputs, and two streams at once with workspaces of their own, give the
+    eager call's bits."""
+    import torch
+    B, T, P0, window, sinks = 2, 260, 100, 150, 5
+    sets = [(normal(10 * i + 1, B, T, 64 * 192), normal(10 * i + 2, B, 64, P0 + T, 192),
+             normal(10 * i + 3, B, 64, P0 + T, 128)) for i in range(4)]
+
+    def run(x, out, ws):
+        m.mla_window_attention(x[0], P0, x[1], x[2], out, ws, window=window, sinks=sinks)
+
+    def fresh():
+        return torch.empty((B, T, 64 * 128), dtype=torch.bfloat16, device="cuda"), \
+            m.alloc_workspace(m.MODE_WINDOW_ATTN, B, T)
+
+    want = []
+    for x in sets:
+        out, ws = fresh()
+        run(x, out, ws)
+        want.append(out)
+    torch.cuda.synchronize()
+    x, (out, ws) = [t.clone() for t in sets[0]], fresh()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        run(x, out, ws)
+    for i in range(4):
+        with torch.cuda.stream(s):
+            for dst, src in zip(x, sets[i]):
+                dst.copy_(src)
+            g.replay()
+        s.synchronize()
+        assert torch.equal(out, want[i]), i
+    streams, res = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    own = [fresh() for _ in range(8)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for n in range(2):
+            with torch.cuda.stream(streams[n]):
+                run(sets[i], *own[2 * i + n])
+                res.append((i, own[2 * i + n][0]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in res)
