@@ -412,8 +412,10 @@ int mla_ffn(const mla_ffn_weights_t* w, const mla_params_t* params, const void* 
  *   k_codes, v_codes  uint8 [n_pages, heads, page, 128], E4M3 (the OCP FP8
  *                     encoding, largest finite 448)
  *   k_pe              bf16 [n_pages, page, 64], rotated
- *   k_scales, v_scales float [n_pages, heads], positive; mla_paged_append
- *                     writes powers of two, 2^-60 .. 2^60
+ *   k_scales, v_scales float [n_pages, heads], positive and finite;
+ *                     mla_paged_append writes powers of two, 2^-60 .. 2^60,
+ *                     except that a partly filled page keeps a larger scale
+ *                     that it came with
  *   table             int [B, max_pages] in DEVICE memory: the pages of each
  *                     sequence in order, position p in page table[b][p / page],
  *                     slot p % page.  Read by the kernels: a captured graph
@@ -453,8 +455,9 @@ typedef struct {
  * Scales: with k the smallest integer in [-60, 60] for which the new tokens
  * of a page and head have amax <= 448 * 2^k, the page's scale becomes 2^k; in
  * a page that already holds tokens (P[b] not on a page's start) it only grows:
- * the larger of that and the old scale, and the codes already there are
- * re-expressed at the new scale (rounded again).  Code = x / scale rounded to
+ * the larger of that and the old scale (any positive number), and where it
+ * grows the codes already there are re-expressed at the new scale (rounded
+ * again).  Code = x / scale rounded to
  * nearest even, saturating at +-448 (an infinity gives the page 2^60); NaN
  * stays NaN and does not count for amax.  Slots behind the last token, and
  * every other page, are left as they were.
@@ -540,7 +543,8 @@ int mla_decode_paged(const mla_weights_t* w, const mla_params_t* params, const v
 
 /* Prefill of T new tokens per sequence at positions P0..P0+T-1 into the paged
  * 8-bit cache (64 heads): their keys and values are appended to the pages, and
- * the tokens attend to the P0 cached positions (as the pages hold them) and to
+ * the tokens attend to the P0 cached positions (as the pages hold them, code *
+ * scale rounded to bf16: exact for a power of two) and to
  * each other (as computed, not quantized), causally, with window > 0 only to
  * the last `window` keys and the first `sinks`.  P0 = 0, window = 0 computes
  * the out of mla_prefill.

@@ -333,7 +333,8 @@ struct PagedAppendArgs {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 
 // Positions of the dense caches K [B, heads, cap, 192], V [B, heads, cap, 128]
-// filled with the paged ones' values (code * scale, exact in bf16): positions
+// filled with the paged ones' values (code * scale in bf16, exact where the scale
+// is a power of two): positions
 // j < P with j >= from or j < first, of every sequence.
 struct PagedGatherArgs {
   PagedCache c;

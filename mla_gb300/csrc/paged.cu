@@ -5,11 +5,15 @@
 // 16 lanes, 16 bytes a lane), held in registers while their largest magnitude
 // is reduced over the page's warps, and written as E4M3 codes of x * 2^-k with
 // the smallest k in [-60, 60] that keeps amax <= 448 * 2^k.  A page that
-// already holds tokens keeps max(k, old k); when k grows, its codes are
-// decoded and coded again at the new scale.  Scales are powers of two, so that
-// a code and its re-expression differ only where the larger scale drops bits.
+// already holds tokens keeps the larger of 2^k and its scale; when 2^k is the
+// larger, its codes are decoded and coded again at the new scale.  Scales are
+// powers of two, so that a code and its re-expression differ only where the
+// larger scale drops bits; a page that something else has filled may bring any
+// positive scale, by which the new tokens are divided then.
 // The rotary keys (one per token, shared by the heads) are rotated by a
-// further row of CTAs, angles as in the RoPE table.
+// further row of CTAs, angles as in the RoPE table.  The kernel is held to 64
+// registers: the division by a foreign scale would take it to 97, with fewer
+// warps to load (8 x 4096 tokens 345 us where they take 259).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -63,6 +67,59 @@ __device__ __forceinline__ uint2 code8(const uint4& u, float r) {
                     code2(c.x * r, c.y * r) | code2(d.x * r, d.y * r) << 16);
 }
 
+// y rounded towards zero from a value that is y + rest: to odd, so that the
+// rounding of y to a code (4 bits of 24) has the value's own answer
+__device__ __forceinline__ float to_odd(float y, float rest) {
+  return rest > 0.f || rest < 0.f ? __uint_as_float(__float_as_uint(y) | 1u) : y;
+}
+// x / s and c * r for a rounding to a code
+__device__ __forceinline__ float quotient(float x, float s) {
+  const float y = __fdiv_rz(x, s);
+  return to_odd(y, fmaf(-y, s, x));
+}
+__device__ __forceinline__ float product(float c, float r) {
+  const float y = __fmul_rz(c, r);
+  return to_odd(y, fmaf(c, r, -y));
+}
+
+// The two rare forms of a page's rows, 8 elements of n rows each.  New tokens in a page whose scale is not a power of two: divided by it.
+__device__ __forceinline__ void divide_rows(const __nv_bfloat16* src, long long src_step, uint8_t* dst, int dst_step, int n,
+                                         float scale) {
+#pragma unroll 1
+  for (int i = 0; i < n; ++i, src += src_step, dst += dst_step) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
+    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_bf16x2(in[e]);
+      out[e] = code2(quotient(f.x, scale), quotient(f.y, scale));
+    }
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0] | out[1] << 16, out[2] | out[3] << 16);
+  }
+}
+// Codes that a growing scale re-expresses, r = old scale / new scale.
+__device__ __forceinline__ void rescale_rows(uint8_t* at, int step, int n, float r) {
+#pragma unroll 1
+  for (int i = 0; i < n; ++i, at += step) {
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
+    const uint32_t in[4] = {x.x, x.x >> 16, x.y, x.y >> 16};
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = decode2(in[e]);
+      out[e] = code2(product(f.x, r), product(f.y, r));
+    }
+    *reinterpret_cast<uint2*>(at) = make_uint2(out[0] | out[1] << 16, out[2] | out[3] << 16);
+  }
+}
+
+// keys or values of sequence b's new token t, head h
+__device__ __forceinline__ const __nv_bfloat16* source(const PagedAppendArgs& a, int b, int h, int t, int row, bool is_v) {
+  return is_v ? a.v + b * a.v_seq + (a.v_seq ? t : row + t) * a.v_token + h * a.v_head
+              : a.k + b * a.k_seq + (a.k_seq ? t : row + t) * a.k_token + h * a.k_head;
+}
+
 // larger |x| of two pairs of bf16, element by element, NaN ignored
 __device__ __forceinline__ __nv_bfloat162 top_pair(__nv_bfloat162 m, uint32_t u) {
   const uint32_t a = u & 0x7fff7fffu;
@@ -71,7 +128,7 @@ __device__ __forceinline__ __nv_bfloat162 top_pair(__nv_bfloat162 m, uint32_t u)
 
 // Grid: x = (sequence, touched page), y = head group, and one row of CTAs more
 // for the rotary keys.  2^w_log warps share a head, each holding up to 8 tokens.
-__global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs a, int pages_per_seq, int w_log) {
+__global__ void __launch_bounds__(512, 2) paged_append_kernel(const PagedAppendArgs a, int pages_per_seq, int w_log) {
   __shared__ float red[16][2];
   pdl_launch_dependents();
   pdl_wait();
@@ -135,12 +192,11 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
   uint4 u[kRows];
   float top = 0.f;
   float* scale_at = nullptr;
-  int k_old = kFloorExp;
+  float old = 0.f;  // the scale that the page's tokens have
   const int mine = (n - wi + W - 1) >> w_log;  // this warp's tokens: wi, wi + W, ..
   if (live) {
-    const __nv_bfloat16* src = is_v ? a.v + b * a.v_seq + (a.v_seq ? t0 : s.row + t0) * a.v_token + h * a.v_head
-                                    : a.k + b * a.k_seq + (a.k_seq ? t0 : s.row + t0) * a.k_token + h * a.k_head;
     const long long token = is_v ? a.v_token : a.k_token;
+    const __nv_bfloat16* src = source(a, b, h, t0, s.row, is_v);
     const __nv_bfloat16* at = src + wi * token + col;
     const long long step = token << w_log;
 #pragma unroll
@@ -149,7 +205,7 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
       at += step;
     }
     scale_at = (is_v ? a.c.v_scales : a.c.k_scales) + (size_t)pid * a.c.heads + h;
-    if (slot0 > 0) k_old = min(kCeilExp, max(kFloorExp, (int)((__float_as_uint(*scale_at) >> 23) & 255) - 127));
+    if (slot0 > 0) old = *scale_at;
     __nv_bfloat162 m0 = __floats2bfloat162_rn(0.f, 0.f), m1 = m0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -167,30 +223,27 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const PagedAppendArgs
     for (int i = 0; i < W; ++i) top = fmaxf(top, red[warp - wi + i][is_v]);
   }
   if (!live) return;
-  const int k_new = max(k_old, block_exp(top));
+  const float need = exp2_int(block_exp(top)), scale = fmaxf(need, old);
+  if (wi == 0 && (lane & 15) == 0) *scale_at = scale;
   uint8_t* dst = (is_v ? a.c.v_codes : a.c.k_codes) + (((size_t)pid * a.c.heads + h) << page_log) * 128 + col;
-  if (slot0 > 0 && k_new > k_old) {
-    const float r = exp2_int(max(k_old - k_new, -126));
-    for (int i = wi; i < slot0; i += W) {
-      uint2* at = reinterpret_cast<uint2*>(dst + i * 128);
-      const uint2 c = *at;
-      const float2 x0 = decode2(c.x), x1 = decode2(c.x >> 16), x2 = decode2(c.y), x3 = decode2(c.y >> 16);
-      *at = make_uint2(code2(x0.x * r, x0.y * r) | code2(x1.x * r, x1.y * r) << 16,
-                       code2(x2.x * r, x2.y * r) | code2(x3.x * r, x3.y * r) << 16);
-    }
-  }
-  if (wi == 0 && (lane & 15) == 0) *scale_at = exp2_int(k_new);
-  const float r = exp2_int(-k_new);
-  uint8_t* at = dst + (slot0 + wi) * 128;
+  const uint32_t bits = __float_as_uint(scale);
+  if (!(bits & 0x7fffffu) && bits - (1u << 23) < 253u << 23) {  // a power of two that has a reciprocal
+    const float r = __uint_as_float((254u << 23) - bits);
+    uint8_t* at = dst + (slot0 + wi) * 128;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (i < mine) *reinterpret_cast<uint2*>(at) = code8(u[i], r);
-    at += 128 << w_log;
+    for (int i = 0; i < kRows; ++i) {
+      if (i < mine) *reinterpret_cast<uint2*>(at) = code8(u[i], r);
+      at += 128 << w_log;
+    }
+  } else {
+    divide_rows(source(a, b, h, t0 + wi, s.row, is_v) + col, (is_v ? a.v_token : a.k_token) << w_log,
+                dst + (slot0 + wi) * 128, 128 << w_log, mine, scale);
   }
+  if (slot0 > 0 && need > old) rescale_rows(dst + wi * 128, 128 << w_log, (slot0 - wi + W - 1) >> w_log, old / need);
 }
 
 // Grid: x = (sequence, page of 16 positions), y = head: a warp per 2
-// positions, 16 codes a lane and step.  The rotary key of a position is
+// positions, 8 codes a lane and step.  The rotary key of a position is
 // copied into each head's row.
 __global__ void __launch_bounds__(256) paged_gather_kernel(const PagedGatherArgs a, int blocks) {
   pdl_launch_dependents();
