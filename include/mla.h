@@ -494,9 +494,12 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
  * hold (table entries of pages without a visible key are not looked at, so
  * pages that a window has passed can be given back).  A key that one query
  * sees has weight zero for the others; a NaN among its values reaches those
- * of its call too.  Scores, softmax
- * statistics and sums are float32; the weights (probability times value
- * scale) are rounded to float16 for the product with V.
+ * of its call too.  Scores, softmax statistics and sums are float32.  For the
+ * product with V the weights of the up to 32 keys that a page holds of a tile
+ * are rounded to float16, relative to the largest of them: by 2^-11 of the
+ * weight, or 2^-40 of that largest one where it is below 2^-29 of it.  Query
+ * values of the nope part that are below 2^-17 of the largest one of their row
+ * and head are rounded to 2^-24 of the power of two below that one.
  * A P[b] outside [-1, P_max] is taken as idle, a page number outside
  * [0, n_pages) is clamped, and mla_device_status then returns
  * MLA_ERR_INVALID_ARG.

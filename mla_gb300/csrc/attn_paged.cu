@@ -42,14 +42,23 @@
 //     a power of two per row so that its largest element is in [1, 2) (bf16's
 //     8 bits fit float16's 11; elements below 2^-14 of the largest lose bits
 //     below 2^-24 of it).  The rotary part is a bf16 MMA with its own sum.
-//   * softmax on the accumulator fragments: a running maximum per query (moved
-//     only when it grows by more than 2^8, so that weights stay below 2^8)
-//     over log2(p) + log2(vscale), so that weights that include the value
-//     scale stay in float16's range; the sum of p is kept beside it in float32.
-//   * O^T = V^T P^T: the weights are rounded to float16 (relative 2^-11, an
-//     eighth of the output's own bf16 rounding) and transposed 8 x 8
-//     (movmatrix) into the B operand; V codes of two keys are interleaved by
-//     byte permutes into A fragments, a thread's 16 bytes being 16 rows.
+//   * softmax on the accumulator fragments, in float32: a running maximum per
+//     query, moved only when it grows by more than 2^8, and the sum of p.
+//   * O^T = V^T P^T: the weights of the 32 keys (16 with 16-token pages) that
+//     share a value scale, over the largest of them and times 2^15, are rounded
+//     to float16: relative 2^-11, an eighth of the output's own bf16 rounding,
+//     down to 2^-29 of the largest, and 2^-40 of it below.  They are transposed
+//     8 x 8 (movmatrix) into the B operand; V codes of two keys are interleaved by
+//     byte permutes into A fragments, a thread's 16 bytes being 16 rows.  The
+//     sum of those keys enters the accumulators in float32, times the value
+//     scale and the largest weight: neither a page whose scale is far above
+//     its visible values nor a key that outweighs a long context by far takes
+//     bits from the other pages.  (With weight times scale rounded against one
+//     running maximum, a page whose scale was 2^24 times what its visible
+//     values need took a third of the output.  It costs nothing at 64-token
+//     pages, 64 x 1001 keys 170 us; with 16-token ones, two maxima a tile, 32
+//     ragged sequences take 379 us for 370, four drafts on 32-token ones 39.6
+//     for 37.3.)
 // Keys that no query sees give weight zero and their value codes are cleared
 // (they may decode to NaN).
 #include <cuda_fp16.h>
@@ -65,6 +74,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kWeightScale = 32768.f;    // of the float16 weights: the largest one, 2^15
 
 constexpr int kTile = 64, kStages = 3, kGroup = 4;
 constexpr int kThreads = 384;
@@ -204,8 +214,9 @@ __device__ __forceinline__ void pair_wait(int k) {
   }
 }
 
-// ONE: one query per sequence (a fragment's second column is not there)
-template <bool ONE>
+// ONE: one query per sequence (a fragment's second column is not there).
+// TWO_PAGES: pages of 16 tokens, i.e. a warp's 32 keys of a tile lie in two.
+template <bool ONE, bool TWO_PAGES>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmPe, const PagedAttnArgs a, uint64_t wait_limit_ns) {
@@ -406,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, t = lane & 3;
   const float sl2 = a.scale * kLog2e;
   float* merge = reinterpret_cast<float*>(smem + kMergeOff) + hh * kMergeRows * 128;
-  constexpr int kKeys = kTile / 2, kBlocks = kKeys / 16, NE = ONE ? 1 : 2;
+  constexpr int kKeys = kTile / 2, kBlocks = kKeys / 16, NE = ONE ? 1 : 2, kRefs = TWO_PAGES ? kBlocks : 1;
   uint32_t off16[kBlocks];  // byte offset of this head's 16-key blocks in the tile's K and V
   int sub16[kBlocks];       // and their page of the tile
 #pragma unroll
@@ -560,20 +571,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // running maximum of log2(p * vscale) per query, over the 8 lanes of its column
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int ks = 0; ks < kBlocks; ++ks) {
-          const float lv = __log2f(vsc[ks]);
-#pragma unroll
-          for (int e = 0; e < NE; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[ks][e], s[ks][e + 2]) + lv);
-        }
+        // maximum score per query and page, over the 8 lanes of its column
+        float mx[2] = {-INFINITY, -INFINITY}, top[kRefs][2];
         bool need[2] = {false, false};
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+#pragma unroll
+          for (int r = 0; r < kRefs; ++r) {
+            float x = fmaxf(s[r][e], s[r][e + 2]);
+            if (kRefs == 1) x = fmaxf(x, fmaxf(s[kBlocks - 1][e], s[kBlocks - 1][e + 2]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            top[r][e] = x;
+            mx[e] = fmaxf(mx[e], x);
+          }
           need[e] = mx[e] > m[e] + kRescaleThreshold;
         }
         if (__any_sync(0xffffffffu, need[0] | need[1])) {
@@ -593,31 +605,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[c][e] *= alpha[e & 1];
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        uint32_t pw[kBlocks][2];  // weights of keys 2t, 2t+1 (and 8 further) of query g
+        float to_acc[kRefs][2];   // largest weight * value scale
 #pragma unroll
         for (int ks = 0; ks < kBlocks; ++ks) {
+          const int r = ks < kRefs ? ks : kRefs - 1;
           float p[4] = {0.f, 0.f, 0.f, 0.f};
+          to_acc[r][1] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((e & 1) >= NE) continue;
-            p[e] = ex2_approx(s[ks][e] - ref[e & 1]);
-            l[e & 1] += p[e];
+          for (int e = 0; e < NE; ++e) {
+            const bool none = top[r][e] == -INFINITY;
+            const float ref = none ? 0.f : top[r][e], f = none ? 0.f : ex2_approx(ref - m[e]);
+            p[e] = ex2_approx(s[ks][e] - ref);
+            p[e + 2] = ex2_approx(s[ks][e + 2] - ref);
+            l[e] = fmaf(f, p[e] + p[e + 2], l[e]);
+            to_acc[r][e] = f * (vsc[ks] * (1.f / kWeightScale));
           }
-          // weights of keys 2t, 2t+1 (and 8 further) of query g
-          const uint32_t p0 = transpose8(pack_f16x2(p[0] * vsc[ks], p[1] * vsc[ks]));
-          const uint32_t p1 = transpose8(pack_f16x2(p[2] * vsc[ks], p[3] * vsc[ks]));
-          const uint4 x0 = xv[ks][0], x1 = xv[ks][1], x2 = xv[ks][2], x3 = xv[ks][3];
-          const uint32_t e0[4] = {x0.x, x0.y, x0.z, x0.w}, e1[4] = {x1.x, x1.y, x1.z, x1.w};
-          const uint32_t e2[4] = {x2.x, x2.y, x2.z, x2.w}, e3[4] = {x3.x, x3.y, x3.z, x3.w};
+          pw[ks][0] = transpose8(pack_f16x2(p[0] * kWeightScale, p[1] * kWeightScale));
+          pw[ks][1] = transpose8(pack_f16x2(p[2] * kWeightScale, p[3] * kWeightScale));
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t b0, b1, b2, b3;
-            decode4(__byte_perm(e0[e], e1[e], 0x5140), b0, b1);
-            decode4(__byte_perm(e2[e], e3[e], 0x5140), b2, b3);
-            mma_f16(acc[2 * e], b0, b1, b2, b3, p0, p1);
-            decode4(__byte_perm(e0[e], e1[e], 0x7362), b0, b1);
-            decode4(__byte_perm(e2[e], e3[e], 0x7362), b2, b3);
-            mma_f16(acc[2 * e + 1], b0, b1, b2, b3, p0, p1);
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int r = 0; r < kRefs; ++r) {
+            float c0[4] = {}, c1[4] = {};
+#pragma unroll
+            for (int ks = r; ks < kBlocks; ks += kRefs) {
+              const uint4 (&x)[4] = xv[ks];
+              uint32_t w4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w4[i] = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+              uint32_t b0, b1, b2, b3;
+              decode4(__byte_perm(w4[0], w4[1], 0x5140), b0, b1);
+              decode4(__byte_perm(w4[2], w4[3], 0x5140), b2, b3);
+              mma_f16(c0, b0, b1, b2, b3, pw[ks][0], pw[ks][1]);
+              decode4(__byte_perm(w4[0], w4[1], 0x7362), b0, b1);
+              decode4(__byte_perm(w4[2], w4[3], 0x7362), b2, b3);
+              mma_f16(c1, b0, b1, b2, b3, pw[ks][0], pw[ks][1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((i & 1) >= NE) continue;
+              acc[2 * e][i] = fmaf(c0[i], to_acc[r][i & 1], acc[2 * e][i]);
+              acc[2 * e + 1][i] = fmaf(c1[i], to_acc[r][i & 1], acc[2 * e + 1][i]);
+            }
           }
         }
       }
@@ -781,17 +812,19 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
       !make_tmap_rows128_3d(&tv, a.c.v_codes, a.c.page, planes, tp, kGroup) ||
       !make_tmap_rows128_3d(&tpe, a.c.k_pe, a.c.page, a.c.n_pages, tp, 1))
     return cudaErrorInvalidValue;
-  const bool one = a.T == 1;
-  auto kern = one ? paged_attn_kernel<true> : paged_attn_kernel<false>;
+  const bool one = a.T == 1, two_pages = a.c.page < kTile / 2;
+  auto kern = one ? (two_pages ? paged_attn_kernel<true, true> : paged_attn_kernel<true, false>)
+                  : (two_pages ? paged_attn_kernel<false, true> : paged_attn_kernel<false, false>);
   constexpr int kMaxDevices = 64;
-  static bool attr_set[kMaxDevices][2] = {};
+  static bool attr_set[kMaxDevices][4] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= kMaxDevices || !attr_set[dev][one]) {
+  const int variant = 2 * one + two_pages;
+  if (dev >= kMaxDevices || !attr_set[dev][variant]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices) attr_set[dev][one] = true;
+    if (dev < kMaxDevices) attr_set[dev][variant] = true;
   }
   // the most tiles that a sequence can have
   long long nt = ((long long)a.P_max + a.T + kTile - 1) / kTile;

@@ -4,11 +4,13 @@ pages whose scale no visible key needs, long contexts of small weights, far posi
 References in 64 bits, from the definitions in include/mla.h.  Tolerances count roundings: a value rounded to nearest
 in bf16 is off by at most 2^-8 of it, in float16 by 2^-11 (eps/2 of the type)."""
 
+import math
+
 import numpy as np
 import pytest
 
 import mla_gb300 as m
-from test_paged import f64, ints, normal
+from test_paged import f64, filled, ints, normal
 
 gpu = pytest.mark.gpu
 
@@ -80,3 +82,131 @@ def test_append_into_pages_of_other_quantizers(gpu_available, page, T, size):
             assert np.array_equal(got[h, :fill], e4m3(before[name][h, :fill] * (s0 / s))), (name, s0, "older codes")
             assert np.array_equal(got[h, fill:fill + n0], e4m3(x[:n0, h] / s)), (name, s0, "new codes")
             assert np.all(got[h, fill + n0:] == 0), "slots behind the last token"
+
+
+# ---- attention -----------------------------------------------------------------------------------------------
+def attend(t, q, P, T=1, window=0, sinks=0):
+    import torch
+    out = torch.full((q.shape[0], q.shape[1] // 192 * 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = m.alloc_workspace(m.MODE_PAGED_ATTN, len(P), T)
+    m.mla_paged_attention(m.make_paged_cache(t), q, ints(P), max(P), out, ws, window=window, sinks=sinks)
+    assert m.mla_device_status(ws) == 0
+    return f64(out).reshape(len(P), T, -1, 128)
+
+
+def check_attention(t, q, P, T=1, window=0, sinks=0, what="", scale=1 / math.sqrt(192), rows=4):
+    """The first `rows` sequences, element by element, with A = sum p |v| of the element (the weights sum to one): the output's own rounding
+    2^-8 |o|; the weights' rounding to float16, 2^-11 A; float32 scores, exponentials and sums, 2^-14 A (scores here
+    stay below 2^7 in log2 units, off by 2^-24 of that a few times over: 2^-15; chains of a few hundred float32 sums:
+    2^-16); weights below 2^-29 of the largest of their 32 keys, 2^-40 of it for each of the 32: 2^-35 p max |v| of
+    its page."""
+    import torch
+    got = attend(t, q, P, T, window, sinks)
+    heads, page = t["k_codes"].shape[1], t["k_codes"].shape[2]
+    table, qn = t["table"].cpu().numpy(), f64(q).reshape(len(P), T, heads, 192)
+    v_all = t["v_codes"].view(torch.float8_e4m3fn)
+    for b, p in enumerate(P[:rows]):
+        for i in range(T):
+            at = p + i
+            j = np.arange(at + 1)
+            if window:
+                j = j[(at - j < window) | (j < sinks)]
+            key, count = np.unique(table[b][j // page].astype(np.int64) * page + j % page, return_counts=True)
+            pid, slot = torch.from_numpy(key // page).cuda(), torch.from_numpy(key % page).cuda()
+            k = f64(t["k_codes"].view(torch.float8_e4m3fn)[pid, :, slot]) * f64(t["k_scales"][pid])[..., None]
+            v = f64(v_all[pid, :, slot]) * f64(t["v_scales"][pid])[..., None]
+            s = (np.einsum("hd,jhd->jh", qn[b, i, :, :128], k) + f64(t["k_pe"][pid, slot]) @ qn[b, i, :, 128:].T) * scale
+            assert np.abs(s).max() / math.log(2) < 2 ** 7, "scores as the bound has them"
+            w = np.exp(s - s.max(0)) * count[:, None]
+            w /= w.sum(0)
+            page_max = np.zeros((int(key.max()) // page + 1, heads))
+            np.maximum.at(page_max, key // page, np.abs(v).max(2))
+            ref, A = np.einsum("jh,jhd->hd", w, v), np.einsum("jh,jhd->hd", w, np.abs(v))
+            low = (w * page_max[key // page]).sum(0)[:, None]
+            bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -14) * A + 2.0 ** -35 * low
+            d = np.abs(got[b, i] - ref)
+            assert np.all(d <= bound), f"{what}: sequence {b} query {i}: {np.max(d / np.maximum(bound, 1e-300)):.3g} of the bound"
+
+
+@gpu
+@pytest.mark.parametrize("page,T", [(16, 1), (16, 4), (32, 1), (64, 3), (128, 1), (128, 8)])
+@pytest.mark.parametrize("up", [0, 20, 24, 30, 60, 100])
+def test_page_scales_that_no_visible_value_needs(gpu_available, page, T, up):
+    """Pages whose value scale is far above their values: all zero, or small. The other pages keep their bits."""
+    import torch
+    P, heads = [700, 45] * 30, 8                  # several tiles a CTA
+    t, _ = filled(P, T, page, heads, 3 + up)
+    for b in range(len(P)):
+        for i, pid in enumerate(t["table"][b].tolist()):
+            if pid >= 0 and i % 2 == 0:
+                t["v_scales"][pid, ::2] *= 2.0 ** up
+                t["v_codes"][pid, ::2] = 0
+            elif pid >= 0 and i % 3 == 0:
+                t["v_scales"][pid, 1::2] *= 2.0 ** -up
+    check_attention(t, normal(5, len(P) * T, heads * 192), P, T, what=f"scales times 2^{up}")
+
+
+@gpu
+@pytest.mark.parametrize("value", [2.0 ** 24, 2.0 ** 50, math.inf])
+def test_a_value_that_the_window_has_passed(gpu_available, value):
+    """A page keeps the scale that an outlier gave it; once the window has passed the outlier, its page and the others
+    answer as if it had not been. The same for a rejected draft that other tokens overwrite."""
+    import torch
+    heads, page, n = 4, 16, 96
+    kv, pe, q = normal(1, n, heads, 256), normal(2, n, 64), normal(3, 1, heads * 192)
+    kv[34, :, 128] = value
+    t = m.alloc_paged_cache(6, page, heads)
+    t["table"] = ints([[2, 0, 1, 5, 3, 4]])
+    ws = m.alloc_workspace(m.MODE_PAGED_APPEND, 1, n)
+
+    def put(at, x, y):
+        m.mla_paged_append(m.make_paged_cache(t), x[..., :128], x[..., 128:], y, ints([at]), x.shape[0], ws)
+        assert m.mla_device_status(ws) == 0
+
+    put(0, kv, pe)
+    check_attention(t, q, [n - 1], window=n - 35, what="behind the window")
+    draft = kv[66:].clone()
+    draft[0, :, 128:] = value
+    put(66, draft, pe[66:])
+    put(66, kv[66:], pe[66:])
+    check_attention(t, q, [n - 1], window=n - 35, what="rejected draft")
+
+
+@gpu
+@pytest.mark.parametrize("page,n,gap", [(128, 1 << 21, 21), (16, 1 << 17, 24), (64, 1 << 20, 33), (32, 5000, 40)])
+def test_many_keys_of_small_weight(gpu_available, page, n, gap):
+    """One key outweighs each other one by 2^gap, and the others are many: together they carry a share of the output
+    that float16 steps of the one key's weight would lose. Their pages are shared, so that the cache stays small."""
+    import torch
+    heads = 4
+    t = m.alloc_paged_cache(3, page, heads)
+    wide = -(-n // page)
+    t["table"] = torch.full((1, wide), 1, dtype=torch.int32, device="cuda")
+    t["table"][0, 0] = 0
+    for name in ("k", "v"):
+        x = normal(4, 3, heads, page, 128, scale=0.25 if name == "k" else 1.0)
+        t[name + "_codes"].copy_(x.to(torch.float8_e4m3fn).view(torch.uint8))
+    t["v_codes"][1] &= 0x7F                       # all of one sign: their sum does not cancel
+    t["v_codes"][0, :, :, :64] = 0
+    q = normal(6, 1, heads * 192, scale=0.25)
+    q[0, 128::192] = 8.0                          # the first rotary value weighs the first key up
+    t["k_pe"][:, :, 0] = 0
+    t["k_pe"][0, 3, 0] = gap * math.log(2) * math.sqrt(192) / 8
+    check_attention(t, q, [n - 1], what=f"{n} keys")
+
+
+@gpu
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("up", [10, 25, 50])
+def test_large_values_of_small_weight(gpu_available, page, up):
+    """A page whose weights are 2^-up of the others' and whose values are 2^up of theirs carries half of the output."""
+    import torch
+    P, heads = [3 * 64 - 1], 4
+    t, _ = filled(P, 1, page, heads, 8, spread=0)
+    low = t["table"][0, 64 // page:128 // page].long()
+    t["v_scales"][low] *= 2.0 ** up
+    q = normal(6, 1, heads * 192, scale=0.25)
+    q[0, 128::192] = 8.0
+    t["k_pe"][:, :, 0] = 0
+    t["k_pe"][low, :, 0] = -up * math.log(2) * math.sqrt(192) / 8
+    check_attention(t, q, P, what=f"2^{up}")
