@@ -550,11 +550,13 @@ __global__ void __launch_bounds__(Shape<WIN>::kThreads, 1)
         const bool need = mx > m + kRescaleThreshold;
         const float m_new = need ? mx : m;
         const float alpha = need ? ex2_approx(m - m_new) : 1.f;
+        // WIN: all that a row sees of its first tiles may score -infinity
+        const float ref = WIN && m_new == -INFINITY ? 0.f : m_new;
         float sp[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kCols; c += 2) {
           float x0, x1;
-          fma_x2(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, -m_new, -m_new);
+          fma_x2(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, -ref, -ref);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
           s[c] = __float_as_uint(p0);
           s[c + 1] = __float_as_uint(p1);
