@@ -781,13 +781,9 @@ int decode_splits(int B, int L, int num_sms) {
 
 cudaError_t launch_decode_attention(const DecodeAttnArgs& a, const DevStatusHost& st, cudaStream_t stream,
                                     int* launches) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(DecodeSmem));
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static PerDevice<bool> allowed;
+  const cudaError_t attr_err = allow_smem(allowed, decode_attn_kernel, sizeof(DecodeSmem));
+  if (attr_err != cudaSuccess) return attr_err;
   const int cl = chunk_len_for(a.L, a.splits, kDecChunk);
   DevStatus dst{st.word, st.wait_limit_ns};
   dim3 grid(a.splits, 64, a.B);
@@ -821,13 +817,9 @@ cudaError_t launch_latent_attention(const LatentAttnArgs& a, const DevStatusHost
       !make_tmap_bf16_3d(&tc, a.ckv, 512, a.L, planes, 1024, (uint64_t)a.cap * 1024, 64, 64) ||
       !make_tmap_bf16_3d(&tr, a.kpe, 64, a.L, planes, 128, (uint64_t)a.cap * 128, 64, 64))
     return cudaErrorInvalidValue;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(latent_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kLatSmemBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static PerDevice<bool> allowed;
+  const cudaError_t attr_err = allow_smem(allowed, latent_attn_tc, kLatSmemBytes);
+  if (attr_err != cudaSuccess) return attr_err;
   DevStatus dst{st.word, st.wait_limit_ns};
   cudaError_t e;
   LatentAttnArgs la = a;

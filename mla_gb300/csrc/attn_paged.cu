@@ -815,17 +815,9 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
   const bool one = a.T == 1, two_pages = a.c.page < kTile / 2;
   auto kern = one ? (two_pages ? paged_attn_kernel<true, true> : paged_attn_kernel<true, false>)
                   : (two_pages ? paged_attn_kernel<false, true> : paged_attn_kernel<false, false>);
-  constexpr int kMaxDevices = 64;
-  static bool attr_set[kMaxDevices][4] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static PerDevice<bool> allowed[2][2];
+  cudaError_t e = allow_smem(allowed[one][two_pages], kern, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int variant = 2 * one + two_pages;
-  if (dev >= kMaxDevices || !attr_set[dev][variant]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices) attr_set[dev][variant] = true;
-  }
   // the most tiles that a sequence can have
   long long nt = ((long long)a.P_max + a.T + kTile - 1) / kTile;
   if (a.window)

@@ -649,12 +649,9 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   auto kern = win ? prefill_attn_tc<true> : prefill_attn_tc<false>;
   const uint32_t smem_bytes = win ? Shape<true>::kSmemBytes : Shape<false>::kSmemBytes;
   const int threads = win ? Shape<true>::kThreads : Shape<false>::kThreads;
-  static bool attr_set[2] = {false, false};
-  if (!attr_set[win]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes);
-    if (e != cudaSuccess) return e;
-    attr_set[win] = true;
-  }
+  static PerDevice<bool> allowed[2];
+  const cudaError_t attr_err = allow_smem(allowed[win], kern, smem_bytes);
+  if (attr_err != cudaSuccess) return attr_err;
   const int n_qt = (a.T + 127) / 128;
   const long long items = (long long)n_qt * 64 * a.B;
   if (items > INT32_MAX || !st.word) return cudaErrorInvalidValue;

@@ -910,27 +910,15 @@ cudaError_t launch_impl(const GemmShape& s, const GemmOperands& op, const EpiArg
     if (!ok) return cudaErrorInvalidValue;
   }
   auto kern = gemm_kernel<BM, BN, STAGES, KSUB, EPI, B_MN, TMA_ST, PAIR>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_clusters = 0;  // pair mode: clusters of 2 that fit at once
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
-    if (attr_err == cudaSuccess && PAIR) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2 * num_sms);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = L::kBytes;
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2;
-      at[0].val.clusterDim.y = 1;
-      at[0].val.clusterDim.z = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      attr_err = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg);
-      if (attr_err == cudaSuccess && max_clusters < 1) attr_err = cudaErrorInvalidConfiguration;
-    }
-  });
+  int max_clusters = 0;  // pair mode: clusters of 2 that fit at once
+  cudaError_t attr_err;
+  if constexpr (PAIR) {
+    static PerDevice<int> known;
+    attr_err = allow_smem_cluster2(known, kern, L::kBytes, kThreads, num_sms, &max_clusters);
+  } else {
+    static PerDevice<bool> allowed;
+    attr_err = allow_smem(allowed, kern, L::kBytes);
+  }
   if (attr_err != cudaSuccess) return attr_err;
   GemmShape sh = s;
   if (sh.raster_g < 1) sh.raster_g = 1;
@@ -1226,26 +1214,9 @@ cudaError_t launch_resb_pair(const GemmShape& s, const GemmOperands& op, const E
   }
   if (!ok) return cudaErrorInvalidValue;
   auto kern = gemm_resb_pair_kernel<EPI>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_clusters = 0;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
-    if (attr_err != cudaSuccess) return;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * num_sms);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::kBytes;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    attr_err = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg);
-    if (attr_err == cudaSuccess && max_clusters < 1) attr_err = cudaErrorInvalidConfiguration;
-  });
+  static PerDevice<int> known;
+  int max_clusters = 0;
+  const cudaError_t attr_err = allow_smem_cluster2(known, kern, L::kBytes, kThreads, num_sms, &max_clusters);
   if (attr_err != cudaSuccess) return attr_err;
   // row-pair groups: about six units per cluster, at least 4 tiles per unit
   const int m_pairs = s.M / 256, n_tiles = s.N / BN;
@@ -1651,11 +1622,8 @@ cudaError_t launch_w8_impl(const GemmShape& s, const GemmW8Operands& op, const E
   CUtensorMap ta;
   if (!make_tmap_bf16_2d(&ta, op.A, op.a_rows, (uint64_t)op.lda, op.lda, BM, 64)) return cudaErrorInvalidValue;
   auto kern = gemm_w8_kernel<BM, BN, SA, SF, EPI>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
-  });
+  static PerDevice<bool> allowed;
+  const cudaError_t attr_err = allow_smem(allowed, kern, L::kBytes);
   if (attr_err != cudaSuccess) return attr_err;
   GemmShape sh = s;
   if (sh.raster_g < 1) sh.raster_g = 1;

@@ -9,7 +9,46 @@
 
 #include <utility>
 
+#include "per_device.h"
+
 namespace mla {
+
+// Lets `kern` take `smem` bytes of dynamic shared memory on the current
+// device: set by the kernel's first launch on each device.
+template <typename... KArgs>
+cudaError_t allow_smem(PerDevice<bool>& allowed, void (*kern)(KArgs...), size_t smem) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  bool done = false;
+  return e != cudaSuccess ? e : allowed.get(dev, done, [&](bool&) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+}
+
+// The same, and *n = clusters of two CTAs that fit on the current device at once.
+template <typename... KArgs>
+cudaError_t allow_smem_cluster2(PerDevice<int>& known, void (*kern)(KArgs...), size_t smem, int threads, int num_sms,
+                                int* n) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : known.get(dev, *n, [&](int& max_clusters) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * num_sms);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t asked = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg);
+    return asked == cudaSuccess && max_clusters < 1 ? cudaErrorInvalidConfiguration : asked;
+  });
+}
 
 // Launch with programmatic stream serialization (see pdl_wait in common.cuh).
 template <typename... KArgs, typename... Args>
