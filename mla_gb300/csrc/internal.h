@@ -348,7 +348,8 @@ struct PagedCache {
 // leave that number zero.
 constexpr int kStatusExtraWord = 1;
 constexpr int kStatusExtraFirst = 64;
-constexpr int kMaxStatusExtra = 1024;
+constexpr int kPagedMaxCtas = 256;
+constexpr int kMaxStatusExtra = kPagedMaxCtas;
 
 struct PagedAppendArgs {
   PagedCache c;
@@ -398,7 +399,6 @@ struct PagedAttnArgs {
   float2* part_ml;             // [2 * kPagedMaxCtas][T][4 heads]
   int* first_unit;             // [B + 1]: units of work of the sequences before b, one head group
 };
-constexpr int kPagedMaxCtas = 256;
 constexpr int kPagedMaxT = 8;
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream,
                                    int* launches);

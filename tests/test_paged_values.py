@@ -210,3 +210,21 @@ def test_large_values_of_small_weight(gpu_available, page, up):
     t["k_pe"][:, :, 0] = 0
     t["k_pe"][low, :, 0] = -up * math.log(2) * math.sqrt(192) / 8
     check_attention(t, q, P, what=f"2^{up}")
+
+
+# ---- the status word -----------------------------------------------------------------------------------------
+@gpu
+def test_status_words_end_inside_the_status_region(gpu_available):
+    """A workspace that no call has written may hold any count of further status words: no more are read than a call
+    writes, one for each of at most 256 thread blocks."""
+    import torch
+    ws = torch.zeros(8192, dtype=torch.uint8, device="cuda")
+    words = ws.view(torch.int32)
+    words[64 + 256:] = -1
+    for count in (0, 1, 256, 257, 400, 960, 961, 1024, 1025, -1, 2 ** 31 - 1):
+        words[1] = count
+        assert m.mla_device_status(ws) == 0, count
+    words[1], words[64 + 255] = 256, -1
+    assert m.mla_device_status(ws) != 0
+    words[1] = 255
+    assert m.mla_device_status(ws) == 0
