@@ -465,9 +465,10 @@ typedef struct {
  * max_pages * page or a page number outside [0, n_pages) cannot be checked on
  * the host: the kernel skips that sequence (or page) and mla_device_status
  * then returns MLA_ERR_INVALID_ARG.
- * Errors: INVALID_ARG (null pointer, B, T or N < 1, N > 2^24, N < B * T
- * without cu, a stride not a multiple of 8 or below 0), UNSUPPORTED (page,
- * heads), ALIGNMENT, WORKSPACE, CUDA. */
+ * Errors: INVALID_ARG (null pointer, B, T or N < 1, B or N > 2^24, T > 2^30,
+ * N < B * T without cu, B times the pages that T tokens touch >= 2^31, a stride
+ * not a multiple of 8 or below 0), UNSUPPORTED (page, heads), ALIGNMENT,
+ * WORKSPACE, CUDA. */
 int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params, const void* k, long long k_token,
                      long long k_head, const void* v, long long v_token, long long v_head, const void* k_pe,
                      long long pe_token, const int* P, const int* cu, int B, int T, int N, void* workspace,

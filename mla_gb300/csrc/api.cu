@@ -14,6 +14,8 @@ namespace {
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kMaxSmsForSizing = 256;                     // workspace upper bound
 constexpr int64_t kMaxTokens = 1 << 24;
+// positions of a paged sequence: positions and a call's tokens behind them stay in 31 bits
+constexpr int kMaxPagedPositions = 1 << 30;
 
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -476,7 +478,9 @@ size_t mla_workspace_size(int mode, int B, int t_or_p, int cap) {
   } else if (mode == MLA_MODE_CHUNK_ABSORBED) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens || cap < t_or_p || cap >= (1 << 24)) return 0;
   } else if (mode == MLA_MODE_FOLD) {
-  } else if (mode == MLA_MODE_PAGED_APPEND || mode == MLA_MODE_WINDOW_ATTN) {
+  } else if (mode == MLA_MODE_PAGED_APPEND) {
+    if (t_or_p < 1 || t_or_p > kMaxPagedPositions || B > kMaxTokens) return 0;
+  } else if (mode == MLA_MODE_WINDOW_ATTN) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
   } else if (mode == MLA_MODE_PAGED_ATTN) {
     if (t_or_p < 1 || t_or_p > kPagedMaxT || B > kMaxTokens) return 0;
@@ -1073,7 +1077,7 @@ int check_cache(const mla_paged_cache_t* c) {
   if (c->heads < 4 || c->heads > 128 || c->heads % 4) return MLA_ERR_UNSUPPORTED;
   // (a position, a call's tokens and a page behind them stay in 31 bits)
   if ((int64_t)c->n_pages * c->heads > INT32_MAX || (int64_t)c->n_pages * c->page > INT32_MAX ||
-      (int64_t)c->max_pages * c->page > (int64_t)1 << 30)
+      (int64_t)c->max_pages * c->page > kMaxPagedPositions)
     return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
@@ -1117,9 +1121,10 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
   if (rc) return rc;
   const Params p = resolve(params);
   if (!params_ok(p)) return MLA_ERR_INVALID_ARG;
-  if (!k || !v || !k_pe || !P || B < 1 || T < 1 || N < 1 || N > kMaxTokens || (int64_t)B * T > kMaxTokens)
+  if (!k || !v || !k_pe || !P || B < 1 || B > kMaxTokens || T < 1 || T > kMaxPagedPositions || N < 1 || N > kMaxTokens)
     return MLA_ERR_INVALID_ARG;
   if (!cu && (int64_t)B * T > N) return MLA_ERR_INVALID_ARG;
+  if ((int64_t)B * paged_append_pages(T, cache->page) > INT32_MAX) return MLA_ERR_INVALID_ARG;
   for (long long s : {k_token, k_head, v_token, v_head, pe_token})
     if (!good_stride(s)) return MLA_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_pe) || (reinterpret_cast<uintptr_t>(P) & 3) ||

@@ -371,6 +371,8 @@ struct PagedAppendArgs {
   bool status_cleared;         // the caller cleared the status region: OR into it
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+// Pages that T tokens of one sequence may touch, wherever they begin; times B at most INT32_MAX.
+inline int paged_append_pages(int T, int page) { return (T - 1 + page - 1) / page + 1; }
 
 // Positions of the dense caches K [B, heads, cap, 192], V [B, heads, cap, 128]
 // filled with the paged ones' values (code * scale in bf16, exact where the scale

@@ -289,7 +289,7 @@ cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-  const int pages_per_seq = (a.T - 1 + a.c.page - 1) / a.c.page + 1;
+  const int pages_per_seq = paged_append_pages(a.T, a.c.page);
   // 8 tokens a warp: one warp per head for a few new tokens, else page / 8
   const int w_log = a.T <= 8 ? 0 : a.c.page == 16 ? 1 : a.c.page == 32 ? 2 : a.c.page == 64 ? 3 : 4;
   const int W = 1 << w_log, warps = W > 8 ? W : 8;

@@ -228,3 +228,54 @@ def test_status_words_end_inside_the_status_region(gpu_available):
     assert m.mla_device_status(ws) != 0
     words[1] = 255
     assert m.mla_device_status(ws) == 0
+
+
+# ---- far positions and long, ragged batches ------------------------------------------------------------------
+def test_sizes_of_an_append_that_are_taken_and_refused():
+    """What mla.h states: 2^24 rows and sequences, T up to 2^30, counts of pages in 31 bits. A call that passes these
+    checks meets the next one here, on its workspace (-3): nothing is enqueued."""
+    from test_paged import append, fake_cache, FAKE
+    far = fake_cache(max_pages=1 << 23, page=128, heads=4)
+    assert m.workspace_size(m.MODE_PAGED_APPEND, 600, 32768) > 0
+    assert append(far, B=600, T=32768, N=40000, cu=FAKE + 16384, wsb=16) == -3
+    assert append(far, B=600, T=32768, N=40000, wsb=16) == -1
+    assert append(far, B=2, T=(1 << 30) + 1, N=7, cu=FAKE + 16384, wsb=16) == -1
+    assert append(far, B=(1 << 24) + 1, T=1, N=7, cu=FAKE + 16384, wsb=16) == -1
+    assert append(far, B=1 << 20, T=1 << 20, N=7, cu=FAKE + 16384, wsb=16) == -1
+
+
+@gpu
+def test_one_long_prompt_among_many_sequences(gpu_available):
+    """600 sequences of which one brings 3,000 tokens and the others one each, with room for 32,768: more than 2^24
+    tokens by their bound, 3,599 rows. The same pages as from two calls with close bounds."""
+    import torch
+    heads, page, B, n = 4, 64, 600, 3000
+    counts = [1] * B
+    counts[411] = n
+    cu = np.cumsum([0] + counts)
+    P = [(7 * b) % 100 for b in range(B)]
+    P[411] = 5
+    pages = [(p + c - 1) // page + 1 for p, c in zip(P, counts)]
+    first = np.cumsum([0] + pages)
+    table = torch.full((B, max(pages)), -1, dtype=torch.int32)
+    for b in range(B):
+        table[b, :pages[b]] = torch.arange(int(first[b]), int(first[b + 1]))
+    N = int(cu[-1])
+    kv, pe = normal(1, N, heads, 256), normal(2, N, 64)
+    worlds = []
+    for split in (False, True):
+        t = m.alloc_paged_cache(int(first[-1]), page, heads)
+        t["table"] = table.cuda()
+        cache = m.make_paged_cache(t)
+        for T, mine in (((32768, range(B)),) if not split else ((n, [411]), (1, [b for b in range(B) if b != 411]))):
+            ws = m.alloc_workspace(m.MODE_PAGED_APPEND, B, T)
+            now = [P[b] if b in set(mine) else -1 for b in range(B)]
+            k = [counts[b] if b in set(mine) else 0 for b in range(B)]
+            rows = np.concatenate([np.arange(cu[b], cu[b + 1]) for b in mine])
+            r = torch.from_numpy(rows).cuda()
+            m.mla_paged_append(cache, kv[r][..., :128], kv[r][..., 128:], pe[r], ints(now), T, ws,
+                               cu=ints(list(np.cumsum([0] + k))))
+            assert m.mla_device_status(ws) == 0
+        worlds.append(t)
+    for name in m.PAGED_TENSORS:
+        assert torch.equal(worlds[0][name], worlds[1][name]), name
