@@ -486,7 +486,8 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
  *            multiple of 8, >= heads * 128
  *   P        int [B] in DEVICE memory, -1 .. P_max; P[b] = -1 marks an idle
  *            sequence (its output rows are zeros).  P_max sizes the launch;
- *            P_max + T <= max_pages * page.
+ *            P_max + T <= max_pages * page.  A query sees at most 2^24 keys:
+ *            P_max + T, or window + T - 1 + sinks, is at most that
  *   window   0 = every key; sinks is then ignored
  *   params   softmax_scale (the others are not used)
  *   workspace mla_workspace_size(MLA_MODE_PAGED_ATTN, B, T, 0); not shared by
@@ -504,9 +505,10 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
  * A P[b] outside [-1, P_max] is taken as idle, a page number outside
  * [0, n_pages) is clamped, and mla_device_status then returns
  * MLA_ERR_INVALID_ARG.
- * Errors: INVALID_ARG (null pointer, B or T < 1, P_max < 0, P_max + T >
- * max_pages * page, window or sinks < 0, row strides), UNSUPPORTED (T > 8,
- * page, heads), ALIGNMENT, WORKSPACE, CUDA. */
+ * Errors: INVALID_ARG (null pointer, B < 1 or > 2^24, T < 1, P_max < 0, P_max +
+ * T > max_pages * page, more than 2^24 keys, B times the tiles of 64 keys that
+ * a sequence may take >= 2^31, window or sinks < 0, row strides), UNSUPPORTED
+ * (T > 8, page, heads), ALIGNMENT, WORKSPACE, CUDA. */
 int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* params, const void* q, long long q_row,
                         int B, int T, const int* P, int P_max, int window, int sinks, void* out, long long out_row,
                         void* workspace, size_t workspace_bytes, void* stream);
@@ -525,7 +527,8 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
  * A NaN among a key's values may also reach queries that do not see the key
  * but share a tile with one that does (weight zero times NaN): those less than
  * 256 positions short of it, or past the end of its window.
- * Errors: INVALID_ARG (null pointer, sizes), ALIGNMENT, WORKSPACE, CUDA. */
+ * Errors: INVALID_ARG (null pointer, sizes, B * T > 2^24), ALIGNMENT,
+ * WORKSPACE, CUDA. */
 int mla_window_attention(const mla_params_t* params, const void* q, int B, int T, int P0, const void* k_cache,
                          const void* v_cache, int cap, int window, int sinks, void* out, void* workspace,
                          size_t workspace_bytes, void* stream);
@@ -536,7 +539,8 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
  * T = 1, its own key as the cache holds it), window and sinks as there.
  *   x, out   [B, 7168]      (out may alias x exactly); idle rows (P[b] = -1)
  *                           append nothing and get out = x
- *   P        int [B] in DEVICE memory, -1 .. P_max; P_max + 1 <= max_pages * page
+ *   P        int [B] in DEVICE memory, -1 .. P_max; P_max + 1 <= max_pages * page,
+ *            and the bounds on keys and tiles of mla_paged_attention
  *   workspace mla_workspace_size(MLA_MODE_DECODE_PAGED, B, P_max, 0)
  * The kv_b product is rounded to bf16 before it is quantized.
  * Errors: those of mla_decode_varlen and of the cache (UNSUPPORTED unless
@@ -554,7 +558,8 @@ int mla_decode_paged(const mla_weights_t* w, const mla_params_t* params, const v
  * the out of mla_prefill.
  *   x, out   [B, T, 7168]  (out may alias x exactly)
  *   workspace mla_workspace_size(MLA_MODE_PREFILL_PAGED, B, T, P0 + T)
- * Requires P0 >= 0 and P0 + T <= max_pages * page.
+ * Requires P0 >= 0, P0 + T <= max_pages * page, B * T <= 2^24 and
+ * B * (P0 + T) <= 2^26 (the workspace holds those positions in bf16).
  * Errors: INVALID_ARG, UNSUPPORTED (cache), ALIGNMENT, WORKSPACE, CUDA. */
 int mla_prefill_paged(const mla_weights_t* w, const mla_params_t* params, const void* x, int B, int T, int P0,
                       const mla_paged_cache_t* cache, int window, int sinks, void* out, void* workspace,

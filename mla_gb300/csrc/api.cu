@@ -8,6 +8,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 namespace mla {
 namespace {
 
@@ -471,8 +473,10 @@ size_t mla_workspace_size(int mode, int B, int t_or_p, int cap) {
   } else if (mode == MLA_MODE_CHUNK_LATENT || mode == MLA_MODE_PREFILL_PAGED) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens || cap < t_or_p || (int64_t)B * cap > (int64_t)1 << 26)
       return 0;
-  } else if (mode == MLA_MODE_DECODE || mode == MLA_MODE_DECODE_LATENT || mode == MLA_MODE_DECODE_PAGED) {
+  } else if (mode == MLA_MODE_DECODE || mode == MLA_MODE_DECODE_LATENT) {
     if (t_or_p < 0 || B > kMaxTokens || t_or_p >= (1 << 24)) return 0;
+  } else if (mode == MLA_MODE_DECODE_PAGED) {
+    if (t_or_p < 0 || B > kMaxTokens || t_or_p >= kMaxPagedPositions) return 0;
   } else if (mode == MLA_MODE_FFN) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
   } else if (mode == MLA_MODE_CHUNK_ABSORBED) {
@@ -1106,6 +1110,17 @@ void rope_frequencies(float base, double (&f)[32]) {
   memcpy(f, theta, sizeof(theta));
 }
 
+// Whether the attention of T queries per sequence, positions up to
+// P_max + T - 1, is inside the table, sees at most 2^24 keys (float32 sums of
+// more would lose what the output keeps) and counts its tiles in 31 bits.
+bool good_reach(const mla_paged_cache_t* c, int B, int T, int P_max, int window, int sinks) {
+  if ((int64_t)P_max + T > (int64_t)c->max_pages * c->page) return false;
+  int64_t keys = (int64_t)P_max + T;
+  if (window) keys = std::min<int64_t>(keys, (int64_t)window + T - 1 + sinks);
+  return keys <= (1 << 24) && (paged_attention_tiles(P_max, T, window, sinks) + 1) * B <= INT32_MAX &&
+         (int64_t)B * (c->heads / 4) <= INT32_MAX;
+}
+
 // strides in elements whose rows stay 16-byte aligned
 bool good_stride(long long s) { return s >= 0 && s % 8 == 0; }
 
@@ -1163,8 +1178,7 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
   if (!q || !out || !P || B < 1 || B > kMaxTokens || T < 1 || P_max < 0 || window < 0 || sinks < 0)
     return MLA_ERR_INVALID_ARG;
   if (T > kPagedMaxT) return MLA_ERR_UNSUPPORTED;
-  if ((int64_t)P_max + T > (int64_t)cache->max_pages * cache->page || (int64_t)P_max + T > (1 << 24))
-    return MLA_ERR_INVALID_ARG;
+  if (!good_reach(cache, B, T, P_max, window, sinks)) return MLA_ERR_INVALID_ARG;
   if (!good_stride(q_row) || q_row < cache->heads * MLA_QK || !good_stride(out_row) ||
       out_row < cache->heads * MLA_V)
     return MLA_ERR_INVALID_ARG;
@@ -1271,8 +1285,8 @@ int mla_decode_paged(const mla_weights_t* w, const mla_params_t* params, const v
   int rc = check_cache(cache);
   if (rc) return rc;
   if (cache->heads != MLA_HEADS) return MLA_ERR_UNSUPPORTED;
-  if (!P || B < 1 || B > kMaxTokens || P_max < 0 || P_max >= (1 << 24) || window < 0 || sinks < 0 ||
-      (int64_t)P_max + 1 > (int64_t)cache->max_pages * cache->page)
+  if (!P || B < 1 || B > kMaxTokens || P_max < 0 || window < 0 || sinks < 0 ||
+      !good_reach(cache, B, 1, P_max, window, sinks))
     return MLA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(P) & 3) return MLA_ERR_ALIGNMENT;
   rc = common_checks(w, p, x, out, (size_t)B, workspace, workspace_bytes,

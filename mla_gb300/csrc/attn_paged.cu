@@ -818,11 +818,9 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& 
   static PerDevice<bool> allowed[2][2];
   cudaError_t e = allow_smem(allowed[one][two_pages], kern, kSmemBytes);
   if (e != cudaSuccess) return e;
-  // the most tiles that a sequence can have
-  long long nt = ((long long)a.P_max + a.T + kTile - 1) / kTile;
-  if (a.window)
-    nt = std::min(nt, ((long long)a.window + a.T - 2) / kTile + 2 + ((long long)a.sinks + kTile - 1) / kTile);
+  const long long nt = paged_attention_tiles(a.P_max, a.T, a.window, a.sinks);
   const long long most = nt * a.B * (a.c.heads / kGroup);
+  static_assert(kTile == 64 && kPieceCost == 1, "the host's count of tiles");
   if ((nt + kPieceCost) * a.B > INT32_MAX || (long long)a.B * (a.c.heads / kGroup) > INT32_MAX) return cudaErrorInvalidValue;
   const int C = (int)std::min<long long>(most, std::min(num_sms, kPagedMaxCtas));
   e = launch_pdl(kern, dim3(C), dim3(kThreads), kSmemBytes, stream, tk, tv, tpe, a, st.wait_limit_ns);

@@ -402,6 +402,13 @@ struct PagedAttnArgs {
   int* first_unit;             // [B + 1]: units of work of the sequences before b, one head group
 };
 constexpr int kPagedMaxT = 8;
+// The most tiles of 64 keys that a sequence can have, plus one times B at most INT32_MAX.
+inline long long paged_attention_tiles(int P_max, int T, int window, int sinks) {
+  const long long all = ((long long)P_max + T + 63) / 64;
+  if (!window) return all;
+  const long long seen = ((long long)window + T - 2) / 64 + 2 + ((long long)sinks + 63) / 64;
+  return seen < all ? seen : all;
+}
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream,
                                    int* launches);
 

@@ -4,6 +4,7 @@ pages whose scale no visible key needs, long contexts of small weights, far posi
 References in 64 bits, from the definitions in include/mla.h.  Tolerances count roundings: a value rounded to nearest
 in bf16 is off by at most 2^-8 of it, in float16 by 2^-11 (eps/2 of the type)."""
 
+import ctypes
 import math
 
 import numpy as np
@@ -94,12 +95,12 @@ def attend(t, q, P, T=1, window=0, sinks=0):
     return f64(out).reshape(len(P), T, -1, 128)
 
 
-def check_attention(t, q, P, T=1, window=0, sinks=0, what="", scale=1 / math.sqrt(192), rows=4):
-    """The first `rows` sequences, element by element, with A = sum p |v| of the element (the weights sum to one): the output's own rounding
-    2^-8 |o|; the weights' rounding to float16, 2^-11 A; float32 scores, exponentials and sums, 2^-14 A (scores here
-    stay below 2^7 in log2 units, off by 2^-24 of that a few times over: 2^-15; chains of a few hundred float32 sums:
-    2^-16); weights below 2^-29 of the largest of their 32 keys, 2^-40 of it for each of the 32: 2^-35 p max |v| of
-    its page."""
+def check_attention(t, q, P, T=1, window=0, sinks=0, what="", scale=1 / math.sqrt(192), rows=4, sums=2.0 ** -14):
+    """The first `rows` sequences, element by element, with A = sum p |v| of the element (the weights sum to one): the
+    output's own rounding 2^-8 |o|; the weights' rounding to float16, 2^-11 A; float32 scores, exponentials and sums,
+    2^-14 A (scores here stay below 2^7 in log2 units, off by 2^-24 of that a few times over: 2^-15; chains of a few
+    hundred float32 sums: 2^-16); weights below 2^-29 of the largest of their 32 keys, 2^-40 of it for each of the 32:
+    2^-35 p max |v| of its page."""
     import torch
     got = attend(t, q, P, T, window, sinks)
     heads, page = t["k_codes"].shape[1], t["k_codes"].shape[2]
@@ -123,7 +124,7 @@ def check_attention(t, q, P, T=1, window=0, sinks=0, what="", scale=1 / math.sqr
             np.maximum.at(page_max, key // page, np.abs(v).max(2))
             ref, A = np.einsum("jh,jhd->hd", w, v), np.einsum("jh,jhd->hd", w, np.abs(v))
             low = (w * page_max[key // page]).sum(0)[:, None]
-            bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -14) * A + 2.0 ** -35 * low
+            bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + sums) * A + 2.0 ** -35 * low
             d = np.abs(got[b, i] - ref)
             assert np.all(d <= bound), f"{what}: sequence {b} query {i}: {np.max(d / np.maximum(bound, 1e-300)):.3g} of the bound"
 
@@ -173,7 +174,8 @@ def test_a_value_that_the_window_has_passed(gpu_available, value):
 
 
 @gpu
-@pytest.mark.parametrize("page,n,gap", [(128, 1 << 21, 21), (16, 1 << 17, 24), (64, 1 << 20, 33), (32, 5000, 40)])
+@pytest.mark.parametrize("page,n,gap", [(128, 1 << 21, 21), (16, 1 << 17, 24), (64, 1 << 20, 33), (32, 5000, 40),
+                                        (128, 1 << 24, 30)])
 def test_many_keys_of_small_weight(gpu_available, page, n, gap):
     """One key outweighs each other one by 2^gap, and the others are many: together they carry a share of the output
     that float16 steps of the one key's weight would lose. Their pages are shared, so that the cache stays small."""
@@ -192,7 +194,9 @@ def test_many_keys_of_small_weight(gpu_available, page, n, gap):
     q[0, 128::192] = 8.0                          # the first rotary value weighs the first key up
     t["k_pe"][:, :, 0] = 0
     t["k_pe"][0, 3, 0] = gap * math.log(2) * math.sqrt(192) / 8
-    check_attention(t, q, [n - 1], what=f"{n} keys")
+    # 2^24 keys are 2^18 tiles, 1,725 a thread block: as many sums in a row for O and twice as many for the weights'
+    # total, each off by up to 2^-24: 2^-11.6
+    check_attention(t, q, [n - 1], what=f"{n} keys", **(dict(sums=2.0 ** -11.5) if n > 1 << 21 else {}))
 
 
 @gpu
@@ -242,6 +246,102 @@ def test_sizes_of_an_append_that_are_taken_and_refused():
     assert append(far, B=2, T=(1 << 30) + 1, N=7, cu=FAKE + 16384, wsb=16) == -1
     assert append(far, B=(1 << 24) + 1, T=1, N=7, cu=FAKE + 16384, wsb=16) == -1
     assert append(far, B=1 << 20, T=1 << 20, N=7, cu=FAKE + 16384, wsb=16) == -1
+
+
+def test_reaches_that_are_taken_and_refused():
+    """What mla.h states: positions up to 2^30, 2^24 visible keys, counts of tiles in 31 bits; else as above."""
+    from test_paged import attend, fake_cache, FAKE
+    from test_paged_sublayer import fake_weights
+    far = fake_cache(max_pages=1 << 23, page=128, heads=4)
+    assert attend(far, P_max=(1 << 24) - 1, wsb=16) == -3 and attend(far, P_max=1 << 24, wsb=16) == -1
+    assert attend(far, P_max=(1 << 30) - 1, window=1 << 20, sinks=4, wsb=16) == -3
+    assert attend(far, P_max=(1 << 30) - 1, window=(1 << 24) - 4, sinks=4, wsb=16) == -3
+    assert attend(far, P_max=(1 << 30) - 1, window=(1 << 24) - 3, sinks=4, wsb=16) == -1
+    assert attend(far, P_max=1 << 30, window=1 << 20, wsb=16) == -1
+    assert attend(far, P_max=(1 << 24) - 1, B=(1 << 13) - 1, wsb=16) == -3
+    assert attend(far, P_max=(1 << 24) - 1, B=1 << 13, wsb=16) == -1
+    assert m.workspace_size(m.MODE_DECODE_PAGED, 2, (1 << 30) - 1) > 0
+    L, w, c = m.lib(), fake_weights(), fake_cache(max_pages=1 << 23, page=128)
+
+    def dec(P_max, window):
+        return L.mla_decode_paged(ctypes.byref(w), None, FAKE + (1 << 30), 2, FAKE, P_max, ctypes.byref(c), window, 4,
+                                  FAKE + (2 << 30), FAKE + (3 << 30), 64, None)
+
+    assert dec((1 << 30) - 1, 4096) == -3 and dec((1 << 24) - 1, 0) == -3
+    assert dec(1 << 24, 0) == -1 and dec(1 << 30, 4096) == -1
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 3])
+def test_window_at_positions_past_24_bits(gpu_available, T):
+    """Tokens appended and attended to around positions 2^24, 2^25 and 2^30, under a window with sinks: the pages
+    in between are not there."""
+    import torch
+    heads, page, n = 4, 128, 300
+    ends = [2 ** 25 + 77, 2 ** 24 + 5, 2 ** 30 - 128]
+    wide = 2 ** 30 // page
+    t = m.alloc_paged_cache(16, page, heads)
+    table = torch.full((3, wide), -1, dtype=torch.int32)
+    at = 0
+    for b, e in enumerate(ends):
+        for pi in [0] + list(range((e - n) // page, (e + T - 1) // page + 1)):
+            table[b, pi] = at
+            at += 1
+    assert at <= 16
+    t["table"] = table.cuda()
+    ws = m.alloc_workspace(m.MODE_PAGED_APPEND, 3, n + T)
+    for P, count, seed in (([0] * 3, 5, 1), ([e - n for e in ends], n + T, 2)):
+        kv, pe = normal(seed, 3 * count, heads, 256), normal(seed + 5, 3 * count, 64)
+        m.mla_paged_append(m.make_paged_cache(t), kv[..., :128], kv[..., 128:], pe, ints(P), count, ws)
+        assert m.mla_device_status(ws) == 0
+    theta = 10000.0 ** (-np.arange(32) / 32.0)
+    x, keys = f64(pe).reshape(3, n + T, 64), f64(t["k_pe"])
+    for b, e in enumerate(ends):                  # the last position of each: rotated by its angle
+        pos = e + T - 1
+        x1, x2, got = x[b, -1, :32], x[b, -1, 32:], keys[int(table[b, pos // page]), pos % page]
+        want = np.concatenate([x1 * np.cos(pos * theta) - x2 * np.sin(pos * theta),
+                               x2 * np.cos(pos * theta) + x1 * np.sin(pos * theta)])
+        # 2^-8 of the value, 2^-20 of its parts, and the angle's own rounding, 2^-53 of up to 2^30, twice (here and there)
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -20 + 2.0 ** -21) * np.tile(np.abs(x1) + np.abs(x2), 2))
+    q = normal(9, 3 * T, heads * 192)
+    for window, sinks in ((200, 5), (64, 0), (1, 1)):
+        got = attend(t, q, ends, T, window, sinks)
+        # the same keys and values at small positions: pages in the order in which they are seen, the mask by hand
+        for b, e in enumerate(ends):
+            for i in range(T):
+                pos = e + i
+                j = np.concatenate([np.arange(sinks), np.arange(pos - window + 1, pos + 1)])
+                pid, slot = t["table"][b][torch.from_numpy(j // page).cuda()].long(), torch.from_numpy(j % page).cuda()
+                k = f64(t["k_codes"].view(torch.float8_e4m3fn)[pid, :, slot]) * f64(t["k_scales"][pid])[..., None]
+                v = f64(t["v_codes"].view(torch.float8_e4m3fn)[pid, :, slot]) * f64(t["v_scales"][pid])[..., None]
+                qn = f64(q).reshape(3, T, heads, 192)[b, i]
+                s = np.einsum("hd,jhd->jh", qn[:, :128], k) + f64(t["k_pe"][pid, slot]) @ qn[:, 128:].T
+                w = np.exp((s - s.max(0)) / math.sqrt(192))
+                w /= w.sum(0)
+                ref, A = np.einsum("jh,jhd->hd", w, v), np.einsum("jh,jhd->hd", w, np.abs(v))
+                assert np.all(np.abs(got[b, i] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -14) * A), (b, i, window)
+
+
+@gpu
+def test_decode_step_at_positions_past_24_bits(gpu_available):
+    """The sublayer's step depends on differences of positions only: the same tokens, under a window, from position 70
+    and from 2^25 + 70 on."""
+    import torch
+    from mla_testlib import cuda_to_f64, cuda_weights, parity_out
+    W, page, steps, outs = m.make_weights(cuda_weights(0)), 64, 6, []
+    xs = normal(4, steps, 2, 7168)
+    for base in (0, 2 ** 25):
+        t = m.alloc_paged_cache(4, page)
+        t["table"] = torch.full((2, base // page + 2), -1, dtype=torch.int32, device="cuda")
+        t["table"][:, base // page:] = ints([[0, 1], [2, 3]])
+        cache, ws = m.make_paged_cache(t), m.alloc_workspace(m.MODE_DECODE_PAGED, 2, base + 100)
+        for i in range(steps):
+            out = torch.empty_like(xs[i])
+            m.mla_decode_paged(W, xs[i], ints([base + 70 + i] * 2), base + 100, cache, out, ws, window=3)
+            assert m.mla_device_status(ws) == 0
+            outs.append(cuda_to_f64(out))
+    for i in range(steps):
+        parity_out(outs[steps + i], outs[i], f"step {i}")
 
 
 @gpu
