@@ -387,6 +387,8 @@ def make_paged_cache(t: dict) -> MlaPagedCache:
                 (tuple(x.shape) != shapes[n] if n != "table" else x.dim() != 2) or x.device != t["k_codes"].device:
             raise ValueError(f"paged cache {n}: need a contiguous {dtypes[n]} CUDA tensor of shape "
                              f"{shapes.get(n, '[B, max_pages]')} on one device")
+    if not t["table"].numel():
+        raise ValueError("paged cache table: need at least one sequence and one page")
     s = MlaPagedCache(*[t[n].data_ptr() for n in PAGED_TENSORS], t["table"].data_ptr(), n_pages, t["table"].shape[1],
                       page, heads)
     s._keep = dict(t)

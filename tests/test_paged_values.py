@@ -216,6 +216,17 @@ def test_large_values_of_small_weight(gpu_available, page, up):
     check_attention(t, q, P, what=f"2^{up}")
 
 
+# ---- the binding ---------------------------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("shape", [(0, 4), (2, 0), (0, 0)])
+def test_tables_without_entries_are_refused(gpu_available, shape):
+    import torch
+    t = m.alloc_paged_cache(2, 16, 4)
+    t["table"] = torch.zeros(shape, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="at least one"):
+        m.make_paged_cache(t)
+
+
 # ---- the status word -----------------------------------------------------------------------------------------
 @gpu
 def test_status_words_end_inside_the_status_region(gpu_available):
