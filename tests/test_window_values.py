@@ -45,3 +45,33 @@ def test_scores_of_minus_infinity(gpu_available, T, P0, window, sinks, keys):
         ref, A = w @ vh, w @ np.abs(vh)
         d = np.abs(got[some, h] - ref)
         assert np.all(d <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -14) * A), (h, np.nanmax(d))
+
+
+@gpu
+@pytest.mark.parametrize("B,T,P0,page", [(2, 300, 0, 64), (1, 200, 150, 16)])
+def test_window_that_holds_every_key_against_the_causal_kernel(gpu_available, B, T, P0, page):
+    """mla_prefill_paged without a window runs the causal kernel; under a window of every key it runs the windowed one,
+    which sums a row in two halves: the same output within the sublayer's bounds, and the same pages."""
+    import torch
+    from mla_testlib import cuda_to_f64, cuda_weights, parity, parity_out
+    W, outs, deltas, pages = m.make_weights(cuda_weights(0)), [], [], []
+    x0, x = normal(1, B, max(P0, 1), 7168), normal(2, B, T, 7168)
+    n = -(-(P0 + T) // page)
+    for window, sinks in ((0, 0), (P0 + T, 0), (3, P0 + T)):
+        t = m.alloc_paged_cache(B * n, page)
+        t["table"] = torch.arange(B * n, dtype=torch.int32, device="cuda").view(B, n)
+        cache = m.make_paged_cache(t)
+        ws = m.alloc_workspace(m.MODE_PREFILL_PAGED, B, max(T, P0), cap=P0 + T)
+        if P0:
+            m.mla_prefill_paged(W, x0, 0, cache, torch.empty_like(x0), ws)
+        out, delta = torch.empty_like(x), torch.empty((B * T, 7168), dtype=torch.float32, device="cuda")
+        m.mla_prefill_paged(W, x, P0, cache, out, ws, window=window, sinks=sinks, params=m.make_params(delta_out=delta))
+        assert m.mla_device_status(ws) == 0
+        outs.append(out)
+        deltas.append(delta)
+        pages.append([t[name].clone() for name in m.PAGED_TENSORS])
+    for i, what in ((1, "by the window"), (2, "by the sinks")):
+        parity_out(cuda_to_f64(outs[i]), cuda_to_f64(outs[0]), f"out, every key seen {what}")
+        parity(cuda_to_f64(deltas[i]), cuda_to_f64(deltas[0]), f"Delta, every key seen {what}")
+    for other in pages[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(other, pages[0]))
