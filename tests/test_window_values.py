@@ -75,3 +75,29 @@ def test_window_that_holds_every_key_against_the_causal_kernel(gpu_available, B,
         parity(cuda_to_f64(deltas[i]), cuda_to_f64(deltas[0]), f"Delta, every key seen {what}")
     for other in pages[1:]:
         assert all(torch.equal(a, b) for a, b in zip(other, pages[0]))
+
+
+@gpu
+@pytest.mark.parametrize("T,P0,window,sinks,page", [(130, 600, 90, 5, 64), (40, 333, 20, 150, 16), (300, 200, 7, 0, 128),
+                                                    (5, 700, 1, 1, 32)])
+def test_prefill_over_pages_needs_nothing_of_its_workspace(gpu_available, T, P0, window, sinks, page):
+    """The cached positions that no query sees are not expanded: whatever the workspace holds in their place (NaN here)
+    does not reach the output."""
+    import torch
+    from mla_testlib import cuda_weights
+    W, B = m.make_weights(cuda_weights(0)), 2
+    x0, x = normal(1, B, P0, 7168), normal(2, B, T, 7168)
+    n = -(-(P0 + T) // page)
+    outs = []
+    for fill in (0, 255):
+        t = m.alloc_paged_cache(B * n, page)
+        t["table"] = torch.arange(B * n, dtype=torch.int32, device="cuda").view(B, n)
+        cache = m.make_paged_cache(t)
+        m.mla_prefill_paged(W, x0, 0, cache, torch.empty_like(x0),
+                            m.alloc_workspace(m.MODE_PREFILL_PAGED, B, P0, cap=P0))
+        ws = m.alloc_workspace(m.MODE_PREFILL_PAGED, B, T, cap=P0 + T).fill_(fill)
+        out = torch.empty_like(x)
+        m.mla_prefill_paged(W, x, P0, cache, out, ws, window=window, sinks=sinks)
+        assert m.mla_device_status(ws) == 0
+        outs.append(out)
+    assert bool(torch.isfinite(outs[0]).all()) and torch.equal(outs[0], outs[1])
