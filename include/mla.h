@@ -30,6 +30,8 @@
  *     second stream of the library's own, beside q_b (neither fills the GPU
  *     alone, or its last wave of tiles), forked from and joined back into
  *     `stream` with events: the call is still ordered on `stream` as a whole.
+ *     mla_prefill_paged, mla_prefill_chunk_latent and a prefill that only fills
+ *     caches (out NULL) stay on `stream`.
  *     That stream and its two events are created by the first such call of
  *     each host thread on each device (not during a stream capture: a call
  *     captured before any uncaptured call of its thread stays on `stream`)

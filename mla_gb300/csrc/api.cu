@@ -32,7 +32,8 @@ struct Layout {
 // work counter at word kWorkCounterWord, split-K counters from byte 256
 // (kMaxSplitCounters ints); cleared at the start of every call.
 constexpr size_t kStatusRegion = 256 + kMaxSplitCounters * sizeof(int);
-static_assert((kStatusExtraFirst + kMaxStatusExtra) * sizeof(uint32_t) <= kStatusRegion, "status words of the paged operators");
+static_assert((kStatusExtraFirst + kMaxStatusExtra) * sizeof(uint32_t) <= kStatusRegion,
+              "status words of the paged operators");
 
 // Regions of the paged attention: partials of up to two pieces per CTA, and
 // the units of work before each sequence.

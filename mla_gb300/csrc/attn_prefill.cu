@@ -21,7 +21,9 @@
 // second half of every tile's, of Q's and of O's columns; the two maxima, and
 // at the end the two sums, go through shared memory): B=2 T=4096, a window of
 // 1,024 with 128 sinks 325 -> 308 us, of 256 with 4 sinks 218 -> 185 us, of 64
-// 157 -> 135 us.  The causal kernel keeps one thread a row: the tensor pipe and
+// 157 -> 135 us.  (The windowed times in this file are of passes back to back on
+// one set of inputs, part of which stays in L2; over three sets in turn the
+// first case takes 313-318 us as built.)  The causal kernel keeps one thread a row: the tensor pipe and
 // the exponentials (the same number a scheduler either way) set its pace, and
 // its sums keep their order.
 // Chunked prefill: the queries sit at positions past..past+T-1 and attend to
@@ -52,6 +54,8 @@
 //            read S_j from TMEM, scale, causal mask on the diagonal tile,
 //            running max with lazy rescaling (O is rescaled in TMEM only when
 //            the max grows by more than 2^8, so P stays <= 256), P_j as bf16
+//            (2^-8 of each; both operands of an MMA have one type, and V is
+//            bf16; the row sum takes the float32 values)
 //            into the P buffer (once the previous P.V has read it), and at
 //            the end O / l (after the next item's Q has been copied, so its
 //            first scores overlap) through the staging tile that the copy has

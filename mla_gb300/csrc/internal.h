@@ -375,9 +375,9 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 inline int paged_append_pages(int T, int page) { return (T - 1 + page - 1) / page + 1; }
 
 // Positions of the dense caches K [B, heads, cap, 192], V [B, heads, cap, 128]
-// filled with the paged ones' values (code * scale in bf16, exact where the scale
-// is a power of two): positions
-// j < P with j >= from or j < first, of every sequence.
+// filled with the paged ones' values (code * scale in bf16, exact where the
+// scale is a power of two): positions j < P with j >= from or j < first, of
+// every sequence.
 struct PagedGatherArgs {
   PagedCache c;
   __nv_bfloat16* k;

@@ -82,9 +82,10 @@ __device__ __forceinline__ float product(float c, float r) {
   return to_odd(y, fmaf(c, r, -y));
 }
 
-// The two rare forms of a page's rows, 8 elements of n rows each.  New tokens in a page whose scale is not a power of two: divided by it.
-__device__ __forceinline__ void divide_rows(const __nv_bfloat16* src, long long src_step, uint8_t* dst, int dst_step, int n,
-                                         float scale) {
+// The two rare forms of a page's rows, 8 elements of n rows each.  New tokens
+// in a page whose scale is not a power of two: divided by it.
+__device__ __forceinline__ void divide_rows(const __nv_bfloat16* src, long long src_step, uint8_t* dst, int dst_step,
+                                            int n, float scale) {
 #pragma unroll 1
   for (int i = 0; i < n; ++i, src += src_step, dst += dst_step) {
     const uint4 x = *reinterpret_cast<const uint4*>(src);
@@ -115,7 +116,8 @@ __device__ __forceinline__ void rescale_rows(uint8_t* at, int step, int n, float
 }
 
 // keys or values of sequence b's new token t, head h
-__device__ __forceinline__ const __nv_bfloat16* source(const PagedAppendArgs& a, int b, int h, int t, int row, bool is_v) {
+__device__ __forceinline__ const __nv_bfloat16* source(const PagedAppendArgs& a, int b, int h, int t, int row,
+                                                       bool is_v) {
   return is_v ? a.v + b * a.v_seq + (a.v_seq ? t : row + t) * a.v_token + h * a.v_head
               : a.k + b * a.k_seq + (a.k_seq ? t : row + t) * a.k_token + h * a.k_head;
 }
