@@ -452,6 +452,9 @@ typedef struct {
  *   T, cu    cu NULL: T tokens each, row n = b * T + t, N = B * T.  Else cu is
  *            int [B + 1] in DEVICE memory, sequence b's rows are cu[b] ..
  *            cu[b + 1] - 1, at most T of them (0 is allowed), N >= cu[B].
+ *            The launch covers B times the pages that min(T, N) tokens touch:
+ *            one very long prompt among hundreds of short ones (600 with one
+ *            of 32,768: 20 ms at 64 heads) is better in a call of its own
  *   params   rope_base (eps, softmax_scale, delta_out, timing: not used)
  *   workspace mla_workspace_size(MLA_MODE_PAGED_APPEND, B, T, 0)
  * Scales: with k the smallest integer in [-60, 60] for which the new tokens
@@ -468,8 +471,8 @@ typedef struct {
  * the host: the kernel skips that sequence (or page) and mla_device_status
  * then returns MLA_ERR_INVALID_ARG.
  * Errors: INVALID_ARG (null pointer, B, T or N < 1, B or N > 2^24, T > 2^30,
- * N < B * T without cu, B times the pages that T tokens touch >= 2^31, a stride
- * not a multiple of 8 or below 0), UNSUPPORTED (page, heads), ALIGNMENT,
+ * N < B * T without cu, B times the pages that min(T, N) tokens touch > 2^22
+ * where B * T > 2^24, a stride not a multiple of 8 or below 0), UNSUPPORTED (page, heads), ALIGNMENT,
  * WORKSPACE, CUDA. */
 int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params, const void* k, long long k_token,
                      long long k_head, const void* v, long long v_token, long long v_head, const void* k_pe,

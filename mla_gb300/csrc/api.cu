@@ -1140,7 +1140,9 @@ int mla_paged_append(const mla_paged_cache_t* cache, const mla_params_t* params,
   if (!k || !v || !k_pe || !P || B < 1 || B > kMaxTokens || T < 1 || T > kMaxPagedPositions || N < 1 || N > kMaxTokens)
     return MLA_ERR_INVALID_ARG;
   if (!cu && (int64_t)B * T > N) return MLA_ERR_INVALID_ARG;
-  if ((int64_t)B * paged_append_pages(T, cache->page) > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  // thread blocks of a ragged call, most of them empty (2^22 columns are a second at 128 heads)
+  if ((int64_t)B * T > kMaxTokens && (int64_t)B * paged_append_pages(std::min(T, N), cache->page) > (1 << 22))
+    return MLA_ERR_INVALID_ARG;
   for (long long s : {k_token, k_head, v_token, v_head, pe_token})
     if (!good_stride(s)) return MLA_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_pe) || (reinterpret_cast<uintptr_t>(P) & 3) ||

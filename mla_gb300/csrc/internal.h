@@ -371,7 +371,7 @@ struct PagedAppendArgs {
   bool status_cleared;         // the caller cleared the status region: OR into it
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
-// Pages that T tokens of one sequence may touch, wherever they begin; times B at most INT32_MAX.
+// Pages that T tokens of one sequence may touch, wherever they begin; times B at most 2^24.
 inline int paged_append_pages(int T, int page) { return (T - 1 + page - 1) / page + 1; }
 
 // Positions of the dense caches K [B, heads, cap, 192], V [B, heads, cap, 128]

@@ -291,12 +291,13 @@ cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-  const int pages_per_seq = paged_append_pages(a.T, a.c.page);
+  const int most = min(a.T, a.N);  // a sequence has no more rows than the call
+  const int pages_per_seq = paged_append_pages(most, a.c.page);
   // 8 tokens a warp: one warp per head for a few new tokens, else page / 8
-  const int w_log = a.T <= 8 ? 0 : a.c.page == 16 ? 1 : a.c.page == 32 ? 2 : a.c.page == 64 ? 3 : 4;
+  const int w_log = most <= 8 ? 0 : a.c.page == 16 ? 1 : a.c.page == 32 ? 2 : a.c.page == 64 ? 3 : 4;
   const int W = 1 << w_log, warps = W > 8 ? W : 8;
   const long long gx = (long long)a.B * pages_per_seq;
-  if (gx > INT32_MAX) return cudaErrorInvalidValue;
+  if (gx > 1 << 24) return cudaErrorInvalidValue;
   const int gy = (a.c.heads * W + warps - 1) / warps + 1;
   return launch_pdl(paged_append_kernel, dim3((unsigned)gx, gy), dim3(warps * 32), 0, stream, a,
                     pages_per_seq, w_log);

@@ -247,8 +247,8 @@ def test_status_words_end_inside_the_status_region(gpu_available):
 
 # ---- far positions and long, ragged batches ------------------------------------------------------------------
 def test_sizes_of_an_append_that_are_taken_and_refused():
-    """What mla.h states: 2^24 rows and sequences, T up to 2^30, counts of pages in 31 bits. A call that passes these
-    checks meets the next one here, on its workspace (-3): nothing is enqueued."""
+    """What mla.h states: 2^24 rows and sequences, T up to 2^30, 2^22 pages where B * T passes 2^24. A call that passes
+    these checks meets the next one here, on its workspace (-3): nothing is enqueued."""
     from test_paged import append, fake_cache, FAKE
     far = fake_cache(max_pages=1 << 23, page=128, heads=4)
     assert m.workspace_size(m.MODE_PAGED_APPEND, 600, 32768) > 0
@@ -256,7 +256,12 @@ def test_sizes_of_an_append_that_are_taken_and_refused():
     assert append(far, B=600, T=32768, N=40000, wsb=16) == -1
     assert append(far, B=2, T=(1 << 30) + 1, N=7, cu=FAKE + 16384, wsb=16) == -1
     assert append(far, B=(1 << 24) + 1, T=1, N=7, cu=FAKE + 16384, wsb=16) == -1
-    assert append(far, B=1 << 20, T=1 << 20, N=7, cu=FAKE + 16384, wsb=16) == -1
+    assert append(far, B=1 << 20, T=1 << 20, N=1 << 24, cu=FAKE + 16384, wsb=16) == -1
+    assert append(far, B=1 << 20, T=1 << 20, N=7, cu=FAKE + 16384, wsb=16) == -3      # no sequence has more than 7
+    assert append(far, B=512, T=1 << 30, N=(8191 - 1) * 128 + 2, cu=FAKE + 16384, wsb=16) == -3   # 8,192 pages each
+    assert append(far, B=512, T=1 << 30, N=(8191 - 1) * 128 + 130, cu=FAKE + 16384, wsb=16) == -1
+    assert append(far, B=1 << 24, T=1, N=1 << 24, cu=FAKE + 16384, wsb=16) == -3
+    assert append(far, B=(1 << 24) - 1, T=2, N=7, cu=FAKE + 16384, wsb=16) == -1
 
 
 def test_reaches_that_are_taken_and_refused():
