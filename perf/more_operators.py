@@ -295,7 +295,7 @@ def prepare(case, seed):
         s["pool"] = m.make_page_pool(s["table"], s["refs"], page)
         if op != "regrow":
             s["handle"] = m.make_paged_cache(dict(s["cache"], table=s["table"]))
-        s["workspace"] = m.alloc_workspace(m.MODE_PAGES, case.get("n", 1), n_pages, rows)
+        s["workspace"] = m.alloc_workspace(m.MODE_PAGES, case.get("n", 1), n_pages, cap=rows)
     return s
 
 
