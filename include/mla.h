@@ -64,6 +64,7 @@ extern "C" {
 #define MLA_ERR_UNSUPPORTED (-4)  /* a size or mode the library does not implement */
 #define MLA_ERR_CUDA (-5)         /* a CUDA call or kernel launch failed */
 #define MLA_ERR_TIMEOUT (-6)      /* a bounded device-side wait gave up (see mla_device_status) */
+#define MLA_ERR_NO_PAGES (-7)     /* fewer free pages than a call takes (see mla_device_status) */
 
 /* ---- fixed sizes -------------------------------------------------------- */
 #define MLA_D 7168
@@ -89,6 +90,7 @@ extern "C" {
 #define MLA_MODE_WINDOW_ATTN 10
 #define MLA_MODE_DECODE_PAGED 11
 #define MLA_MODE_PREFILL_PAGED 12
+#define MLA_MODE_PAGES 13
 
 /* Weights of one MLA sublayer: device pointers to bf16, nn.Linear [out, in].
  * Key-value compression page, MLA __init__ excerpt, for the projections;
@@ -167,6 +169,10 @@ typedef struct {
  *   mode = MLA_MODE_PREFILL_PAGED: mla_prefill_paged, B sequences of T = t_or_p
  *                                  tokens, cap = P0 + T (or more): it holds
  *                                  those positions' keys and values in bf16.
+ *   mode = MLA_MODE_PAGES:         the mla_pages_ calls on lists of B entries,
+ *                                  t_or_p = n_pages (of the destination cache
+ *                                  in a copy), cap = the table's rows (0 for a
+ *                                  copy).
  * Returns 0 when the arguments are out of range. */
 size_t mla_workspace_size(int mode, int B, int t_or_p, int cap);
 
@@ -570,9 +576,100 @@ int mla_prefill_paged(const mla_weights_t* w, const mla_params_t* params, const 
                       const mla_paged_cache_t* cache, int window, int sinks, void* out, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/* ---- pages of the paged cache -------------------------------------------------
+ * Who holds a page, kept on the device: a pool is the cache's table with one
+ * row per sequence, and the number of holds on each page.  The calls below
+ * change both on `stream`, without a word from the host, so a captured serving
+ * step can take, share and give back pages on every replay.
+ *   table    int [rows, max_pages], the same memory as the cache's table: the
+ *            pages of each sequence in order, -1 where there is none
+ *   refs     int [n_pages]: table entries that hold the page (and holds of the
+ *            user's own, e.g. of a stored prefix); 0 = the page is free
+ * All -1 and all 0 is an empty pool.  Pages are taken lowest number first, in
+ * the order of the list and then of the positions, so a call has one result.
+ * Lists are int [n] in DEVICE memory (4-byte aligned), 1 <= n <= 2^20; P[i]
+ * counts positions, ceil(P[i] / page) entries of a row hold P[i] of them.
+ * Calls on one pool are ordered by their stream; two calls, or a call and one
+ * that reads the cache, must not overlap.  One call of the list is one
+ * transaction: it sees the pool as it was before the call.
+ * An entry that cannot be carried out (a row outside [0, rows), P[i] outside
+ * [0, max_pages * page], what the calls name below) is skipped, and
+ * mla_device_status then returns MLA_ERR_INVALID_ARG. */
+typedef struct {
+  int* table;
+  int* refs;
+  int rows, max_pages, n_pages, page;
+} mla_page_pool_t;
+
+/* Gives back the pages of rows[i] behind its first P[i] positions (0: all of
+ * them; a rejected draft: the positions that stay): entry e >= ceil(P[i] / page)
+ * becomes -1 and its page loses one hold.  A row may be listed more than once
+ * (the smallest P counts); P[i] past the row's end gives nothing back.  Reported:
+ * entries that are no page (they become -1), pages held by nobody (they stay free).
+ *   workspace mla_workspace_size(MLA_MODE_PAGES, n, n_pages, rows), as in the
+ *            calls below; not shared by calls that may run concurrently
+ * Errors: INVALID_ARG (null pointer, n < 1 or > 2^20, rows < 1 or > 2^24,
+ * max_pages < 1, n_pages < 1), UNSUPPORTED (page not 16, 32, 64 or 128,
+ * n_pages * page above 31 bits, max_pages * page > 2^30), ALIGNMENT, WORKSPACE,
+ * CUDA. */
+int mla_pages_free(const mla_page_pool_t* pool, const int* rows, const int* P, int n, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Takes free pages so that rows[i] holds its first P[i] positions: every entry
+ * e < ceil(P[i] / page) that holds none gets one (its contents are what they
+ * were), with one hold.  With too few free pages for the whole list nothing is
+ * changed and mla_device_status returns MLA_ERR_NO_PAGES.  A row that is listed
+ * again is skipped from the second time on and reported, entries past n_pages
+ * are left and reported.  Errors as mla_pages_free. */
+int mla_pages_reserve(const mla_page_pool_t* pool, const int* rows, const int* P, int n, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Row children[i] becomes a sequence that has the first P[i] positions of row
+ * parents[i]: the whole pages are shared (one more hold each), and where P[i]
+ * ends inside a page, its first P[i] % page tokens, in all heads and with the
+ * page's scales, are copied into a new page, so that both sequences can go on
+ * appending.  The other slots of the new page are left as they were.  With too
+ * few free pages nothing is changed (MLA_ERR_NO_PAGES, as mla_pages_reserve).
+ * Skipped and reported: a child whose first ceil(P[i] / page) entries are not
+ * all -1 or that an earlier entry of the list names, a parent that does not
+ * hold P[i] positions in pages that somebody holds.  P[i] = 0 changes nothing.
+ * Errors as mla_pages_free, and those of the cache (INVALID_ARG where its table,
+ * n_pages, max_pages or page are not the pool's). */
+int mla_pages_fork(const mla_paged_cache_t* cache, const mla_page_pool_t* pool, const int* parents, const int* children,
+                   const int* P, int n, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Moves the pages that are held to the numbers 0 .. n_live - 1: those from
+ * n_live on, in order, into the free ones below, in order; refs and the table
+ * follow.  Pages from n_live on are free afterwards, their contents as before.
+ *   moved    int [n_pages] in DEVICE memory: receives the new number of every
+ *            page (its own where it stays, -1 where it was free), for what the
+ *            user keeps page numbers in
+ *   n_live   int [1] in DEVICE memory: receives the number of pages held
+ * Reported: table entries that are no page, or a page held by nobody (they
+ * become -1).
+ *   workspace mla_workspace_size(MLA_MODE_PAGES, 1, n_pages, rows)
+ * Errors as mla_pages_fork. */
+int mla_pages_compact(const mla_paged_cache_t* cache, const mla_page_pool_t* pool, int* moved, int* n_live,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Copies page src[i] of one cache (codes, scales, rotary keys) to page dst[i]
+ * of another of the same page and heads, or of the same one; tables and holds
+ * are the caller's.  Where a destination is named more than once, the last
+ * entry counts; in one cache an entry whose source is written by another entry
+ * is skipped; page numbers outside a cache are skipped; all three are reported
+ * (MLA_ERR_INVALID_ARG from mla_device_status).  The tables of the caches are
+ * not looked at.
+ *   workspace mla_workspace_size(MLA_MODE_PAGES, n, to->n_pages, 0)
+ * Errors: INVALID_ARG (null pointer, n < 1 or > 2^20, caches that overlap
+ * without being one), UNSUPPORTED (page, heads, or different ones), ALIGNMENT,
+ * WORKSPACE, CUDA. */
+int mla_pages_copy(const mla_paged_cache_t* from, const mla_paged_cache_t* to, const int* src, const int* dst, int n,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream` and reads the device status word the last call on
  * this workspace left: MLA_OK, MLA_ERR_TIMEOUT if a bounded device wait
- * gave up (the kernel then skipped its remaining work and returned), or
+ * gave up (the kernel then skipped its remaining work and returned),
+ * MLA_ERR_NO_PAGES (see the mla_pages_ calls), or
  * MLA_ERR_INVALID_ARG if a per-sequence position of a _varlen call was
  * outside [0, P_max].
  * The word describes one call only: every entry point clears it (and the

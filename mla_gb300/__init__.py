@@ -19,12 +19,13 @@ FFN_INTER = 18432
 MODE_PREFILL, MODE_DECODE, MODE_DECODE_LATENT, MODE_FFN, MODE_CHUNK_LATENT, MODE_CHUNK_ABSORBED = 0, 1, 2, 3, 4, 5
 MODE_FOLD = 6
 MODE_PAGED_APPEND, MODE_PAGED_ATTN, MODE_WINDOW_ATTN, MODE_DECODE_PAGED, MODE_PREFILL_PAGED = 8, 9, 10, 11, 12
+MODE_PAGES = 13
 STAGES = ["input_norm", "a_proj", "latent", "q_b", "kv_b", "attn", "combine", "absorb_q", "absorb_o", "o_proj",
           "ffn_norm", "gate_up", "down"]
 MAX_STAGES = len(STAGES)
 
 STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_ALIGNMENT", -3: "MLA_ERR_WORKSPACE",
-          -4: "MLA_ERR_UNSUPPORTED", -5: "MLA_ERR_CUDA", -6: "MLA_ERR_TIMEOUT"}
+          -4: "MLA_ERR_UNSUPPORTED", -5: "MLA_ERR_CUDA", -6: "MLA_ERR_TIMEOUT", -7: "MLA_ERR_NO_PAGES"}
 
 WEIGHT_NAMES = ["w_in_norm", "w_q_a", "w_q_a_norm", "w_q_b", "w_kv_a", "w_kv_a_norm", "w_kv_b", "w_o"]
 WEIGHT_SHAPES = {
@@ -61,6 +62,11 @@ class MlaFfnWeights(ctypes.Structure):
 class MlaPagedCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_pe", "k_scales", "v_scales", "table")] + \
                [(n, ctypes.c_int) for n in ("n_pages", "max_pages", "page", "heads")]
+
+
+class MlaPagePool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "refs")] + \
+               [(n, ctypes.c_int) for n in ("rows", "max_pages", "n_pages", "page")]
 
 
 class MlaTiming(ctypes.Structure):
@@ -113,6 +119,11 @@ _SIGS = {
                               ctypes.POINTER(MlaPagedCache), _I, _I, _VP, _VP, _SZ, _VP]),
     "mla_prefill_paged": (_I, [ctypes.POINTER(MlaWeights), ctypes.POINTER(MlaParams), _VP, _I, _I, _I,
                                ctypes.POINTER(MlaPagedCache), _I, _I, _VP, _VP, _SZ, _VP]),
+    "mla_pages_free": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
+    "mla_pages_reserve": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
+    "mla_pages_fork": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _VP, _SZ, _VP]),
+    "mla_pages_compact": (_I, [_VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "mla_pages_copy": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _SZ, _VP]),
     "mla_device_status": (_I, [_VP, _VP]),
     "mla_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -497,6 +508,77 @@ def mla_window_attention(q, P0: int, k_cache, v_cache, out, workspace, window: i
                                     k_cache.data_ptr(), v_cache.data_ptr(), cap, window, sinks, out.data_ptr(),
                                     _bytes(workspace, dev), workspace.nbytes, s)
     _check(rc, "mla_window_attention")
+
+
+def make_page_pool(table, refs, page: int = 64) -> MlaPagePool:
+    """Pack int32 CUDA tensors table [rows, max_pages] (-1: no page; the paged cache's table) and refs [n_pages]
+    (holds on each page, 0: free) into the C struct, which points at them."""
+    import torch
+    for x, what, dims in ((table, "table", 2), (refs, "refs", 1)):
+        if x.dtype is not torch.int32 or not x.is_cuda or not x.is_contiguous() or x.dim() != dims or \
+                x.device != table.device or not x.numel():
+            raise ValueError(f"page pool {what}: need a contiguous int32 CUDA tensor of {dims} dimension(s), not empty, "
+                             "on the table's device")
+    s = MlaPagePool(table.data_ptr(), refs.data_ptr(), table.shape[0], table.shape[1], refs.shape[0], page)
+    s._keep = (table, refs)
+    s._ref, s._device = ctypes.byref(s), table.get_device()
+    return s
+
+
+def mla_pages_free(pool: MlaPagePool, rows, P, workspace, stream=None):
+    """Gives back the pages of each of the rows behind its first P positions; rows, P: int32 [n]; workspace of
+    MODE_PAGES(n, n_pages, cap=rows of the table) here and below."""
+    dev, n = pool._device, rows.shape[0]
+    s = _stream_on(dev, stream)
+    rc = lib().mla_pages_free(pool._ref, _ints(rows, "rows", n, dev), _ints(P, "P", n, dev), n, _bytes(workspace, dev),
+                              workspace.nbytes, s)
+    _check(rc, "mla_pages_free")
+
+
+def mla_pages_reserve(pool: MlaPagePool, rows, P, workspace, stream=None):
+    """Takes free pages so that each of the rows holds its first P positions; rows, P: int32 [n]."""
+    dev, n = pool._device, rows.shape[0]
+    s = _stream_on(dev, stream)
+    rc = lib().mla_pages_reserve(pool._ref, _ints(rows, "rows", n, dev), _ints(P, "P", n, dev), n,
+                                 _bytes(workspace, dev), workspace.nbytes, s)
+    _check(rc, "mla_pages_reserve")
+
+
+def mla_pages_fork(cache: MlaPagedCache, pool: MlaPagePool, parents, children, P, workspace, stream=None):
+    """Rows `children` get the first P positions of rows `parents`: whole pages shared, the rest of a page copied;
+    int32 [n] each."""
+    dev, n = pool._device, parents.shape[0]
+    s = _stream_on(dev, stream)
+    if cache._device != dev:
+        raise ValueError("cache and pool: need the same device")
+    rc = lib().mla_pages_fork(cache._ref, pool._ref, _ints(parents, "parents", n, dev),
+                              _ints(children, "children", n, dev), _ints(P, "P", n, dev), n, _bytes(workspace, dev),
+                              workspace.nbytes, s)
+    _check(rc, "mla_pages_fork")
+
+
+def mla_pages_compact(cache: MlaPagedCache, pool: MlaPagePool, moved, n_live, workspace, stream=None):
+    """Moves the pages that are held to the lowest numbers; moved: int32 [n_pages] receives each page's new number
+    (-1: free), n_live: int32 [1] the number of pages held; workspace of MODE_PAGES(1, n_pages, cap=rows)."""
+    dev = pool._device
+    s = _stream_on(dev, stream)
+    if cache._device != dev:
+        raise ValueError("cache and pool: need the same device")
+    rc = lib().mla_pages_compact(cache._ref, pool._ref, _ints(moved, "moved", pool.n_pages, dev),
+                                 _ints(n_live, "n_live", 1, dev), _bytes(workspace, dev), workspace.nbytes, s)
+    _check(rc, "mla_pages_compact")
+
+
+def mla_pages_copy(source: MlaPagedCache, target: MlaPagedCache, src, dst, workspace, stream=None):
+    """Copies pages src of one cache to pages dst of another, or of the same one; int32 [n] each; workspace of
+    MODE_PAGES(n, n_pages of the target)."""
+    dev, n = target._device, src.shape[0]
+    s = _stream_on(dev, stream)
+    if source._device != dev:
+        raise ValueError("source and target: need the same device")
+    rc = lib().mla_pages_copy(source._ref, target._ref, _ints(src, "src", n, dev), _ints(dst, "dst", n, dev), n,
+                              _bytes(workspace, dev), workspace.nbytes, s)
+    _check(rc, "mla_pages_copy")
 
 
 def mla_decode_paged(weights: MlaWeights, x, P, P_max: int, cache: MlaPagedCache, out, workspace, window: int = 0,

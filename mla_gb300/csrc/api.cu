@@ -18,6 +18,8 @@ constexpr int kMaxSmsForSizing = 256;                     // workspace upper bou
 constexpr int64_t kMaxTokens = 1 << 24;
 // positions of a paged sequence: positions and a call's tokens behind them stay in 31 bits
 constexpr int kMaxPagedPositions = 1 << 30;
+constexpr int kMaxPoolPages = INT32_MAX / 16;  // pages of 16 tokens whose slots are counted in 31 bits
+constexpr int kMaxPageList = 1 << 20;
 
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -25,6 +27,7 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // and by the entry points.
 struct Layout {
   size_t status, cs, xn, ca, cq, ckv, kpe, q, o, kscr, vscr, qlat, olat, part_o, part_ml, split, h, plan, pos, kv, total;
+  size_t need, first, claims, bits, seg, fresh, from, head;  // the plan of the mla_pages_ calls
   size_t split_bytes;  // split-K partial slots (decode modes), 0 = none
 };
 
@@ -62,6 +65,19 @@ Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
   L.status = take(kStatusRegion);
   // the fold of W_UV into W_o, the append and the window attention: the status region only
   if (mode == MLA_MODE_FOLD || mode == MLA_MODE_PAGED_APPEND || mode == MLA_MODE_WINDOW_ATTN) {
+    L.total = off;
+    return L;
+  }
+  if (mode == MLA_MODE_PAGES) {  // B list entries, t_or_p pages, cap rows
+    const size_t pages = (size_t)t_or_p, segs = (pages + 1023) / 1024;
+    L.head = take(2 * sizeof(int));
+    L.need = take((size_t)B * sizeof(int));
+    L.first = take((size_t)B * sizeof(int));
+    L.claims = take((pages > (size_t)cap ? pages : (size_t)cap) * sizeof(int));
+    L.bits = take(segs * 128);
+    L.seg = take(segs * sizeof(int));
+    L.fresh = take(pages * sizeof(int));
+    L.from = take(pages * sizeof(int));
     L.total = off;
     return L;
   }
@@ -489,6 +505,8 @@ size_t mla_workspace_size(int mode, int B, int t_or_p, int cap) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
   } else if (mode == MLA_MODE_PAGED_ATTN) {
     if (t_or_p < 1 || t_or_p > kPagedMaxT || B > kMaxTokens) return 0;
+  } else if (mode == MLA_MODE_PAGES) {
+    if (t_or_p < 1 || t_or_p > kMaxPoolPages || B > kMaxPageList || cap < 0 || cap > kMaxTokens) return 0;
   } else {
     return 0;
   }
@@ -504,6 +522,7 @@ const char* mla_status_string(int s) {
     case MLA_ERR_UNSUPPORTED: return "MLA_ERR_UNSUPPORTED: size or mode not supported";
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA: CUDA call or kernel launch failed";
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT: a bounded device wait gave up";
+    case MLA_ERR_NO_PAGES: return "MLA_ERR_NO_PAGES: fewer free pages than the call takes";
     default: return "unknown MLA status";
   }
 }
@@ -524,6 +543,7 @@ int mla_device_status(const void* workspace, void* stream) {
     for (uint32_t i = 0; i < head[1]; ++i) word |= extra[i];
   }
   if (word & kStatusTimeout) return MLA_ERR_TIMEOUT;
+  if (word & kStatusNoPages) return MLA_ERR_NO_PAGES;
   return (word & kStatusBadLength) ? MLA_ERR_INVALID_ARG : MLA_OK;
 }
 
@@ -1235,6 +1255,161 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
                     static_cast<const __nv_bfloat16*>(v_cache), static_cast<__nv_bfloat16*>(out), B, T, cap,
                     p.scale, P0, window, sinks};
   return launch_prefill_attention(a, st, sms, stream_) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---- pages of the paged cache -------------------------------------------------
+namespace {
+
+int check_pool(const mla_page_pool_t* p) {
+  if (!p || !p->table || !p->refs || p->rows < 1 || p->rows > kMaxTokens || p->max_pages < 1 || p->n_pages < 1)
+    return MLA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(p->table) & 3) || (reinterpret_cast<uintptr_t>(p->refs) & 3)) return MLA_ERR_ALIGNMENT;
+  if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->n_pages * p->page > INT32_MAX || (int64_t)p->max_pages * p->page > kMaxPagedPositions)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+int check_cache_and_pool(const mla_paged_cache_t* c, const mla_page_pool_t* p) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  rc = check_pool(p);
+  if (rc) return rc;
+  return c->table == p->table && c->n_pages == p->n_pages && c->max_pages == p->max_pages && c->page == p->page
+             ? MLA_OK
+             : MLA_ERR_INVALID_ARG;
+}
+
+// A call's lists (null: not part of it), their length and the workspace.
+int check_lists(const int* a, const int* b, const int* c, int n, void* ws, size_t bytes, int n_pages, int rows) {
+  if (n < 1 || n > kMaxPageList) return MLA_ERR_INVALID_ARG;
+  for (const int* x : {a, b, c})
+    if (reinterpret_cast<uintptr_t>(x) & 3) return MLA_ERR_ALIGNMENT;
+  if (!ws) return MLA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MLA_ERR_ALIGNMENT;
+  return bytes < make_layout(MLA_MODE_PAGES, n, n_pages, kMaxSmsForSizing, rows).total ? MLA_ERR_WORKSPACE : MLA_OK;
+}
+
+PagePool device_pool(const mla_page_pool_t* p) {
+  return PagePool{p->table, p->refs, p->rows, p->max_pages, p->n_pages, p->page};
+}
+
+PagePlanArgs page_plan(const mla_page_pool_t* pool, int n, void* ws) {
+  const Layout L = make_layout(MLA_MODE_PAGES, n, pool->n_pages, kMaxSmsForSizing, pool->rows);
+  PagePlanArgs a{};
+  a.pool = device_pool(pool);
+  a.n = n;
+  a.need = at<int>(ws, L.need);
+  a.first = at<int>(ws, L.first);
+  a.claims = at<int>(ws, L.claims);
+  a.bits = at<uint32_t>(ws, L.bits);
+  a.seg = at<int>(ws, L.seg);
+  a.fresh = at<int>(ws, L.fresh);
+  a.from = at<int>(ws, L.from);
+  a.head = at<int>(ws, L.head);
+  a.status = at<uint32_t>(ws, L.status);
+  return a;
+}
+
+// Whether [a, a + n) and [b, b + m) share a byte.
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + m && y < x + n;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_pages_free(const mla_page_pool_t* pool, const int* rows, const int* P, int n, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  int rc = check_pool(pool);
+  if (rc) return rc;
+  if (!rows || !P) return MLA_ERR_INVALID_ARG;
+  rc = check_lists(rows, P, nullptr, n, workspace, workspace_bytes, pool->n_pages, pool->rows);
+  if (rc) return rc;
+  return launch_pages_free(device_pool(pool), rows, P, n, static_cast<uint32_t*>(workspace),
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int mla_pages_reserve(const mla_page_pool_t* pool, const int* rows, const int* P, int n, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = check_pool(pool);
+  if (rc) return rc;
+  if (!rows || !P) return MLA_ERR_INVALID_ARG;
+  rc = check_lists(rows, P, nullptr, n, workspace, workspace_bytes, pool->n_pages, pool->rows);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  PagePlanArgs a = page_plan(pool, n, workspace);
+  a.rows = rows;
+  a.P = P;
+  return launch_pages_reserve(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_pages_fork(const mla_paged_cache_t* cache, const mla_page_pool_t* pool, const int* parents, const int* children,
+                   const int* P, int n, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache_and_pool(cache, pool);
+  if (rc) return rc;
+  if (!parents || !children || !P) return MLA_ERR_INVALID_ARG;
+  rc = check_lists(parents, children, P, n, workspace, workspace_bytes, pool->n_pages, pool->rows);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  PagePlanArgs a = page_plan(pool, n, workspace);
+  a.rows = children;
+  a.parents = parents;
+  a.P = P;
+  return launch_pages_fork(device_cache(cache), a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK
+                                                                                                         : MLA_ERR_CUDA;
+}
+
+int mla_pages_compact(const mla_paged_cache_t* cache, const mla_page_pool_t* pool, int* moved, int* n_live,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache_and_pool(cache, pool);
+  if (rc) return rc;
+  if (!moved || !n_live) return MLA_ERR_INVALID_ARG;
+  rc = check_lists(moved, n_live, nullptr, 1, workspace, workspace_bytes, pool->n_pages, pool->rows);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  PagePlanArgs a = page_plan(pool, 1, workspace);
+  a.moved = moved;
+  a.n_live = n_live;
+  return launch_pages_compact(device_cache(cache), a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+int mla_pages_copy(const mla_paged_cache_t* from, const mla_paged_cache_t* to, const int* src, const int* dst, int n,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache(from);
+  if (!rc) rc = check_cache(to);
+  if (rc) return rc;
+  if (!src || !dst) return MLA_ERR_INVALID_ARG;
+  if (from->page != to->page || from->heads != to->heads) return MLA_ERR_UNSUPPORTED;
+  const size_t tokens[2] = {(size_t)from->n_pages * from->page, (size_t)to->n_pages * to->page};
+  const size_t heads = from->heads, scale[2] = {from->n_pages * heads * 4, to->n_pages * heads * 4};
+  const bool one = from->k_codes == to->k_codes && from->v_codes == to->v_codes && from->k_pe == to->k_pe && from->k_scales == to->k_scales &&
+                   from->v_scales == to->v_scales && from->n_pages == to->n_pages;
+  if (!one && (overlap(from->k_codes, tokens[0] * heads * 128, to->k_codes, tokens[1] * heads * 128) ||
+               overlap(from->v_codes, tokens[0] * heads * 128, to->v_codes, tokens[1] * heads * 128) ||
+               overlap(from->k_pe, tokens[0] * 128, to->k_pe, tokens[1] * 128) ||
+               overlap(from->k_scales, scale[0], to->k_scales, scale[1]) ||
+               overlap(from->v_scales, scale[0], to->v_scales, scale[1])))
+    return MLA_ERR_INVALID_ARG;
+  rc = check_lists(src, dst, nullptr, n, workspace, workspace_bytes, to->n_pages, 0);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  const Layout L = make_layout(MLA_MODE_PAGES, n, to->n_pages, kMaxSmsForSizing, 0);
+  const PageCopyArgs a{device_cache(from), device_cache(to), one, src, dst, n, at<int>(workspace, L.claims),
+                       at<uint32_t>(workspace, L.status)};
+  return launch_pages_copy(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@ namespace mla {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kStatusTimeout = 1u;
 constexpr uint32_t kStatusBadLength = 2u;  // a per-sequence position outside [0, P_max]
+constexpr uint32_t kStatusNoPages = 4u;    // fewer free pages than the call takes
 
 // Per-sequence position of the new token (decode with per-sequence lengths),
 // clamped into [0, p_max] so that no access leaves the caches; an

@@ -68,10 +68,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The same launch as clusters of two consecutive CTAs (grid.x even).
+// The same launch as clusters of `cluster` consecutive CTAs (grid.x a multiple of it).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_cluster2(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                Args&&... args) {
+cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -81,13 +81,18 @@ cudaError_t launch_pdl_cluster2(void (*kern)(KArgs...), dim3 grid, dim3 block, s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster2(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                Args&&... args) {
+  return launch_pdl_cluster(kern, 2, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 struct DevStatusHost {
@@ -411,6 +416,49 @@ inline long long paged_attention_tiles(int P_max, int T, int window, int sinks) 
 }
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream,
                                    int* launches);
+
+// ---- pages of the paged cache -----------------------------------------------------
+// table [rows, max_pages] (below 0: no page) and refs [n_pages], the holds on
+// each page (0: free).
+struct PagePool {
+  int* table;
+  int* refs;
+  int rows, max_pages, n_pages, page;
+};
+// Scratch of the plan; all but status is written before it is read.
+struct PagePlanArgs {
+  PagePool pool;
+  const int* rows;             // the list: rows of the table (fork: the children) ...
+  const int* parents;          // ... fork: the rows that they follow ...
+  const int* P;                // ... and positions
+  int n;
+  int* need;                   // [n] pages that an entry takes, -1: it is skipped
+  int* first;                  // [n] pages taken by the entries before, -1: skipped
+  int* claims;                 // [rows] of large tables: the first entry that names the row
+  uint32_t* bits;              // [n_pages / 32, whole segments] free pages
+  int* seg;                    // free pages before each segment of 1,024
+  int* fresh;                  // [n_pages] free pages by rank: those to take, or to move to
+  int* from;                   // [n_pages] compact: the pages to move
+  int* moved;                  // [n_pages] compact: every page's new number, -1: free
+  int* n_live;                 // [1] compact
+  int* head;                   // [2] {whether the pages suffice, pages taken} or {live pages, moves}
+  uint32_t* status;
+};
+cudaError_t launch_pages_free(const PagePool& p, const int* rows, const int* P, int n, uint32_t* status,
+                              cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PagePlanArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagedCache& c, const PagePlanArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagedCache& c, const PagePlanArgs& a, int num_sms, cudaStream_t stream);
+struct PageCopyArgs {
+  PagedCache from, to;         // of one page and head count
+  bool same;                   // from and to are one cache
+  const int* src;
+  const int* dst;
+  int n;
+  int* claims;                 // [to.n_pages]
+  uint32_t* status;
+};
+cudaError_t launch_pages_copy(const PageCopyArgs& a, int num_sms, cudaStream_t stream);
 
 // qlat[b, h, 512:576] = q[b, h*192 + 128 : h*192 + 192]
 cudaError_t launch_copy_qpe(const __nv_bfloat16* q, __nv_bfloat16* qlat, int B, cudaStream_t stream);
