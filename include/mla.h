@@ -91,6 +91,7 @@ extern "C" {
 #define MLA_MODE_DECODE_PAGED 11
 #define MLA_MODE_PREFILL_PAGED 12
 #define MLA_MODE_PAGES 13
+#define MLA_MODE_DOCUMENTS 14
 
 /* Weights of one MLA sublayer: device pointers to bf16, nn.Linear [out, in].
  * Key-value compression page, MLA __init__ excerpt, for the projections;
@@ -173,6 +174,8 @@ typedef struct {
  *                                  t_or_p = n_pages (of the destination cache
  *                                  in a copy), cap = the table's rows (0 for a
  *                                  copy).
+ *   mode = MLA_MODE_DOCUMENTS:     mla_document_attention, B documents, t_or_p =
+ *                                  N rows of q (`cap` ignored).
  * Returns 0 when the arguments are out of range. */
 size_t mla_workspace_size(int mode, int B, int t_or_p, int cap);
 
@@ -543,6 +546,46 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
 int mla_window_attention(const mla_params_t* params, const void* q, int B, int T, int P0, const void* k_cache,
                          const void* v_cache, int cap, int window, int sinks, void* out, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* Attention of several documents (ragged prompts, pieces of prompts behind
+ * cached tokens, single new tokens) packed one after the other: rows cu_q[d] ..
+ * cu_q[d + 1] - 1 of q are the n new tokens of document d, rows cu_k[d] ..
+ * cu_k[d + 1] - 1 of the caches its L keys, the last n of which are the new
+ * tokens' own.  Query t of a document sits at position i = L - n + t and sees
+ * key j of its document (0 <= j < L), and no other document's, iff
+ *   j < prefix[d], or j <= i and (window = 0, or i - j < window, or j < sinks).
+ * A row that sees no key (a document with fewer keys than queries) is zeros.
+ *   q        bf16, row n at q + n * q_row: 64 heads x [128 nope | 64 pe], pe
+ *            rotated; q_row a multiple of 8, >= 64 * 192
+ *   k_cache  bf16 [64, cap, 192], v_cache [64, cap, 128]: the layout of
+ *            mla_prefill's caches at B = 1 (a score depends on the distance of
+ *            its positions only, so keys and queries may be rotated by their
+ *            place in the pack or in the document alike)
+ *   out      bf16, row n at out + n * out_row: 64 x 128; out_row a multiple of
+ *            8, >= 64 * 128.  Rows outside cu_q[0] .. cu_q[n_docs] are left as
+ *            they were
+ *   cu_q, cu_k  int [n_docs + 1] in DEVICE memory, 0 <= cu[0] <= cu[1] <= ..,
+ *            cu_q[n_docs] <= N, cu_k[n_docs] <= cap; empty documents are
+ *            allowed; cu_k NULL: cu_q
+ *   prefix   int [n_docs] in DEVICE memory, or NULL: none.  Tokens of the
+ *            document that all its queries see (a prompt read from both sides);
+ *            taken as at least 0 and at most L
+ *   window   0 = no window; sinks is then ignored
+ *   params   softmax_scale (the others are not used)
+ *   workspace mla_workspace_size(MLA_MODE_DOCUMENTS, n_docs, N, 0)
+ * Offsets out of range or order cannot be checked on the host: the kernel then
+ * writes nothing and mla_device_status returns MLA_ERR_INVALID_ARG.
+ * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
+ * Keys behind the last one that a query of its tile of 128 sees are not used,
+ * whatever the caches hold; a NaN among the values of another key may also
+ * reach queries of its document that do not see the key, but no other document.
+ * Errors: INVALID_ARG (null pointer, N, cap < 1 or > 2^24, n_docs < 1 or > 2^20,
+ * window or sinks < 0, row strides), ALIGNMENT (cu_q, cu_k, prefix: 4 bytes),
+ * WORKSPACE, CUDA. */
+int mla_document_attention(const mla_params_t* params, const void* q, long long q_row, int N, const int* cu_q,
+                           const void* k_cache, const void* v_cache, int cap, const int* cu_k, const int* prefix,
+                           int n_docs, int window, int sinks, void* out, long long out_row, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /* One decode step of the sublayer against the paged 8-bit cache (64 heads):
  * sequence b's new token at position P[b] is appended to its pages (as

@@ -19,7 +19,7 @@ FFN_INTER = 18432
 MODE_PREFILL, MODE_DECODE, MODE_DECODE_LATENT, MODE_FFN, MODE_CHUNK_LATENT, MODE_CHUNK_ABSORBED = 0, 1, 2, 3, 4, 5
 MODE_FOLD = 6
 MODE_PAGED_APPEND, MODE_PAGED_ATTN, MODE_WINDOW_ATTN, MODE_DECODE_PAGED, MODE_PREFILL_PAGED = 8, 9, 10, 11, 12
-MODE_PAGES = 13
+MODE_PAGES, MODE_DOCUMENTS = 13, 14
 STAGES = ["input_norm", "a_proj", "latent", "q_b", "kv_b", "attn", "combine", "absorb_q", "absorb_o", "o_proj",
           "ffn_norm", "gate_up", "down"]
 MAX_STAGES = len(STAGES)
@@ -119,6 +119,7 @@ _SIGS = {
                               ctypes.POINTER(MlaPagedCache), _I, _I, _VP, _VP, _SZ, _VP]),
     "mla_prefill_paged": (_I, [ctypes.POINTER(MlaWeights), ctypes.POINTER(MlaParams), _VP, _I, _I, _I,
                                ctypes.POINTER(MlaPagedCache), _I, _I, _VP, _VP, _SZ, _VP]),
+    "mla_document_attention": (_I, [_VP, _VP, _LL, _I, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _VP, _LL, _VP, _SZ, _VP]),
     "mla_pages_free": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
     "mla_pages_reserve": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
     "mla_pages_fork": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _VP, _SZ, _VP]),
@@ -508,6 +509,28 @@ def mla_window_attention(q, P0: int, k_cache, v_cache, out, workspace, window: i
                                     k_cache.data_ptr(), v_cache.data_ptr(), cap, window, sinks, out.data_ptr(),
                                     _bytes(workspace, dev), workspace.nbytes, s)
     _check(rc, "mla_window_attention")
+
+
+def mla_document_attention(q, cu_q, k_cache, v_cache, out, workspace, cu_k=None, prefix=None, window: int = 0,
+                           sinks: int = 0, params: MlaParams | None = None, stream=None):
+    """q: bf16 [N, 64 * 192], out: bf16 [N, 64 * 128] (rows may be strided); k_cache [64, cap, 192], v_cache
+    [64, cap, 128]; cu_q, cu_k: int32 [n + 1], the rows of q and of the caches where each document begins (cu_k None:
+    cu_q); prefix: int32 [n], tokens that all queries of a document see; workspace of MODE_DOCUMENTS(n, N)."""
+    dev, n = q.get_device(), cu_q.shape[0] - 1
+    s = _stream_on(dev, stream)
+    q_row, out_row = _rows(q, "q", HEADS * QK, dev), _rows(out, "out", HEADS * V, dev)
+    N, cap = q.shape[0], k_cache.shape[1]
+    if out.shape[0] != N:
+        raise ValueError("q and out: need the same number of rows")
+    for x, what, shape in ((k_cache, "k_cache", (HEADS, cap, QK)), (v_cache, "v_cache", (HEADS, cap, V))):
+        if not (x.dtype is _torch.bfloat16 and x.get_device() == dev and x.is_contiguous() and x.shape == shape):
+            raise ValueError(f"{what}: need a contiguous bf16 tensor of shape {shape} on the current device")
+    rc = lib().mla_document_attention(None if params is None else ctypes.byref(params), q.data_ptr(), q_row, N,
+                                      _ints(cu_q, "cu_q", n + 1, dev), k_cache.data_ptr(), v_cache.data_ptr(), cap,
+                                      None if cu_k is None else _ints(cu_k, "cu_k", n + 1, dev),
+                                      None if prefix is None else _ints(prefix, "prefix", n, dev), n, window, sinks,
+                                      out.data_ptr(), out_row, _bytes(workspace, dev), workspace.nbytes, s)
+    _check(rc, "mla_document_attention")
 
 
 def make_page_pool(table, refs, page: int = 64) -> MlaPagePool:

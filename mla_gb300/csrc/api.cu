@@ -20,6 +20,7 @@ constexpr int64_t kMaxTokens = 1 << 24;
 constexpr int kMaxPagedPositions = 1 << 30;
 constexpr int kMaxPoolPages = INT32_MAX / 16;  // pages of 16 tokens whose slots are counted in 31 bits
 constexpr int kMaxPageList = 1 << 20;
+constexpr int kMaxDocuments = 1 << 20;
 
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -78,6 +79,12 @@ Layout make_layout(int mode, int B, int t_or_p, int num_sms, int cap = 0) {
     L.seg = take(segs * sizeof(int));
     L.fresh = take(pages * sizeof(int));
     L.from = take(pages * sizeof(int));
+    L.total = off;
+    return L;
+  }
+  if (mode == MLA_MODE_DOCUMENTS) {  // B documents, t_or_p rows: the plan's head and tiles, each document's first tile
+    L.plan = take(kDocTileBytes * (size_t)(1 + doc_tiles_at_most(t_or_p, B)));
+    L.first = take((size_t)B * sizeof(int));
     L.total = off;
     return L;
   }
@@ -505,6 +512,8 @@ size_t mla_workspace_size(int mode, int B, int t_or_p, int cap) {
     if (t_or_p < 1 || (int64_t)B * t_or_p > kMaxTokens) return 0;
   } else if (mode == MLA_MODE_PAGED_ATTN) {
     if (t_or_p < 1 || t_or_p > kPagedMaxT || B > kMaxTokens) return 0;
+  } else if (mode == MLA_MODE_DOCUMENTS) {
+    if (t_or_p < 1 || t_or_p > kMaxTokens || B > kMaxDocuments) return 0;
   } else if (mode == MLA_MODE_PAGES) {
     if (t_or_p < 1 || t_or_p > kMaxPoolPages || B > kMaxPageList || cap < 0 || cap > kMaxTokens) return 0;
   } else {
@@ -1255,6 +1264,34 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
                     static_cast<const __nv_bfloat16*>(v_cache), static_cast<__nv_bfloat16*>(out), B, T, cap,
                     p.scale, P0, window, sinks};
   return launch_prefill_attention(a, st, sms, stream_) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_document_attention(const mla_params_t* params, const void* q, long long q_row, int N, const int* cu_q,
+                           const void* k_cache, const void* v_cache, int cap, const int* cu_k, const int* prefix,
+                           int n_docs, int window, int sinks, void* out, long long out_row, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const Params p = resolve(params);
+  if (!params_ok(p)) return MLA_ERR_INVALID_ARG;
+  if (!q || !cu_q || !k_cache || !v_cache || !out || N < 1 || N > kMaxTokens || cap < 1 || cap > kMaxTokens ||
+      n_docs < 1 || n_docs > kMaxDocuments || window < 0 || sinks < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!good_stride(q_row) || q_row < MLA_HEADS * MLA_QK || !good_stride(out_row) || out_row < MLA_HEADS * MLA_V ||
+      q_row > 1 << 30 || out_row > 1 << 30)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MLA_ERR_ALIGNMENT;
+  for (const int* x : {cu_q, cu_k, prefix})
+    if (reinterpret_cast<uintptr_t>(x) & 3) return MLA_ERR_ALIGNMENT;
+  const int rc = check_workspace(workspace, workspace_bytes, MLA_MODE_DOCUMENTS, n_docs, N);
+  if (rc) return rc;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return MLA_ERR_CUDA;
+  const Layout L = make_layout(MLA_MODE_DOCUMENTS, n_docs, N, kMaxSmsForSizing);
+  const DocAttnArgs a{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k_cache),
+                      static_cast<const __nv_bfloat16*>(v_cache), static_cast<__nv_bfloat16*>(out), q_row, out_row,
+                      cu_q, cu_k, prefix, N, cap, n_docs, window, sinks, p.scale, at<uint8_t>(workspace, L.plan),
+                      at<int>(workspace, L.first)};
+  const DevStatusHost st{at<uint32_t>(workspace, L.status), kDefaultWaitLimitNs};
+  return launch_document_attention(a, st, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -288,6 +288,31 @@ struct PrefillAttnArgs {
 cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHost& st, int num_sms,
                                      cudaStream_t stream);
 
+// Attention over packed documents: rows cu_q[d] .. cu_q[d + 1] - 1 of q against
+// rows cu_k[d] .. of every head's keys and values (cu_k null: cu_q); see
+// mla_document_attention for the mask.
+struct DocAttnArgs {
+  const __nv_bfloat16* q;   // row n at q + n * q_row: 64 x 192
+  const __nv_bfloat16* k;   // [64, cap, 192]
+  const __nv_bfloat16* v;   // [64, cap, 128]
+  __nv_bfloat16* o;         // row n at o + n * o_row: 64 x 128
+  long long q_row, o_row;
+  const int* cu_q;
+  const int* cu_k;
+  const int* prefix;        // [n_docs] or null
+  int N, cap, n_docs, window, sinks;
+  float scale;
+  uint8_t* plan;            // kDocTileBytes for its head and for each of doc_tiles_at_most() tiles
+  int* first_tile;          // [n_docs] of many documents
+};
+constexpr int kDocTileBytes = 32;
+constexpr int kNoWindow = 1 << 29;
+inline long long doc_tiles_at_most(int N, int n_docs) {
+  const long long n = (long long)N / 128 + n_docs;  // whole tiles, and a partial one a document
+  return n < N ? n : N;
+}
+cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream);
+
 struct DecodeAttnArgs {
   const __nv_bfloat16* q;   // [B, 64*192]
   const __nv_bfloat16* k;   // [B, 64, cap, 192]

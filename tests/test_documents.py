@@ -1,0 +1,290 @@
+"""Attention over packed documents.
+
+The reference is the definition in include/mla.h in 64 bits, document by document.  Tolerances count roundings, as for
+the attention under a window: the output's to bf16 is off by at most 2^-8 of it, each probability's (relative to the
+row's sum, which is not rounded) by 2^-8 p, i.e. the output by 2^-8 sum p |v| more; float32 scores, exponentials and
+sums by 2^-14 of that sum."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import mla_gb300 as m
+from test_paged import FAKE, f64, normal
+
+gpu = pytest.mark.gpu
+
+
+# ---- refusals (CPU: nothing is enqueued) --------------------------------------------------------------------
+def attend_c(**kw):
+    a = dict(params=None, q=FAKE, qr=64 * 192, N=100, cq=FAKE + 4096, k=FAKE + (1 << 20), v=FAKE + (2 << 20), cap=200,
+             ck=FAKE + 8192, pre=FAKE + 12288, n=3, window=0, sinks=0, out=FAKE + (3 << 20), outr=64 * 128,
+             ws=FAKE + (4 << 20), wsb=1 << 16)
+    a.update(kw)
+    return m.lib().mla_document_attention(a["params"], a["q"], a["qr"], a["N"], a["cq"], a["k"], a["v"], a["cap"], a["ck"],
+                                          a["pre"], a["n"], a["window"], a["sinks"], a["out"], a["outr"], a["ws"],
+                                          a["wsb"], None)
+
+
+def test_refusals():
+    for kw in (dict(q=None), dict(cq=None), dict(k=None), dict(v=None), dict(out=None), dict(N=0), dict(N=(1 << 24) + 1),
+               dict(cap=0), dict(cap=(1 << 24) + 1), dict(n=0), dict(n=(1 << 20) + 1), dict(window=-1), dict(sinks=-1),
+               dict(qr=64 * 192 - 8), dict(qr=64 * 192 + 4), dict(outr=64 * 128 - 8), dict(outr=64 * 128 + 2),
+               dict(qr=(1 << 30) + 8), dict(outr=-8)):
+        assert attend_c(**kw) == -1, kw
+    for kw in (dict(q=FAKE + 2), dict(k=FAKE + 8), dict(v=FAKE + 8), dict(out=FAKE + 8), dict(cq=FAKE + 2),
+               dict(ck=FAKE + 1), dict(pre=FAKE + 3), dict(ws=FAKE + 8)):
+        assert attend_c(**kw) == -2, kw
+    assert attend_c(ws=None) == -3 and attend_c(wsb=256) == -3
+    bad = m.MlaParams(1e-6, 10000.0, -1.0, None, None)
+    assert attend_c(params=ctypes.byref(bad)) == -1
+
+
+def test_workspace_sizes():
+    assert m.workspace_size(m.MODE_DOCUMENTS, 4, 10000) > m.workspace_size(m.MODE_DOCUMENTS, 4, 100)
+    assert m.workspace_size(m.MODE_DOCUMENTS, 400, 10000) > m.workspace_size(m.MODE_DOCUMENTS, 4, 10000)
+    for n, N in ((0, 1), (1, 0), ((1 << 20) + 1, 5), (1, (1 << 24) + 1)):
+        assert m.lib().mla_workspace_size(m.MODE_DOCUMENTS, n, N, 0) == 0
+
+
+# ---- on the GPU ---------------------------------------------------------------------------------------------
+def ints(x):
+    import torch
+    return torch.tensor([int(v) for v in x], dtype=torch.int32, device="cuda")
+
+
+def starts(lengths, first=0):
+    return [first] + list(first + np.cumsum(lengths))
+
+
+def visible(n, L, prefix, window, sinks):
+    i, j = np.arange(L - n, L)[:, None], np.arange(L)[None, :]
+    seen = j <= i
+    if window:
+        seen &= (i - j < window) | (j < sinks)
+    return seen | (j < prefix)
+
+
+def reference(q, k, v, n, L, prefix, window, sinks, scale=1 / math.sqrt(192)):
+    """One document and head in 64 bits: the output and sum p |v|; rows that see nothing are zeros."""
+    seen = visible(n, L, prefix, window, sinks)
+    s = np.where(seen, q @ k.T * scale, -np.inf)
+    top = s.max(1, keepdims=True, initial=-np.inf)
+    w = np.exp(s - np.where(np.isfinite(top), top, 0))
+    w /= np.maximum(w.sum(1, keepdims=True), 1e-300)
+    return w @ v, w @ np.abs(v)
+
+
+def check(got, q, k, v, cu_q, cu_k, prefix, window, sinks, heads=(0, 17, 63), scale=1 / math.sqrt(192)):
+    """got [N, 64 * 128], q [N, 64 * 192] and the caches in 64 bits."""
+    assert np.isfinite(got[cu_q[0]:cu_q[-1]]).all()
+    for d in range(len(cu_q) - 1):
+        a, b, e, f = cu_q[d], cu_q[d + 1], cu_k[d], cu_k[d + 1]
+        p = min(max(prefix[d], 0), f - e) if prefix is not None else 0
+        for h in heads:
+            ref, mag = reference(q[a:b, h * 192:h * 192 + 192], k[h, e:f], v[h, e:f], b - a, f - e, p, window, sinks,
+                                 scale)
+            diff = np.abs(got[a:b, h * 128:h * 128 + 128] - ref)
+            assert (diff <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -14) * mag).all(), (d, h, diff.max())
+
+
+def run(q, k, v, cu_q, cu_k, prefix=None, window=0, sinks=0, status=0, params=None, fill=float("nan")):
+    import torch
+    out = torch.full((q.shape[0], 64 * 128), fill, dtype=torch.bfloat16, device="cuda")
+    ws = m.alloc_workspace(m.MODE_DOCUMENTS, len(cu_q) - 1, q.shape[0]).fill_(0xa5)
+    m.mla_document_attention(q, ints(cu_q), k, v, out, ws, cu_k=None if cu_k is None else ints(cu_k),
+                             prefix=None if prefix is None else ints(prefix), window=window, sinks=sinks, params=params)
+    assert m.mla_device_status(ws) == status
+    return out
+
+
+CASES = [
+    # new tokens, cached ones before them, prefix, window, sinks
+    ([1], [0], None, 0, 0),
+    ([128], [0], None, 0, 0),
+    ([129], [0], None, 0, 0),
+    ([300, 1, 17, 128, 64], [0] * 5, None, 0, 0),
+    ([5, 0, 33, 0, 0, 70], [0, 7, 0, 0, 200, 1], None, 0, 0),
+    ([1, 1, 1, 1, 1], [0, 500, 127, 128, 129], None, 0, 0),
+    ([100, 260, 31], [333, 1, 128], None, 0, 0),
+    ([200, 40, 128, 9], [0, 300, 5, 0], [77, 310, 0, 9], 0, 0),
+    ([150, 150], [0, 0], [150, 999], 0, 0),
+    ([300, 90, 400], [0, 222, 50], None, 64, 0),
+    ([300, 90, 400], [0, 222, 50], None, 1, 0),
+    ([300, 90, 400], [0, 222, 50], None, 100, 4),
+    ([300, 90, 400, 513], [100, 222, 50, 0], [10, 20, 130, 200], 33, 150),
+    ([260, 700], [900, 10], [140, 0], 50, 3),
+    ([40] * 30, list(range(0, 300, 10)), [i % 41 for i in range(30)], 0, 0),
+    ([513], [1000], [1513], 0, 0),
+    ([64, 64], [0, 0], [0, 0], 1 << 30, 1 << 30),
+]
+
+
+@gpu
+@pytest.mark.parametrize("new,past,prefix,window,sinks", CASES)
+def test_values(gpu_available, new, past, prefix, window, sinks):
+    keys = [a + b for a, b in zip(new, past)]
+    cu_q, cu_k = starts(new), starts(keys)
+    q, k, v = normal(1, cu_q[-1], 64 * 192), normal(2, 64, cu_k[-1], 192), normal(3, 64, cu_k[-1], 128)
+    out = run(q, k, v, cu_q, cu_k, prefix, window, sinks)
+    check(f64(out), f64(q), f64(k), f64(v), cu_q, cu_k, prefix, window, sinks)
+
+
+@gpu
+@pytest.mark.parametrize("new,keys,prefix", [([10, 200, 5], [3, 100, 0], None), ([10, 200, 300], [3, 100, 130], [2, 0, 130]),
+                                             ([130], [1], None), ([3, 3], [0, 0], [4, 4])])
+def test_more_queries_than_keys(gpu_available, new, keys, prefix):
+    """Rows before the document's first key see nothing (but a prefix): zeros."""
+    cu_q, cu_k = starts(new), starts(keys)
+    q, k, v = normal(1, cu_q[-1], 64 * 192), normal(2, 64, max(cu_k[-1], 1), 192), normal(3, 64, max(cu_k[-1], 1), 128)
+    out = run(q, k, v, cu_q, cu_k, prefix)
+    check(f64(out), f64(q), f64(k), f64(v), cu_q, cu_k, prefix, 0, 0)
+    if prefix is None:
+        assert bool((out[:new[0] - keys[0]] == 0).all())
+
+
+@gpu
+def test_without_keys_of_their_own(gpu_available):
+    """cu_k left out: queries and keys share their rows; offsets that begin behind the first row, rows behind the last
+    document, rows with strides."""
+    import torch
+    new = [200, 3, 140]
+    cu = starts(new, 7)
+    wide_q, wide_o = normal(1, cu[-1] + 30, 64 * 192 + 16), torch.full((cu[-1] + 30, 64 * 128 + 8), 3.0,
+                                                                       dtype=torch.bfloat16, device="cuda")
+    q, out = wide_q[:, :64 * 192], wide_o[:, :64 * 128]
+    k, v = normal(2, 64, cu[-1] + 50, 192), normal(3, 64, cu[-1] + 50, 128)
+    ws = m.alloc_workspace(m.MODE_DOCUMENTS, 3, q.shape[0])
+    m.mla_document_attention(q, ints(cu), k, v, out, ws)
+    assert m.mla_device_status(ws) == 0
+    check(f64(out.contiguous()), f64(q.contiguous()), f64(k), f64(v), cu, cu, None, 0, 0)
+    assert bool((wide_o[:7] == 3).all()) and bool((wide_o[cu[-1]:] == 3).all()) and bool((wide_o[:, 64 * 128:] == 3).all())
+
+
+@gpu
+def test_neighbours_do_not_matter(gpu_available):
+    """NaN and infinities in the other documents, in front of the first and behind the last: the same bits."""
+    import torch
+    new, past = [37, 130, 260, 5], [11, 0, 77, 300]
+    keys = [a + b for a, b in zip(new, past)]
+    cu_q, cu_k = starts(new, 3), starts(keys, 9)
+    q, k, v = normal(1, cu_q[-1] + 20, 64 * 192), normal(2, 64, cu_k[-1] + 20, 192), normal(3, 64, cu_k[-1] + 20, 128)
+    for kw in (dict(), dict(prefix=[5, 0, 300, 305]), dict(window=40, sinks=3)):
+        clean = run(q, k, v, cu_q, cu_k, **kw)
+        for d in range(4):
+            q2, k2, v2 = q.clone(), k.clone(), v.clone()
+            for value in (float("nan"), float("inf"), -float("inf")):
+                for x, cu, axis in ((q2, cu_q, 0), (k2, cu_k, 1), (v2, cu_k, 1)):
+                    rows = torch.ones(x.shape[axis], dtype=torch.bool, device="cuda")
+                    rows[cu[d]:cu[d + 1]] = False
+                    if axis == 0:
+                        x[rows] = value
+                    else:
+                        x[:, rows] = value
+                got = run(q2, k2, v2, cu_q, cu_k, **kw)
+                assert torch.equal(got[cu_q[d]:cu_q[d + 1]], clean[cu_q[d]:cu_q[d + 1]]), (kw, d, value)
+
+
+@gpu
+def test_keys_behind_the_last_query(gpu_available):
+    """Keys that no query of a tile sees (behind a short prefix's end): whatever they hold, the rows before them keep
+    their bits."""
+    import torch
+    q, k, v = normal(1, 256, 64 * 192), normal(2, 64, 256, 192), normal(3, 64, 256, 128)
+    clean = run(q, k, v, [0, 256], None, [20])
+    k[:, 128:], v[:, 128:] = float("nan"), float("inf")
+    assert torch.equal(run(q, k, v, [0, 256], None, [20])[:128], clean[:128])
+
+
+@gpu
+@pytest.mark.parametrize("cu_q,cu_k", [([0, 50, 40, 100], None), ([-1, 50, 60, 100], None), ([0, 50, 60, 101], None),
+                                       ([0, 50, 60, 100], [0, 30, 90, 121]), ([0, 50, 60, 100], [0, 90, 30, 120]),
+                                       ([0, 50, 60, 100], [-5, 0, 30, 120]),
+                                       ([0, 1 << 30, -(1 << 30), 100], None)])
+def test_offsets_out_of_range_write_nothing(gpu_available, cu_q, cu_k):
+    q, k, v = normal(1, 100, 64 * 192), normal(2, 64, 120, 192), normal(3, 64, 120, 128)
+    out = run(q, k, v, cu_q, cu_k, status=-1, fill=5.0)
+    assert bool((out == 5).all())
+
+
+@gpu
+def test_against_the_causal_and_the_windowed_kernel(gpu_available):
+    """Documents of equal lengths give what mla_window_attention gives, sequence by sequence."""
+    import torch
+    B, T, P0 = 3, 300, 41
+    L = P0 + T
+    q, k, v = normal(1, B, T, 64 * 192), normal(2, B, 64, L, 192), normal(3, B, 64, L, 128)
+    pk, pv = (x.transpose(0, 1).reshape(64, B * L, -1).contiguous() for x in (k, v))
+    for window, sinks in ((90, 7), (1 << 20, 0)):
+        a = torch.empty((B, T, 64 * 128), dtype=torch.bfloat16, device="cuda")
+        m.mla_window_attention(q, P0, k, v, a, m.alloc_workspace(m.MODE_WINDOW_ATTN, B, T), window=window, sinks=sinks)
+        b = run(q.view(B * T, -1), pk, pv, [T * i for i in range(B + 1)], [L * i for i in range(B + 1)], None, window, sinks)
+        x, y = f64(a).reshape(B * T, -1), f64(b)
+        mag = np.abs(y).max()
+        assert np.abs(x - y).max() <= 2.0 ** -6 * mag
+
+
+@gpu
+def test_many_documents(gpu_available):
+    """More documents than the plan keeps in shared memory, most of them of a token or none."""
+    rng = np.random.default_rng(1)
+    new = np.where(rng.random(6000) < 0.3, 0, 1)
+    new[[5, 700, 5999]] = [140, 3, 33]
+    past = rng.integers(0, 3, 6000)
+    past[700] = 400
+    cu_q, cu_k = starts(new), starts(new + past)
+    q, k, v = normal(1, cu_q[-1], 64 * 192), normal(2, 64, cu_k[-1], 192), normal(3, 64, cu_k[-1], 128)
+    out = run(q, k, v, cu_q, cu_k)
+    check(f64(out), f64(q), f64(k), f64(v), cu_q, cu_k, None, 0, 0, heads=(5,))
+
+
+@gpu
+def test_moving_maxima_and_scale(gpu_available):
+    """Scores that grow along the keys (the running maximum moves in every tile), and another scale."""
+    new, past = [200, 150], [500, 300]
+    cu_q, cu_k = starts(new), starts([700, 450])
+    q, k, v = normal(1, 350, 64 * 192), normal(2, 64, 1150, 192), normal(3, 64, 1150, 128)
+    q.view(350, 64, 192)[..., 5] = 3.0
+    for d in range(2):
+        n = cu_k[d + 1] - cu_k[d]
+        import torch
+        k[:, cu_k[d]:cu_k[d + 1], 5] = torch.linspace(-60, 60, n, device="cuda").to(torch.bfloat16)
+    for scale in (1 / math.sqrt(192), 0.3):
+        out = run(q, k, v, cu_q, cu_k, params=m.make_params(softmax_scale=scale))
+        check(f64(out), f64(q), f64(k), f64(v), cu_q, cu_k, None, 0, 0, scale=scale)
+
+
+@gpu
+def test_captured_and_on_two_streams(gpu_available):
+    """A captured call replayed with other offsets, and two calls at once on streams of their own."""
+    import torch
+    q, k, v = normal(1, 400, 64 * 192), normal(2, 64, 400, 192), normal(3, 64, 400, 128)
+    plans = [[0, 400, 400, 400], [0, 100, 101, 380], [5, 5, 205, 399]]
+    want = [run(q, k, v, cu, None, fill=1.0) for cu in plans]
+    cu, out = ints(plans[0]), torch.empty((400, 64 * 128), dtype=torch.bfloat16, device="cuda")
+    ws = m.alloc_workspace(m.MODE_DOCUMENTS, 3, 400)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        m.mla_document_attention(q, cu, k, v, out, ws)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        m.mla_document_attention(q, cu, k, v, out, ws)
+    for i in (1, 2, 0, 1):
+        cu.copy_(ints(plans[i]))
+        out.fill_(1.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]), i
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.full_like(out, 1.0) for _ in range(2)]
+    cus, wss = [ints(p) for p in plans[:2]], [m.alloc_workspace(m.MODE_DOCUMENTS, 3, 400) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            m.mla_document_attention(q, cus[i], k, v, outs[i], wss[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
