@@ -1,0 +1,831 @@
+// Attention over packed documents for MLA heads (qk = 192, v = 128) on tcgen05.
+//
+// "Mix and project" page, code excerpt: scores = Q K^T * softmax_scale plus
+// the mask, softmax in float32, then P V; here for several sequences packed one
+// after the other, each seeing its own keys only (mla_document_attention).
+// Computed in the flash form: online softmax over 128-key tiles.
+//
+// A plan kernel lists the documents' query tiles of up to 128 rows, a tile
+// never holding rows of two documents, heaviest first.  Persistent: one CTA per
+// SM takes items (tile, head) from an atomic counter, in groups of heads whose
+// K/V stay in L2.  An item's key tiles begin at the document's (or the window's)
+// first key.  V rows behind the last key that the tile's queries see would be
+// another document's: the P.V product takes only the 16-key steps up to that
+// key, and the V producer's warp clears the rows behind it in the last step, so
+// that nothing of a neighbour (a NaN times zero among it) reaches the sum.  Rows
+// of the next document in the Q tile are computed and not stored; a row that
+// sees no key has the sum zero and is stored as zeros.
+//
+// Warp roles (384 threads):
+//   warp 0   work scheduler (counter -> a 4-slot ring of items), then TMA: the
+//            item's Q tile, then its K tiles into a 2-slot ring
+//   warp 1   TMEM allocation; one lane issues S_x = Q K^T (M=128 N=128 K=192)
+//            into score buffer x & 1, x counting this CTA's key tiles: Q's 128
+//            "nope" dimensions from tensor memory, the 64 RoPE ones from one of
+//            two shared-memory slots
+//   warp 2   TMA: V tiles into a 2-slot ring, and their cut
+//   warp 3   one lane issues O += P_x V_x (M=128 N=128 K=128), P from tensor memory
+//   warps 4..7, 8..11   two softmax groups, one thread a query row.  Group g takes
+//            the key tiles with x & 1 = g: while one waits for its scores, looks
+//            for the maximum or stores P, the other one's exponentials fill the
+//            special-function units (1,024 cycles a tile, of 1,280 that its
+//            products take).  Both express P and O in one reference a row, the
+//            running maximum with lazy rescaling (it moves only when the maximum
+//            grows by more than 2^8, so P stays <= 256): the tile before hands its
+//            reference on through shared memory.  Each group sums its own tiles'
+//            rows.  At an item's end the group without the last tile hands over its
+//            sums, copies the next item's Q into tensor memory and goes on to that
+//            item's first tile, which is its own; the other one writes O / l.
+// (Two threads a row on the same tile, as the windowed prefill has them, do
+// their waits, maxima and exponentials all at the same time: 5 documents of up to
+// 4,096 tokens 820 us.)
+// Registers: the four control warps give theirs up to the softmax groups, which
+// hold a row's 128 scores.
+#include "common.cuh"
+#include "internal.h"
+
+namespace mla {
+
+namespace {
+
+constexpr int kKeys = 96;                        // of a key tile
+constexpr uint32_t kAtom = 128 * 128;            // 128 rows x 64 bf16
+constexpr uint32_t kKeyAtom = kKeys * 128;       // 96 rows x 64 bf16
+constexpr uint32_t kQOff = 0;                    // Q: 3 atoms (staging)
+constexpr uint32_t kOOff = 3 * kAtom;            // O: 2 atoms (staging)
+constexpr int kHalf = kKeys / 2;
+constexpr uint32_t kHalfAtom = kHalf * 128;      // 48 rows x 64 bf16
+constexpr int kKSlots = 7, kVSlots = 5;          // of a third of a K tile (64 dimensions), of half a V tile (48 keys)
+constexpr uint32_t kKOff = 5 * kAtom;            // slots of a key atom
+constexpr uint32_t kVOff = kKOff + kKSlots * kKeyAtom;  // slots of 2 half atoms (vdim 0-63, 64-127)
+constexpr uint32_t kBarOff = kVOff + kVSlots * 2 * kHalfAtom;
+constexpr uint32_t kRefOff = kBarOff + 768;      // references by tile parity, 2 x 128 fp32
+constexpr uint32_t kSumOff = kRefOff + 1024;     // sums and references handed over, 128 x 2 fp32
+constexpr uint32_t kTileOff = kSumOff + 1024;    // the query tiles of the item ring
+constexpr uint32_t kSmemBytes = kTileOff + 256;
+static_assert(kSmemBytes <= 232448, "document attention shared memory");
+// tensor memory columns: S_0, S_1 (fp32), O (fp32), P_0, P_1 (bf16 pairs), Q (bf16 pairs)
+constexpr uint32_t kTmS = 0, kTmO = 2 * kKeys, kTmP = kTmO + 128, kTmQ = kTmP + kKeys;
+static_assert(kTmQ + 96 == 512, "tensor memory columns");
+constexpr int kThreads = 384;
+constexpr float kRescaleThreshold = 8.0f;        // log2 units
+constexpr int kItemRing = 4;
+
+// A warp's bounded wait, in few instructions: 2^21 tries (tens of milliseconds at
+// least, where the longest wait there is takes microseconds).  A role whose wait
+// gives up stops, and says so at its end.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  int tries = 1 << 21;
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (--tries == 0) return false;
+  return true;
+}
+
+// A role's place in a ring of N slots.
+template <int N>
+struct Place {
+  int slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+struct Bars {
+  uint64_t q_full, q_tmem, qn_empty, q_free;
+  uint64_t item_full[kItemRing], item_empty[kItemRing];
+  uint64_t k_full[kKSlots], k_empty[kKSlots];
+  uint64_t v_full[kVSlots], v_empty[kVSlots], v_cut[kVSlots];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[2], pv_done[2];
+  // per quarter of the rows (a warp of each group), so that a warp that does not
+  // wait for a phase has completed it itself
+  uint64_t ref[2][4], sum[4], o_free[4], o_stored[4];
+  uint64_t drain_s, drain_pv;
+  uint32_t tmem_slot;
+  int abort;  // the role whose wait gave up
+};
+static_assert(sizeof(Bars) <= 768, "barrier block");
+
+// A document's query tile, as the plan lists it: its rows q_row .. q_row + rows
+// - 1 sit at positions pos .. (below 0: before the document's first key), its
+// keys begin at row k_row; the first `prefix` are seen by every query.  Its key
+// tiles: first n_sink tiles over keys 0 .. n_first - 1, which are seen however far
+// back they are (the prefix, the sinks), then tiles from w0 on, the window's first
+// key; where the former reach the window, the tiles run from key 0.  `end` is the
+// key behind the last one that the tile's queries see.
+struct __align__(16) DocTile {
+  int q_row, rows, k_row, pos, prefix, head;
+  int n_kv, w0, n_first, n_sink, end, pad;
+  __device__ __forceinline__ void set_keys(int window, int sinks) {
+    const int last = pos + rows;  // behind the last query's position
+    w0 = max(0, pos - window + 1);
+    end = max(last, prefix);
+    n_first = max(prefix, min(sinks, last));
+    if (n_first >= w0) w0 = n_first = 0;
+    n_first = max(n_first, 0);
+    n_sink = (n_first + kKeys - 1) / kKeys;
+    // (one tile of nothing where no key is seen: its item stores zeros)
+    n_kv = max(1, n_sink + max(0, end - w0 + kKeys - 1) / kKeys);
+  }
+  // first key of key tile j
+  __device__ __forceinline__ int key0(int j) const { return j < n_sink ? j * kKeys : w0 + (j - n_sink) * kKeys; }
+  // its keys that some query may see: those behind them are not the document's, or nobody's
+  __device__ __forceinline__ int keys(int j) const {
+    return max(0, min(kKeys, (j < n_sink ? n_first : end) - key0(j)));
+  }
+};
+static_assert(sizeof(DocTile) == kDocTileBytes && kItemRing * sizeof(DocTile) <= 256, "tiles of the item ring");
+// The plan: this, then the tiles, heaviest first.
+struct DocPlan {
+  int n_tiles, group_log, pad[10];
+};
+static_assert(sizeof(DocPlan) == kDocTileBytes, "the plan's head is as long as a tile");
+
+// The query tile and head of work item w: groups of 2^log heads, in a group tile
+// after tile, in a tile head after head.
+__device__ __forceinline__ void doc_item(int w, int n_tiles, int log, int& tile, int& head) {
+  const int per = n_tiles << log, g = w / per, r = w - g * per;
+  tile = r >> log;
+  head = (g << log) + (r & ((1 << log) - 1));
+}
+
+// One lane of a whole warp.  The control warps run their loops as warps and let one
+// lane issue, so that the operands of the copies and products are uniform values:
+// with the loops in lane 0 alone the twelve products of a tile's scores took 1,255
+// cycles to issue (with three waits), so 661.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// A warp reads item `it` from the ring, then releases the slot.  False: a wait gave up.
+__device__ __forceinline__ bool read_item(uint8_t* smem, Bars* bar, int it, DocTile& tile) {
+  const int slot = it % kItemRing;
+  if (!wait_for(&bar->item_full[slot], (it / kItemRing) & 1)) return false;
+  tile = reinterpret_cast<const DocTile*>(smem + kTileOff)[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bar->item_empty[slot]);
+  return true;
+}
+
+// the lowest n bits of 32 (none for n < 0, all for n > 32)
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  uint32_t m;
+  asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
+  return m;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    document_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, float sl2, int window,
+                     int sinks, int* __restrict__ work, const uint8_t* __restrict__ plan, __nv_bfloat16* __restrict__ o,
+                     long long o_row, const DevStatus st) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bar = reinterpret_cast<Bars*>(smem + kBarOff);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // (uniform to the compiler)
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar->q_full, 1);
+    mbar_init(&bar->q_tmem, 128);
+    mbar_init(&bar->qn_empty, 4);
+    mbar_init(&bar->q_free, 1);
+    for (int i = 0; i < kItemRing; ++i) {
+      mbar_init(&bar->item_full[i], 1);
+      mbar_init(&bar->item_empty[i], 3 + 8);  // V producer, S issuer, P.V issuer, softmax warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->p_full[i], 128);
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->s_free[i], 128);
+      mbar_init(&bar->pv_done[i], 1);
+      for (int q = 0; q < 4; ++q) mbar_init(&bar->ref[i][q], 32);
+    }
+#pragma unroll 1
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
+    }
+#pragma unroll 1
+    for (int i = 0; i < kVSlots; ++i) {
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
+      mbar_init(&bar->v_cut[i], 1);
+    }
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(&bar->sum[q], 32);
+      mbar_init(&bar->o_free[q], 32);
+      mbar_init(&bar->o_stored[q], 1);
+    }
+    mbar_init(&bar->drain_s, 1);
+    mbar_init(&bar->drain_pv, 1);
+    bar->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  bool ok = true;
+  if (warp == 0) {
+    // ---- work scheduler, Q and K producer ----
+    if (elected()) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+    }
+    const DocPlan* head = reinterpret_cast<const DocPlan*>(plan);
+    const int n_tiles = head->n_tiles, group_log = head->group_log, n_items = 64 * n_tiles;
+    const int* tiles = reinterpret_cast<const int*>(plan + sizeof(DocPlan)) + min(lane, (int)sizeof(DocTile) / 4 - 1);
+    DocTile* const ring = reinterpret_cast<DocTile*>(smem + kTileOff);
+    Place<kKSlots> k;
+    int q_loads = 0;
+    // Item it + 1 is posted to the ring, where every role finds it, before item `it` is
+    // loaded; its tile was fetched (a word a lane) after the item before, its index asked
+    // for before that.
+    int index = lane == 0 ? atomicAdd(work, 1) : 0, word = 0;
+#pragma unroll 1
+    for (int it = -2;; ++it) {
+      const DocTile& tile = ring[(it + kItemRing) % kItemRing];
+      DocTile& next = ring[(it + 1 + kItemRing) % kItemRing];
+      if (it >= -1) {
+        const int slot = (it + 1) % kItemRing;
+        if (it + 1 >= kItemRing && !(ok = wait_for(&bar->item_empty[slot], ((it + 1) / kItemRing - 1) & 1))) break;
+        if (lane < (int)sizeof(DocTile) / 4) reinterpret_cast<int*>(&next)[lane] = word;
+        __syncwarp();
+        if (elected()) mbar_arrive(&bar->item_full[slot]);  // release
+        __syncwarp();
+      }
+      if (it >= 0 && tile.rows == 0) break;
+      const int after = lane == 0 ? atomicAdd(work, 1) : 0;
+      // K tiles, 64 dimensions at a time; behind the second one (at once, for the first item)
+      // the next item's Q, into the staging atoms once this one's has been copied into tensor
+      // memory: by then it has, and the copy has the rest of the item to arrive
+      const int n_kv = it < 0 ? 0 : tile.n_kv, q_at = min(2, n_kv);
+#pragma unroll 1
+      for (int j = 0; ok; ++j) {
+        if (j == q_at && it >= -1 && next.rows > 0) {
+          if (it >= 0 && !(ok = wait_for(&bar->qn_empty, it & 1))) break;
+          if (elected()) {
+            mbar_arrive_expect_tx(&bar->q_full, 3 * kAtom);
+            for (int c = 0; c < 3; ++c)
+              tma_load_3d(smem + kQOff + c * kAtom, &tmQ, &bar->q_full, next.head * 192 + 64 * c, next.q_row, 0);
+          }
+          __syncwarp();
+          ++q_loads;
+        }
+        if (j == n_kv) break;
+        const int key = tile.k_row + tile.key0(j);
+#pragma unroll 1
+        for (int c = 0; c < 192; c += 64, k.next()) {
+          if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
+          if (elected()) {
+            mbar_arrive_expect_tx(&bar->k_full[k.slot], kKeyAtom);
+            tma_load_3d(smem + kKOff + k.slot * kKeyAtom, &tmK, &bar->k_full[k.slot], c, key, tile.head);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      index = __shfl_sync(0xffffffffu, index, 0);
+      word = 0;  // (no rows: the end)
+      if (index < n_items) {
+        int at, of;
+        doc_item(index, n_tiles, group_log, at, of);
+        word = tiles[at * (int)(sizeof(DocTile) / 4)];
+        if (lane == (int)offsetof(DocTile, head) / 4) word = of;
+      }
+      index = after;
+    }
+    // no copy may still be in flight into shared memory: the last round of the ring
+    if (q_loads) ok &= wait_for(&bar->q_full, (q_loads - 1) & 1);
+#pragma unroll 1
+    for (int i = 0; i < kKSlots; ++i, k.next()) ok &= wait_for(&bar->k_full[k.slot], k.phase ^ 1);
+  } else if (warp == 1) {
+    // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
+    constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
+    const uint32_t k_addr = smem_u32(smem + kKOff);
+    int x = 0;
+    Place<kKSlots> k;
+#pragma unroll 1
+    for (int it = 0; ok; ++it) {
+      DocTile tile;
+      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+      if (!(ok = wait_for(&bar->q_tmem, it & 1))) break;  // this item's Q in tensor memory
+#pragma unroll 1
+      for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
+        const int sb = x & 1;
+        // the group has read the buffer's previous scores (tile x - 2)
+        if (x > 1 && !(ok = wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))) break;
+        // 64 dimensions at a time, as they arrive
+#pragma unroll 1
+        for (int c = 0; c < 3; ++c, k.next()) {
+          if (!(ok = wait_for(&bar->k_full[k.slot], k.phase))) break;
+          tc_fence_after();
+          const uint64_t kb = sdesc_sw128(k_addr + k.slot * kKeyAtom, 16, 1024);
+          if (elected()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_ts(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc_s,
+                           c > 0 || kk > 0 ? 1u : 0u);
+            umma_commit(&bar->k_empty[k.slot]);
+            if (c == 2) umma_commit(&bar->s_full[sb]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (elected()) umma_commit(&bar->q_free);  // the item's S are done: its Q may be replaced
+      __syncwarp();
+    }
+    if (elected()) umma_commit(&bar->drain_s);
+    __syncwarp();
+    ok &= wait_for(&bar->drain_s, 0);
+  } else if (warp == 2) {
+    // ---- V producer: half tiles, and clears what lies behind the last key ----
+    Place<kVSlots> v;
+    if (elected()) tma_prefetch_desc(&tmV);
+#pragma unroll 1
+    for (int it = 0; ok; ++it) {
+      DocTile tile;
+      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+#pragma unroll 1
+      for (int h = 0; h < 2 * tile.n_kv; ++h) {
+        // its keys; a second half that no query sees is left out
+        const int keys = tile.keys(h >> 1) - (h & 1) * kHalf;
+        if ((h & 1) && keys <= 0) continue;
+        uint8_t* const at = smem + kVOff + v.slot * 2 * kHalfAtom;
+        if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
+        if (elected()) {
+          mbar_arrive_expect_tx(&bar->v_full[v.slot], 2 * kHalfAtom);
+          const int key = tile.k_row + tile.key0(h >> 1) + (h & 1) * kHalf;
+          tma_load_3d(at, &tmV, &bar->v_full[v.slot], 0, key, tile.head);
+          tma_load_3d(at + kHalfAtom, &tmV, &bar->v_full[v.slot], 64, key, tile.head);
+        }
+        __syncwarp();
+        if (keys < kHalf && (keys == 0 || (keys & 15))) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
+          if (!(ok = wait_for(&bar->v_full[v.slot], v.phase))) break;
+          uint8_t* const mine = at + ((lane >> 3) & 1) * kHalfAtom + (lane & 7) * 16;
+#pragma unroll 1
+          for (int r = keys + (lane >> 4); r < max(16, (keys + 15) & ~15); r += 2)
+            *reinterpret_cast<uint4*>(mine + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elected()) mbar_arrive(&bar->v_cut[v.slot]);
+          __syncwarp();
+        }
+        v.next();
+      }
+    }
+#pragma unroll 1
+    for (int i = 0; i < kVSlots; ++i, v.next()) ok &= wait_for(&bar->v_full[v.slot], v.phase ^ 1);
+  } else if (warp == 3) {
+    // ---- P.V issuer: O += P_x V_x ----
+    constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
+    const uint32_t v_addr = smem_u32(smem + kVOff);
+    int x = 0;
+    Place<kVSlots> v;
+    uint32_t cuts = 0;  // parity of each slot's cuts so far
+#pragma unroll 1
+    for (int it = 0; ok; ++it) {
+      DocTile tile;
+      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+#pragma unroll 1
+      for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
+        const int sb = x & 1;
+        // P_x is written (and, for an item's first tile, the previous item's O read)
+        if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
+        // the 16-key steps that hold a key (one where there is none: O becomes zeros), half a
+        // tile at a time, the last step's other rows cleared
+        const int all = tile.keys(j);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int keys = all - h * kHalf;
+          if (h && keys <= 0) break;
+          if (!(ok = wait_for(&bar->v_full[v.slot], v.phase))) break;
+          if (keys < kHalf && (keys == 0 || (keys & 15))) {
+            if (!(ok = wait_for(&bar->v_cut[v.slot], (cuts >> v.slot) & 1))) break;
+            cuts ^= 1u << v.slot;
+          }
+          tc_fence_after();
+          const uint64_t vb = sdesc_sw128(v_addr + v.slot * 2 * kHalfAtom, kHalfAtom, 1024);
+          if (elected()) {
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              if (kk * 16 < max(keys, 1))
+                umma_bf16_ts(tmem + kTmO, tmem + kTmP + sb * kHalf + h * (kHalf / 2) + kk * 8, vb + kk * 128, idesc_pv,
+                             (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bar->v_empty[v.slot]);
+            if (h == 1 || all <= kHalf) umma_commit(&bar->pv_done[sb]);
+          }
+          __syncwarp();
+          v.next();
+        }
+      }
+    }
+    if (elected()) umma_commit(&bar->drain_pv);
+    __syncwarp();
+    ok &= wait_for(&bar->drain_pv, 0);
+  } else {
+    // ---- softmax groups, one thread a query row ----
+    const int g = (warp >> 2) - 1;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    float* const refs = reinterpret_cast<float*>(smem + kRefOff) + row;    // + 128 x parity of the tile
+    float2* const sums = reinterpret_cast<float2*>(smem + kSumOff) + row;
+    auto wait = [&](uint64_t& b, int phase) { return wait_for(&b, phase & 1); };
+    // Item by item, this group's tiles of each.  At an item's end the group with the
+    // last tile `ends` it: it writes O / l.  The other group has copied the next item's
+    // Q into tensor memory by then, while it worked on its own last tile (every S of the
+    // item is done or on its way at that time), and goes on to that item's first tile,
+    // which is its own.  The first pass (it = -1) has no tiles: its group 0 copies the
+    // first Q.
+    int x0 = 0;    // this CTA's key tiles before the item
+    DocTile tile{};
+    bool stored = false;  // the staging atoms of O are still being read
+#pragma unroll 1
+    for (int it = -1;; ++it) {
+      const int last = x0 + (it < 0 ? 0 : tile.n_kv) - 1;
+      const bool ends = (last & 1) == g;
+      float m = -INFINITY, l = 0.f;  // this group's sum, relative to 2^m
+      const int next_slot = (it + 1) % kItemRing;
+      const DocTile& next = reinterpret_cast<const DocTile*>(smem + kTileOff)[next_slot];
+      if (!(ok = wait(bar->item_full[next_slot], (it + 1) / kItemRing))) break;
+      bool to_copy = !ends && next.rows > 0;
+#pragma unroll 1
+      for (int x = x0 + ((x0 ^ g) & 1);; x += 2) {
+        const bool here = x <= last;
+        const int j = x - x0;
+        float m_old = 0.f, m_new = 0.f;
+        bool need = false;
+        uint32_t pk[kKeys / 2];
+        if (here) {
+          if (!(ok = wait(bar->s_full[g], x >> 1))) break;
+          tc_fence_after();
+          uint32_t s[kKeys];
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32)
+            tmem_ld32(tmem + lanes + kTmS + g * kKeys + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(&bar->s_free[g]);  // the score buffer may take S_{x+2}
+          // where some row of the warp sees a part of the tile: the keys that this thread's
+          // row sees, lo .. hi - 1 of the window and 0 .. near - 1 however far back, as bits
+          const int k0 = tile.key0(j), first = tile.pos + quarter * 32;
+          const bool in_sinks = j < tile.n_sink;
+          if (in_sinks ? k0 + kKeys > tile.n_first
+                       : k0 + kKeys > tile.prefix && (first + 31 - k0 >= window || k0 + kKeys - 1 > first)) {
+            const int i = first + lane;
+            const int hi = in_sinks ? 0 : i + 1 - k0, lo = i + 1 - window - k0, near = max(tile.prefix, min(sinks, i + 1)) - k0;
+#pragma unroll
+            for (int c0 = 0; c0 < kKeys; c0 += 32) {
+              const uint32_t seen = (first_bits(hi - c0) & ~first_bits(lo - c0)) | first_bits(near - c0);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) s[c0 + c] = __float_as_uint(-INFINITY);
+            }
+          }
+          // max of the raw scores (the scale is positive): eight partial maxima and
+          // sums, three-input maxima, two-lane FMA and add
+          float mp[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mp[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 8]));
+#pragma unroll
+          for (int c = 16; c < kKeys; c += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mp[i] = fmax3(mp[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
+          const float mx = sl2 * fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], fmax3(mp[5], mp[6], mp[7])));
+          // the reference after the tile before, and after this one
+          if (x > 0 && !(ok = wait(bar->ref[g ^ 1][quarter], (x - 1) >> 1))) break;
+          m_old = j > 0 ? refs[(g ^ 1) * 128] : -INFINITY;
+          need = mx > m_old + kRescaleThreshold;
+          m_new = need ? mx : m_old;
+          refs[g * 128] = m_new;
+          mbar_arrive(&bar->ref[g][quarter]);
+          if (m != m_new) l *= ex2_approx(m - m_new);
+          m = m_new;
+          const float ref = m_new == -INFINITY ? 0.f : m_new;  // (all that a row sees so far may score -infinity)
+          // P as bf16 pairs (low half = even key; 2^-8 of each, both operands of an MMA
+          // have one type and V is bf16; the sum takes the float32 values)
+          float sp[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 2) {
+            float y0, y1;
+            fma_x2(y0, y1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, -ref, -ref);
+            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+            add_x2(sp[c & 7], sp[(c & 7) + 1], sp[c & 7], sp[(c & 7) + 1], p0, p1);
+            pk[c / 2] = pack_bf16x2(p0, p1);
+          }
+          l += ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
+        }
+        if (stored) {
+          if (lane == 0) {
+            bulk_wait_read<0>();
+            mbar_arrive(&bar->o_stored[quarter]);
+          }
+          stored = false;
+        }
+        if (to_copy && x + 2 > last) {
+          // the next item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory
+          // as bf16 pairs, the A operand of every S, once the S of this item are done
+          if (!(ok = (it < 0 || wait(bar->q_free, it)) && wait(bar->q_full, it + 1))) break;
+          tc_fence_after();
+          const uint8_t* qrow = smem + kQOff + row * 128;
+#pragma unroll 1
+          for (int c = 0; c < 3; ++c) {
+            uint32_t v[32];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kAtom + ((q ^ (row & 7)) << 4));
+              v[4 * q] = u.x;
+              v[4 * q + 1] = u.y;
+              v[4 * q + 2] = u.z;
+              v[4 * q + 3] = u.w;
+            }
+            tmem_st32(tmem + lanes + kTmQ + c * 32, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bar->q_tmem);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->qn_empty);  // the staging atoms may take the Q after it
+          to_copy = false;
+        }
+        if (!here) break;
+        // this group's tile before has been read: its P may be replaced
+        if (x > 1 && !(ok = wait(bar->pv_done[g], (x - 2) >> 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 16) tmem_st16(tmem + lanes + kTmP + g * kHalf + c, &pk[c]);
+        // an item's first tile replaces O, which must have been read
+        if (j == 0 && it > 0 && !(ok = wait(bar->o_free[quarter], it - 1))) break;
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          // O in the new reference, once the tile before has been added
+          if (!(ok = wait(bar->pv_done[g ^ 1], (x - 1) >> 1))) break;
+          tc_fence_after();
+          const float alpha = need ? ex2_approx(m_old - m_new) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(tmem + lanes + kTmO + c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st16(tmem + lanes + kTmO + c, r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar->p_full[g]);
+      }
+      if (!ok) break;
+      if (it >= 0 && !ends) {
+        *sums = make_float2(l, m);
+        mbar_arrive(&bar->sum[quarter]);
+      } else if (it >= 0) {
+        // O / l through this row of the staging atoms, once the O before has left them, and a
+        // TMA store; where the document ends among this warp's rows, each row that it has is
+        // stored by itself
+        if (!(ok = wait(bar->sum[quarter], it) && (it == 0 || wait(bar->o_stored[quarter], it - 1)) &&
+                   wait(bar->pv_done[g], last >> 1)))
+          break;
+        tc_fence_after();
+        const float2 other = *sums;
+        if (other.x != 0.f) l += other.x * ex2_approx(other.y - m);
+        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);  // (a row that saw no key: its O is zeros)
+        const bool whole = quarter * 32 + 32 <= tile.rows, mine = row < tile.rows;
+        // 16-byte unit u of the row: base + (u / 8) * atom + ((u % 8) ^ flip) * 16
+        uint8_t* base = whole ? smem + kOOff + row * 128
+                              : reinterpret_cast<uint8_t*>(o + (long long)(tile.q_row + row) * o_row + tile.head * 128);
+        const int atom = whole ? (int)kAtom : 128, flip = whole ? row & 7 : 0;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[64];
+          tmem_ld32(tmem + lanes + kTmO + c * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+          tmem_ld32(tmem + lanes + kTmO + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y0, y1;
+              fma_x2(y0, y1, __uint_as_float(r[8 * u + 2 * i]), __uint_as_float(r[8 * u + 2 * i + 1]), inv, inv, 0.f, 0.f);
+              w[i] = pack_bf16x2(y0, y1);
+            }
+            if (mine) *reinterpret_cast<uint4*>(base + ((u ^ flip) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          base += atom;
+        }
+        tc_fence_before();
+        mbar_arrive(&bar->o_free[quarter]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (whole && lane == 0) {
+          const uint8_t* rows = smem + kOOff + quarter * 32 * 128;
+          for (int c = 0; c < 2; ++c)
+            tma_store_3d(&tmO, rows + c * kAtom, tile.head * 128 + 64 * c, tile.q_row + quarter * 32, 0);
+          bulk_commit();
+        }
+        stored = true;
+      }
+      x0 = last + 1;
+      tile = next;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->item_empty[next_slot]);
+      if (tile.rows == 0) break;
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  if (!ok && lane == 0) bar->abort = warp + 1;
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && bar->abort) report_timeout(st, bar->abort);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- the documents' query tiles ------------------------------------------------
+constexpr int kDocPlanThreads = 1024;
+constexpr int kDocBuckets = 1024;  // tiles are ordered by their number of key tiles, up to this many
+constexpr int kDocsInSmem = 4096;
+
+// Document d's rows and keys.
+struct Doc {
+  int q0, n, k0, keys, prefix;
+  __device__ __forceinline__ Doc(const DocAttnArgs& a, int d) {
+    const int* ck = a.cu_k ? a.cu_k : a.cu_q;
+    q0 = a.cu_q[d];
+    n = a.cu_q[d + 1] - q0;
+    k0 = ck[d];
+    keys = ck[d + 1] - k0;
+    prefix = a.prefix ? max(0, min(a.prefix[d], keys)) : 0;
+  }
+};
+
+// Exclusive sums over the block, and the total (sh: one int a warp).
+__device__ __forceinline__ int block_before(int v, int& total, int* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  int before = x - v;
+  total = 0;
+#pragma unroll 8
+  for (int w = 0; w < kDocPlanThreads / 32; ++w) {
+    if (w < warp) before += sh[w];
+    total += sh[w];
+  }
+  __syncthreads();
+  return before;
+}
+
+// One CTA: the documents' numbers of query tiles, the tiles' numbers of key
+// tiles counted by value, and the tiles in that order, the heaviest first (the
+// order among equals is any: an item's result does not depend on it).  An
+// offset that is out of order or out of range leaves the plan empty.
+__global__ void __launch_bounds__(kDocPlanThreads, 1)
+    doc_plan_kernel(const DocAttnArgs a, int window, int sinks, int grid, int* work, uint32_t* status) {
+  __shared__ int first_smem[kDocsInSmem + 1];
+  __shared__ int bucket[kDocBuckets];
+  __shared__ int sh[kDocPlanThreads / 32];
+  __shared__ unsigned long long all_key_tiles;
+  __shared__ int heaviest;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  int* first = a.n_docs <= kDocsInSmem ? first_smem : a.first_tile;
+  bucket[tid] = 0;
+  if (tid == 0) {
+    all_key_tiles = 0;
+    heaviest = 1;
+  }
+  bool bad = false;
+  int n_tiles = 0;
+  const int* ck = a.cu_k ? a.cu_k : a.cu_q;
+  for (int d0 = 0; d0 < a.n_docs; d0 += kDocPlanThreads) {
+    const int d = d0 + tid;
+    int mine = 0, total;
+    if (d < a.n_docs) {
+      const int q0 = a.cu_q[d], q1 = a.cu_q[d + 1], k0 = ck[d], k1 = ck[d + 1];
+      if (q0 < 0 || q1 < q0 || q1 > a.N || k0 < 0 || k1 < k0 || k1 > a.cap)
+        bad = true;
+      else
+        mine = (q1 - q0 + 127) / 128;
+    }
+    const int before = block_before(mine, total, sh);
+    if (d < a.n_docs) first[d] = n_tiles + before;
+    n_tiles += total;
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    status[0] = bad ? kStatusBadLength : 0u;
+    status[kStatusExtraWord] = 0u;
+    *work = 0;
+  }
+  DocPlan* head = reinterpret_cast<DocPlan*>(a.plan);
+  DocTile* tiles = reinterpret_cast<DocTile*>(a.plan + sizeof(DocPlan));
+  if (bad || n_tiles == 0) {
+    if (tid == 0) {
+      head->n_tiles = 0;
+      head->group_log = 0;
+    }
+    return;
+  }
+  // tile t: its document is the last one that begins at or before it (and has tiles)
+  auto tile_of = [&](int t) {
+    int lo = 0, hi = a.n_docs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= t)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const Doc d(a, lo);
+    const int at = (t - first[lo]) * 128;
+    DocTile tile{};
+    tile.q_row = d.q0 + at;
+    tile.rows = min(128, d.n - at);
+    tile.k_row = d.k0;
+    tile.pos = d.keys - d.n + at;
+    tile.prefix = d.prefix;
+    tile.set_keys(window, sinks);
+    return tile;
+  };
+  for (int t = tid; t < n_tiles; t += kDocPlanThreads) {
+    const int n_kv = tile_of(t).n_kv;
+    atomicAdd(&bucket[kDocBuckets - 1 - min(n_kv, kDocBuckets - 1)], 1);
+    atomicAdd(&all_key_tiles, (unsigned long long)n_kv);
+    atomicMax(&heaviest, n_kv);
+  }
+  __syncthreads();
+  {
+    int total;
+    const int before = block_before(bucket[tid], total, sh);
+    bucket[tid] = before;
+  }
+  __syncthreads();
+  for (int t = tid; t < n_tiles; t += kDocPlanThreads) {
+    const DocTile tile = tile_of(t);
+    const int n_kv = tile.n_kv;
+    tiles[atomicAdd(&bucket[kDocBuckets - 1 - min(n_kv, kDocBuckets - 1)], 1)] = tile;
+  }
+  if (tid == 0) {
+    // the head group, by the rule of launch_prefill_attention
+    const unsigned long long need = (3ull * grid * heaviest + 2 * all_key_tiles - 1) / (2 * all_key_tiles);
+    const long long kv_head_bytes = ((long long)ck[a.n_docs] - ck[0]) * (192 + 128) * 2;
+    int G = 1;
+    while ((unsigned long long)G < need && G < 64) G *= 2;
+    while (G > 1 && G * kv_head_bytes > (16ll << 20)) G /= 2;
+    head->n_tiles = n_tiles;
+    head->group_log = __ffs(G) - 1;
+  }
+}
+}  // namespace
+
+cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv, to;
+  if (!make_tmap_bf16_3d(&tq, a.q, 12288, a.N, 1, (uint64_t)a.q_row * 2, (uint64_t)a.q_row * 2, 64, 128) ||
+      !make_tmap_bf16_3d(&tk, a.k, 192, a.cap, 64, 384, (uint64_t)a.cap * 384, 64, kKeys) ||
+      !make_tmap_bf16_3d(&tv, a.v, 128, a.cap, 64, 256, (uint64_t)a.cap * 256, 64, kHalf) ||
+      !make_tmap_store_bf16_3d(&to, a.o, 8192, a.N, 1, (uint64_t)a.o_row * 2, (uint64_t)a.o_row * 2))
+    return cudaErrorInvalidValue;
+  static PerDevice<bool> allowed;
+  const cudaError_t attr_err = allow_smem(allowed, document_attn_tc, kSmemBytes);
+  if (attr_err != cudaSuccess) return attr_err;
+  // no window: one that reaches behind every key (positions minus it stay in range)
+  const int window = a.window > 0 && a.window < kNoWindow ? a.window : kNoWindow;
+  const int sinks = a.window > 0 ? a.sinks : 0;
+  int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
+  const long long items = 64 * doc_tiles_at_most(a.N, a.n_docs);
+  const int grid = items < num_sms ? (int)items : num_sms;
+  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kDocPlanThreads), 0, stream, a, window, sinks, grid,
+                                   work, st.word);
+  if (e != cudaSuccess) return e;
+  DevStatus dst{st.word, st.wait_limit_ns};
+  return launch_pdl(document_attn_tc, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, to,
+                    a.scale * 1.4426950408889634f, window, sinks, work, (const uint8_t*)a.plan, a.o, a.o_row, dst);
+}
+
+}  // namespace mla

@@ -26,17 +26,6 @@
 // first case takes 313-318 us as built.)  The causal kernel keeps one thread a row: the tensor pipe and
 // the exponentials (the same number a scheduler either way) set its pace, and
 // its sums keep their order.
-// Documents (DOC): the rows of q are those of several documents one after the
-// other, each with keys of its own.  A plan kernel lists their query tiles, a
-// tile never holding rows of two documents, heaviest first; an item is a tile
-// and a head.  Its key tiles begin at the document's (or the window's) first
-// key; V rows behind the last key that the tile's queries see would be another
-// document's: the P.V product takes only the 16-key steps up to that key, and
-// the V producer's warp clears the rows behind it in the last step, so that
-// nothing of a neighbour (a NaN times zero among it) reaches the sum.  Rows of
-// the next document in the Q tile are computed and not stored; a row that sees
-// no key has the sum zero and is stored as zeros.  The softmax is the windowed
-// kernel's, two threads a row, for the same reason: a document has few key tiles.
 // Chunked prefill: the queries sit at positions past..past+T-1 and attend to
 // keys 0..past+T-1 of the cache (the chunk's own keys written after the
 // cached ones), the causal mask offset by past.
@@ -95,18 +84,15 @@ constexpr uint32_t kBarOff = 14 * kAtom;
 // Q dims 0-127 (bf16 pairs)
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = 384, kTmQ = 448;
 constexpr uint32_t kXchOff = kBarOff + 512;      // WIN: a row's two partial maxima (or sums), 2 x 2 x 128 fp32
-constexpr uint32_t kTileOff = kXchOff + 2048;    // DOC: the query tiles of the item ring
-enum class Mask { kCausal, kWindow, kDocuments };
-// WIN (also for documents): two threads a row, each with half of a key tile's (and of O's) columns
-template <Mask M>
+// WIN: two threads a row, each with half of a key tile's (and of O's) columns
+template <bool WIN>
 struct Shape {
-  static constexpr bool kWin = M != Mask::kCausal, kDoc = M == Mask::kDocuments;
-  static constexpr int kHalves = kWin ? 2 : 1;
+  static constexpr int kHalves = WIN ? 2 : 1;
   static constexpr int kThreads = 128 + 128 * kHalves;
   static constexpr int kCols = 128 / kHalves;
-  static constexpr uint32_t kSmemBytes = kDoc ? kTileOff + 256 : kWin ? kXchOff + 2048 : kXchOff;  // (1,024-byte aligned)
+  static constexpr uint32_t kSmemBytes = WIN ? kXchOff + 2048 : kXchOff;  // (1,024-byte aligned)
 };
-static_assert(Shape<Mask::kDocuments>::kSmemBytes <= 232448, "prefill attention shared memory");
+static_assert(Shape<true>::kSmemBytes <= 232448, "prefill attention shared memory");
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 
 constexpr int kItemRing = 4;
@@ -120,56 +106,21 @@ struct Bars {
   uint64_t p_full, pv_done;
   uint64_t drain_s, drain_pv;
   uint64_t xch[4];  // WIN: per quarter of the rows
-  uint64_t v_cut[2];  // DOC: the V tile's rows behind its last key are cleared
   uint32_t tmem_slot;
   int abort;
   int item[kItemRing];
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-// A document's query tile, as the plan lists it: its rows q_row .. q_row + rows
-// - 1 sit at positions pos .. (below 0: before the document's first key), its
-// keys begin at row k_row; the first `prefix` are seen by every query.
-struct DocTile {
-  int q_row, rows, k_row, pos, prefix, head, pad[2];
-};
-static_assert(sizeof(DocTile) == kDocTileBytes && kItemRing * sizeof(DocTile) <= 256, "tiles of the item ring");
-// The plan: this, then the tiles, heaviest first.
-struct DocPlan {
-  int n_tiles, head_group, pad[6];
-};
-static_assert(sizeof(DocPlan) == kDocTileBytes, "the plan's head is as long as a tile");
-
 // Work item w (the order described above) -> its query tile, head, sequence
 // and key tiles.  Under a sliding window (WIN) the tile's queries together
 // see the keys from w0 on, and the sinks before w0: first n_sink tiles over
 // keys 0 .. n_first - 1, then tiles from w0 on (a TMA box may start at any
 // row, so no key before w0 is loaded).
-// Documents: w0 and the sinks as under a window, the sinks being the keys that
-// are seen however far back they are; where they reach w0, the tiles run from
-// key 0.  `end` is the key behind the last one that the tile's queries see.
-template <Mask M>
+template <bool WIN>
 struct Item {
-  static constexpr bool WIN = Shape<M>::kWin;
   int qt, h, b, q0, n_kv;
   int w0, n_first, n_sink;
-  int end, k_row, pos, rows, prefix;  // documents
-  __device__ __forceinline__ Item(const DocTile& t, int window, int sinks)
-      : qt(0), h(t.head), b(0), q0(t.q_row), k_row(t.k_row), pos(t.pos), rows(t.rows), prefix(t.prefix) {
-    const int last = pos + rows;  // behind the last query's position
-    w0 = max(0, pos - window + 1);
-    end = max(last, prefix);
-    n_first = max(prefix, min(sinks, last));
-    if (n_first >= w0) w0 = n_first = 0;
-    n_first = max(n_first, 0);
-    n_sink = (n_first + 127) / 128;
-    // (one tile of nothing where no key is seen: its item stores zeros)
-    n_kv = max(1, n_sink + max(0, end - w0 + 127) / 128);
-  }
-  // keys of tile j that some query may see: those behind them are not the document's, or nobody's
-  __device__ __forceinline__ int keys(int j) const {
-    return max(0, min(128, (j < n_sink ? n_first : end) - key0(j)));
-  }
   __device__ __forceinline__ Item(int w, int n_qt, int T, int past, int G, int window, int sinks) {
     const int per_seq = 64 * n_qt;
     b = w / per_seq;
@@ -205,21 +156,11 @@ struct Item {
   }
 };
 
-// The query tile and head of work item w, in the order described above.
-__device__ __forceinline__ void doc_item(int w, int n_tiles, int G, int& tile, int& head) {
-  const int g = w / (G * n_tiles), r = w - g * G * n_tiles;  // (G divides 64)
-  tile = r / G;
-  head = g * G + (r - tile * G);
-}
-
 // Every role reads item `it` from the ring (bounded wait), then releases the slot.
-template <bool DOC>
-__device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, DocTile& tile, const DevStatus& st,
-                                          volatile int* abort_flag) {
+__device__ __forceinline__ bool read_item(Bars* bar, int it, int& w, const DevStatus& st, volatile int* abort_flag) {
   const int slot = it % kItemRing;
   if (!mbar_wait(&bar->item_full[slot], (it / kItemRing) & 1, st, abort_flag, 39)) return false;
   w = *reinterpret_cast<volatile int*>(&bar->item[slot]);
-  if constexpr (DOC) tile = reinterpret_cast<const DocTile*>(reinterpret_cast<uint8_t*>(bar) + (kTileOff - kBarOff))[slot];
   mbar_arrive(&bar->item_empty[slot]);
   return true;
 }
@@ -241,16 +182,14 @@ __device__ __forceinline__ void keep_order(float& l, uint32_t (&p)[N]) {
                  "+r"(p[c + 12]), "+r"(p[c + 13]), "+r"(p[c + 14]), "+r"(p[c + 15]));
 }
 
-template <Mask M>
-__global__ void __launch_bounds__(Shape<M>::kThreads, 1)
+template <bool WIN>
+__global__ void __launch_bounds__(Shape<WIN>::kThreads, 1)
     prefill_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVsink,
                     const __grid_constant__ CUtensorMap tmO, int T, int n_qt, int n_items, float sl2, int past, int head_group,
-                    int window, int sinks, int* __restrict__ work, const uint8_t* __restrict__ plan,
-                    __nv_bfloat16* __restrict__ o, long long o_row, const DevStatus st) {
+                    int window, int sinks, int* __restrict__ work, const DevStatus st) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr bool WIN = Shape<M>::kWin, DOC = Shape<M>::kDoc;
-  constexpr int kHalves = Shape<M>::kHalves, kCols = Shape<M>::kCols;
+  constexpr int kHalves = Shape<WIN>::kHalves, kCols = Shape<WIN>::kCols;
   constexpr int kItemReaders = 3 + 128 * kHalves;  // V producer, S issuer, P.V issuer, softmax threads
   Bars* bar = reinterpret_cast<Bars*>(smem + kBarOff);
   volatile int* abort_flag = &bar->abort;
@@ -278,7 +217,6 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
       mbar_init(&bar->s_free[i], 128 * kHalves);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bar->xch[i], 64);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar->v_cut[i], 1);
     mbar_init(&bar->drain_s, 1);
     mbar_init(&bar->drain_pv, 1);
     bar->abort = 0;
@@ -294,13 +232,6 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
   const uint32_t tmem = bar->tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  // an item as every role sees it
-  auto make_item = [&](int w, const DocTile& tile) {
-    if constexpr (DOC)
-      return Item<M>(tile, window, sinks);
-    else
-      return Item<M>(w, n_qt, T, past, head_group, window, sinks);
-  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -310,35 +241,16 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
       int issued[2] = {0, 0};
       int q_loads = 0;
       int gt = 0;  // this CTA's K tiles so far (ring position)
-      int next = 0, doc_tiles = 0, doc_group = 1;
-      if constexpr (DOC) {
-        const DocPlan* head = reinterpret_cast<const DocPlan*>(plan);
-        doc_tiles = head->n_tiles;
-        doc_group = head->head_group;
-        n_items = 64 * doc_tiles;
-        next = atomicAdd(work, 1);
-      }
       for (int it = 0;; ++it) {
         const int slot = it % kItemRing;
         if (it >= kItemRing && !mbar_wait(&bar->item_empty[slot], (it / kItemRing - 1) & 1, st, abort_flag, 38))
           break;
-        int w = DOC ? next : atomicAdd(work, 1);
+        int w = atomicAdd(work, 1);
         if (w >= n_items) w = -1;
-        DocTile tile{};
-        if constexpr (DOC) {
-          if (w >= 0) {
-            int at, head;
-            doc_item(w, doc_tiles, doc_group, at, head);
-            tile = reinterpret_cast<const DocTile*>(plan + sizeof(DocPlan))[at];
-            tile.head = head;
-            reinterpret_cast<DocTile*>(smem + kTileOff)[slot] = tile;
-          }
-        }
         bar->item[slot] = w;
         mbar_arrive(&bar->item_full[slot]);  // release: the index is visible to every waiting role
         if (w < 0) break;
-        if constexpr (DOC) next = atomicAdd(work, 1);  // (arrives while this item's copies are issued)
-        const Item<M> t = make_item(w, tile);
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         // the Q tile: dims 0-127 into the staging atoms once the softmax threads
         // copied the previous item's into tensor memory, dims 128-191 into the
         // slot of this item's parity once the S of the item two back are done
@@ -358,9 +270,8 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&bar->k_full[ks], 3 * kAtom);
-          const int key = DOC ? t.k_row + t.key0(j) : t.key0(j);
           for (int c = 0; c < 3; ++c)
-            tma_load_3d(smem + kKOff + (ks * 3 + c) * kAtom, &tmK, &bar->k_full[ks], 64 * c, key, kv_row);
+            tma_load_3d(smem + kKOff + (ks * 3 + c) * kAtom, &tmK, &bar->k_full[ks], 64 * c, t.key0(j), kv_row);
           issued[ks]++;
         }
         if (!ok) break;
@@ -370,47 +281,6 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
       for (int i = 0; i < 2; ++i)
         if (issued[i]) mbar_wait(&bar->k_full[i], (issued[i] - 1) & 1, st, nullptr, 41);
     }
-  } else if (DOC && warp == 6) {
-    // ---- V producer of documents: lane 0 issues the copies, the warp clears ----
-    int issued[2] = {0, 0};
-    int gt = 0;
-    bool ok = true;
-    if (lane == 0) tma_prefetch_desc(&tmV);
-    for (int it = 0; ok; ++it) {
-      const int slot = it % kItemRing;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar->item_full[slot], (it / kItemRing) & 1, st, abort_flag, 39));
-      if (!ok) break;
-      const int w = *reinterpret_cast<volatile int*>(&bar->item[slot]);
-      const DocTile tile = reinterpret_cast<const DocTile*>(smem + kTileOff)[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->item_empty[slot]);
-      if (w < 0) break;
-      const Item<M> t = make_item(w, tile);
-      for (int j = 0; j < t.n_kv; ++j, ++gt) {
-        const int vs = gt & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar->v_empty[vs], ((gt >> 1) & 1) ^ 1, st, abort_flag, 42));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar->v_full[vs], 2 * kAtom);
-          for (int c = 0; c < 2; ++c)
-            tma_load_3d(smem + kVOff + (vs * 2 + c) * kAtom, &tmV, &bar->v_full[vs], 64 * c, t.k_row + t.key0(j), t.h);
-        }
-        issued[vs]++;
-        const int keys = t.keys(j);
-        if (keys & 15) {  // rows keys .. of the last 16-key step: eight lanes a row and atom
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar->v_full[vs], (gt >> 1) & 1, st, abort_flag, 56));
-          if (!ok) break;
-          for (int r = keys + (lane >> 4); r < ((keys + 15) & ~15); r += 2)
-            *reinterpret_cast<uint4*>(smem + kVOff + (vs * 2 + ((lane >> 3) & 1)) * kAtom + r * 128 + (lane & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->v_cut[vs]);
-        }
-      }
-    }
-    for (int i = 0; i < 2; ++i)
-      if (issued[i]) mbar_wait(&bar->v_full[i], (issued[i] - 1) & 1, st, nullptr, 43);
   } else if (warp == 6) {
     if (lane == 0) {
       // ---- V producer ----
@@ -420,9 +290,8 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
       bool ok = true;
       for (int it = 0; ok; ++it) {
         int w;
-        DocTile tile;
-        if (!read_item<DOC>(bar, it, w, tile, st, abort_flag) || w < 0) break;
-        const Item<M> t = make_item(w, tile);
+        if (!read_item(bar, it, w, st, abort_flag) || w < 0) break;
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         const int kv_row = t.b * 64 + t.h;
         for (int j = 0; j < t.n_kv; ++j, ++gt) {
           const int vs = gt & 1;
@@ -452,9 +321,8 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
       bool ok = true;
       for (int it = 0; ok; ++it) {
         int w;
-        DocTile tile;
-        if (!read_item<DOC>(bar, it, w, tile, st, abort_flag) || w < 0) break;
-        const Item<M> t = make_item(w, tile);
+        if (!read_item(bar, it, w, st, abort_flag) || w < 0) break;
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         if (!mbar_wait(&bar->q_tmem, it & 1, st, abort_flag, 44)) break;  // this item's Q in tensor memory
         const uint32_t qpe_addr = smem_u32(smem + kQpeOff + (it & 1) * kAtom);
         for (int j = 0; j < t.n_kv; ++j, ++gt) {
@@ -495,13 +363,12 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
       // ---- P.V issuer: O += P_j V_j ----
       constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
       const uint32_t v_addr = smem_u32(smem + kVOff);
-      int gt = 0, cuts[2] = {0, 0};
+      int gt = 0;
       bool ok = true;
       for (int it = 0; ok; ++it) {
         int w;
-        DocTile tile;
-        if (!read_item<DOC>(bar, it, w, tile, st, abort_flag) || w < 0) break;
-        const Item<M> t = make_item(w, tile);
+        if (!read_item(bar, it, w, st, abort_flag) || w < 0) break;
+        const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
         for (int j = 0; j < t.n_kv; ++j, ++gt) {
           const int sb = gt & 1;
           // P_j is written (and, for an item's first tile, the previous item's
@@ -511,21 +378,11 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
             ok = false;
             break;
           }
-          int steps = 8;
-          if constexpr (DOC) {  // the 16-key steps that hold a key, the last one's other rows cleared
-            const int keys = t.keys(j);
-            steps = (keys + 15) >> 4;
-            if ((keys & 15) && !mbar_wait(&bar->v_cut[sb], cuts[sb]++ & 1, st, abort_flag, 57)) {
-              ok = false;
-              break;
-            }
-          }
           tc_fence_after();
           const uint32_t vb = v_addr + sb * 2 * kAtom;
           const uint32_t pa = tmem + kTmP;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            if (DOC && kk >= steps) break;
             const uint64_t bdesc = sdesc_sw128(vb + kk * 2048, kAtom, 1024);
             umma_bf16_ts(tmem + kTmO, pa + kk * 8, bdesc, idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
           }
@@ -559,12 +416,10 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
     };
     // the previous item, whose O is written out once the next item's Q is in place
     int prev_qpos = -1, prev_h = 0, prev_b = 0, prev_last = -1;
-    int prev_rows = 0;  // DOC: the tile's rows
     float prev_l = 1.f;
     for (int it = 0; ok; ++it) {
       int w = -1;
-      DocTile tile;
-      ok = __all_sync(0xffffffffu, read_item<DOC>(bar, it, w, tile, st, abort_flag));
+      ok = __all_sync(0xffffffffu, read_item(bar, it, w, st, abort_flag));
       if (!ok) break;
       if (w >= 0) {
         // this item's Q rows, dims 0-127 (two 128-byte-swizzled 64-column
@@ -599,37 +454,14 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&bar->pv_done, prev_last & 1, st, abort_flag, 52));
         if (!ok) break;
         tc_fence_after();
-        // (DOC: a row that saw no key is zeros, whatever lies in O)
-        const bool none = DOC && prev_l == 0.f;
-        const float inv = none ? 0.f : 1.f / prev_l;
+        const float inv = 1.f / prev_l;
         const uint32_t ta = tmem + lane_addr + kTmO;
         uint8_t* orow = smem + kQOff + row * 128;
-        // DOC: where the document ends among this warp's rows, each row that it has is stored by itself
-        const bool whole = !DOC || quarter * 32 + 32 <= prev_rows;
 #pragma unroll 1
         for (int c = half * kCols; c < half * kCols + kCols; c += 32) {
           uint32_t r[32];
           tmem_ld32(ta + c, r);
           tmem_wait_ld();
-          if constexpr (DOC) {
-            if (none) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = 0u;
-            }
-            if (!whole) {
-              if (row < prev_rows) {
-                uint4* dst = reinterpret_cast<uint4*>(o + (long long)prev_qpos * o_row + prev_h * 128 + c);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  dst[q] = make_uint4(
-                      pack_bf16x2(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
-                      pack_bf16x2(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
-                      pack_bf16x2(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
-                      pack_bf16x2(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
-              }
-              continue;
-            }
-          }
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<uint4*>(orow + (c >> 6) * kAtom + ((((c & 32) >> 3) + q) ^ (row & 7)) * 16) = make_uint4(
@@ -643,7 +475,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
         if (lane == 0) {
           const uint8_t* rows = smem + kQOff + quarter * 32 * 128;
           const int first = prev_qpos - lane;  // this warp's first query
-          if (DOC ? whole : first < T) {
+          if (first < T) {
             for (int c = half; c < half + 2 / kHalves; ++c)
               tma_store_3d(&tmO, rows + c * kAtom, prev_h * 128 + 64 * c, first, prev_b);
           }
@@ -652,7 +484,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
         prev_last = -1;
       }
       if (w < 0) break;
-      const Item<M> t = make_item(w, tile);
+      const Item<WIN> t(w, n_qt, T, past, head_group, window, sinks);
       const int qpos = t.q0 + row;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < t.n_kv; ++j, ++gt) {
@@ -673,25 +505,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
         // max of the raw scores (the scale is positive), causal mask (key k
         // visible to query position past + qpos iff k <= past + qpos) on the
         // tiles that reach beyond the tile's first query
-        if constexpr (DOC) {
-          // as under a window, and the prefix (a tile that the rows all see in full needs no look)
-          const bool in_sinks = j < t.n_sink;
-          if (in_sinks ? k0 + kCols > t.n_first
-                       : k0 + kCols > t.prefix && (t.pos + t.rows - 1 - k0 >= window || k0 + kCols - 1 > t.pos)) {
-#pragma unroll
-            for (int c0 = 0; c0 < kCols; c0 += 32) {
-              const int kw = k0 + c0, i = t.pos + row;
-              uint32_t seen = (first_bits(i + 1 - kw) & (~first_bits(i + 1 - window - kw) | first_bits(sinks - kw))) |
-                              first_bits(t.prefix - kw);
-              if (in_sinks) seen &= first_bits(t.n_first - kw);
-              if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(seen & (1u << c))) s[c0 + c] = __float_as_uint(-INFINITY);
-              }
-            }
-          }
-        } else if constexpr (WIN) {
+        if constexpr (WIN) {
           // tiles that some query of the item sees a part of: 32 columns at a time,
           // the visible ones of this thread's row as bits (one short piece of code for
           // every mask: with a loop of comparisons for each, a window of 1,024 with
@@ -802,7 +616,6 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
         l += other;
       }
       prev_qpos = qpos;
-      prev_rows = DOC ? t.rows : 0;
       prev_h = t.h;
       prev_b = t.b;
       prev_l = l;
@@ -816,142 +629,6 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
-  }
-}
-
-// ---- the documents' query tiles ------------------------------------------------
-constexpr int kDocPlanThreads = 1024;
-constexpr int kDocBuckets = 1024;  // tiles are ordered by their number of key tiles, up to this many
-constexpr int kDocsInSmem = 4096;
-
-// Document d's rows and keys.
-struct Doc {
-  int q0, n, k0, keys, prefix;
-  __device__ __forceinline__ Doc(const DocAttnArgs& a, int d) {
-    const int* ck = a.cu_k ? a.cu_k : a.cu_q;
-    q0 = a.cu_q[d];
-    n = a.cu_q[d + 1] - q0;
-    k0 = ck[d];
-    keys = ck[d + 1] - k0;
-    prefix = a.prefix ? max(0, min(a.prefix[d], keys)) : 0;
-  }
-};
-
-// Exclusive sums over the block, and the total (sh: one int a warp).
-__device__ __forceinline__ int block_before(int v, int& total, int* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  int before = x - v;
-  total = 0;
-#pragma unroll 8
-  for (int w = 0; w < kDocPlanThreads / 32; ++w) {
-    if (w < warp) before += sh[w];
-    total += sh[w];
-  }
-  __syncthreads();
-  return before;
-}
-
-// One CTA: the documents' numbers of query tiles, the tiles' numbers of key
-// tiles counted by value, and the tiles in that order, the heaviest first (the
-// order among equals is any: an item's result does not depend on it).  An
-// offset that is out of order or out of range leaves the plan empty.
-__global__ void __launch_bounds__(kDocPlanThreads, 1)
-    doc_plan_kernel(const DocAttnArgs a, int window, int sinks, int grid, int* work, uint32_t* status) {
-  __shared__ int first_smem[kDocsInSmem + 1];
-  __shared__ int bucket[kDocBuckets];
-  __shared__ int sh[kDocPlanThreads / 32];
-  __shared__ unsigned long long all_key_tiles;
-  __shared__ int heaviest;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int tid = threadIdx.x;
-  int* first = a.n_docs <= kDocsInSmem ? first_smem : a.first_tile;
-  bucket[tid] = 0;
-  if (tid == 0) {
-    all_key_tiles = 0;
-    heaviest = 1;
-  }
-  bool bad = false;
-  int n_tiles = 0;
-  const int* ck = a.cu_k ? a.cu_k : a.cu_q;
-  for (int d0 = 0; d0 < a.n_docs; d0 += kDocPlanThreads) {
-    const int d = d0 + tid;
-    int mine = 0, total;
-    if (d < a.n_docs) {
-      const int q0 = a.cu_q[d], q1 = a.cu_q[d + 1], k0 = ck[d], k1 = ck[d + 1];
-      if (q0 < 0 || q1 < q0 || q1 > a.N || k0 < 0 || k1 < k0 || k1 > a.cap)
-        bad = true;
-      else
-        mine = (q1 - q0 + 127) / 128;
-    }
-    const int before = block_before(mine, total, sh);
-    if (d < a.n_docs) first[d] = n_tiles + before;
-    n_tiles += total;
-  }
-  bad = __syncthreads_or(bad);
-  if (tid == 0) {
-    status[0] = bad ? kStatusBadLength : 0u;
-    status[kStatusExtraWord] = 0u;
-    *work = 0;
-  }
-  DocPlan* head = reinterpret_cast<DocPlan*>(a.plan);
-  DocTile* tiles = reinterpret_cast<DocTile*>(a.plan + sizeof(DocPlan));
-  if (bad || n_tiles == 0) {
-    if (tid == 0) {
-      head->n_tiles = 0;
-      head->head_group = 1;
-    }
-    return;
-  }
-  // tile t: its document is the last one that begins at or before it (and has tiles)
-  auto tile_of = [&](int t) {
-    int lo = 0, hi = a.n_docs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= t)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const Doc d(a, lo);
-    const int at = (t - first[lo]) * 128;
-    return DocTile{d.q0 + at, min(128, d.n - at), d.k0, d.keys - d.n + at, d.prefix, 0, {0, 0}};
-  };
-  for (int t = tid; t < n_tiles; t += kDocPlanThreads) {
-    const int n_kv = Item<Mask::kDocuments>(tile_of(t), window, sinks).n_kv;
-    atomicAdd(&bucket[kDocBuckets - 1 - min(n_kv, kDocBuckets - 1)], 1);
-    atomicAdd(&all_key_tiles, (unsigned long long)n_kv);
-    atomicMax(&heaviest, n_kv);
-  }
-  __syncthreads();
-  {
-    int total;
-    const int before = block_before(bucket[tid], total, sh);
-    bucket[tid] = before;
-  }
-  __syncthreads();
-  for (int t = tid; t < n_tiles; t += kDocPlanThreads) {
-    const DocTile tile = tile_of(t);
-    const int n_kv = Item<Mask::kDocuments>(tile, window, sinks).n_kv;
-    tiles[atomicAdd(&bucket[kDocBuckets - 1 - min(n_kv, kDocBuckets - 1)], 1)] = tile;
-  }
-  if (tid == 0) {
-    // the head group, by the rule of launch_prefill_attention
-    const unsigned long long need = (3ull * grid * heaviest + 2 * all_key_tiles - 1) / (2 * all_key_tiles);
-    const long long kv_head_bytes = ((long long)ck[a.n_docs] - ck[0]) * (192 + 128) * 2;
-    int G = 1;
-    while ((unsigned long long)G < need && G < 64) G *= 2;
-    while (G > 1 && G * kv_head_bytes > (16ll << 20)) G /= 2;
-    head->n_tiles = n_tiles;
-    head->head_group = G;
   }
 }
 }  // namespace
@@ -973,11 +650,9 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
       !make_tmap_bf16_3d(&tvs, a.v, 128, (uint64_t)a.sinks < n_keys ? (uint64_t)a.sinks : n_keys, (uint64_t)a.B * 64,
                          256, (uint64_t)a.cap * 256, 64, 128))
     return cudaErrorInvalidValue;
-  using W = Shape<Mask::kWindow>;
-  using C = Shape<Mask::kCausal>;
-  auto kern = win ? prefill_attn_tc<Mask::kWindow> : prefill_attn_tc<Mask::kCausal>;
-  const uint32_t smem_bytes = win ? W::kSmemBytes : C::kSmemBytes;
-  const int threads = win ? W::kThreads : C::kThreads;
+  auto kern = win ? prefill_attn_tc<true> : prefill_attn_tc<false>;
+  const uint32_t smem_bytes = win ? Shape<true>::kSmemBytes : Shape<false>::kSmemBytes;
+  const int threads = win ? Shape<true>::kThreads : Shape<false>::kThreads;
   static PerDevice<bool> allowed[2];
   const cudaError_t attr_err = allow_smem(allowed[win], kern, smem_bytes);
   if (attr_err != cudaSuccess) return attr_err;
@@ -1010,34 +685,7 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, const DevStatusHo
   int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
   DevStatus dst{st.word, st.wait_limit_ns};
   return launch_pdl(kern, dim3(grid), dim3(threads), smem_bytes, stream, tq, tk, tv, tvs, to, a.T, n_qt, n_items,
-                    a.scale * 1.4426950408889634f, a.past, G, window, a.sinks, work, (const uint8_t*)nullptr,
-                    (__nv_bfloat16*)nullptr, 0ll, dst);
-}
-
-cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream) {
-  using S = Shape<Mask::kDocuments>;
-  CUtensorMap tq, tk, tv, to;
-  if (!make_tmap_bf16_3d(&tq, a.q, 12288, a.N, 1, (uint64_t)a.q_row * 2, (uint64_t)a.q_row * 2, 64, 128) ||
-      !make_tmap_bf16_3d(&tk, a.k, 192, a.cap, 64, 384, (uint64_t)a.cap * 384, 64, 128) ||
-      !make_tmap_bf16_3d(&tv, a.v, 128, a.cap, 64, 256, (uint64_t)a.cap * 256, 64, 128) ||
-      !make_tmap_store_bf16_3d(&to, a.o, 8192, a.N, 1, (uint64_t)a.o_row * 2, (uint64_t)a.o_row * 2))
-    return cudaErrorInvalidValue;
-  static PerDevice<bool> allowed;
-  const cudaError_t attr_err = allow_smem(allowed, prefill_attn_tc<Mask::kDocuments>, S::kSmemBytes);
-  if (attr_err != cudaSuccess) return attr_err;
-  // no window: one that reaches behind every key (positions minus it stay in range)
-  const int window = a.window > 0 && a.window < kNoWindow ? a.window : kNoWindow;
-  const int sinks = a.window > 0 ? a.sinks : 0;
-  int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
-  const long long items = 64 * doc_tiles_at_most(a.N, a.n_docs);
-  const int grid = items < num_sms ? (int)items : num_sms;
-  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kDocPlanThreads), 0, stream, a, window, sinks, grid,
-                                   work, st.word);
-  if (e != cudaSuccess) return e;
-  DevStatus dst{st.word, st.wait_limit_ns};
-  return launch_pdl(prefill_attn_tc<Mask::kDocuments>, dim3(grid), dim3(S::kThreads), S::kSmemBytes, stream, tq, tk, tv,
-                    tv, to, a.N, 0, 0, a.scale * 1.4426950408889634f, 0, 1, window, sinks, work, (const uint8_t*)a.plan,
-                    a.o, a.o_row, dst);
+                    a.scale * 1.4426950408889634f, a.past, G, window, a.sinks, work, dst);
 }
 
 }  // namespace mla

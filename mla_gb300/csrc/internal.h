@@ -305,7 +305,7 @@ struct DocAttnArgs {
   uint8_t* plan;            // kDocTileBytes for its head and for each of doc_tiles_at_most() tiles
   int* first_tile;          // [n_docs] of many documents
 };
-constexpr int kDocTileBytes = 32;
+constexpr int kDocTileBytes = 48;
 constexpr int kNoWindow = 1 << 29;
 inline long long doc_tiles_at_most(int N, int n_docs) {
   const long long n = (long long)N / 128 + n_docs;  // whole tiles, and a partial one a document
