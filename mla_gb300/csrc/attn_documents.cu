@@ -3,7 +3,7 @@
 // "Mix and project" page, code excerpt: scores = Q K^T * softmax_scale plus
 // the mask, softmax in float32, then P V; here for several sequences packed one
 // after the other, each seeing its own keys only (mla_document_attention).
-// Computed in the flash form: online softmax over 128-key tiles.
+// Computed in the flash form: online softmax over tiles of 96 keys.
 //
 // A plan kernel lists the documents' query tiles of up to 128 rows, a tile
 // never holding rows of two documents, heaviest first.  Persistent: one CTA per
@@ -17,30 +17,47 @@
 // sees no key has the sum zero and is stored as zeros.
 //
 // Warp roles (384 threads):
-//   warp 0   work scheduler (counter -> a 4-slot ring of items), then TMA: the
-//            item's Q tile, then its K tiles into a 2-slot ring
-//   warp 1   TMEM allocation; one lane issues S_x = Q K^T (M=128 N=128 K=192)
-//            into score buffer x & 1, x counting this CTA's key tiles: Q's 128
-//            "nope" dimensions from tensor memory, the 64 RoPE ones from one of
-//            two shared-memory slots
-//   warp 2   TMA: V tiles into a 2-slot ring, and their cut
-//   warp 3   one lane issues O += P_x V_x (M=128 N=128 K=128), P from tensor memory
+//   warp 0   work scheduler (counter -> a 4-slot ring of items), then TMA: K
+//            tiles, 64 dimensions at a time, into a ring of 7 such thirds (TMA
+//            takes 1,900 cycles under load: with a ring of two whole tiles, each
+//            slot idle for that long, a tile took 1,400 cycles, so 1,240), and
+//            the next item's Q tile
+//   warp 1   TMEM allocation; an item's Q into tensor memory (tcgen05.cp), then
+//            S_x = Q K_x^T (M=128 N=96 K=192) into score buffer x & 1, x
+//            counting this CTA's key tiles
+//   warp 2   TMA: V, half a tile at a time, into a ring of 5 halves, and their cut
+//   warp 3   O += P_x V_x (M=128 N=128 K=96), P from tensor memory
 //   warps 4..7, 8..11   two softmax groups, one thread a query row.  Group g takes
-//            the key tiles with x & 1 = g: while one waits for its scores, looks
-//            for the maximum or stores P, the other one's exponentials fill the
-//            special-function units (1,024 cycles a tile, of 1,280 that its
-//            products take).  Both express P and O in one reference a row, the
-//            running maximum with lazy rescaling (it moves only when the maximum
-//            grows by more than 2^8, so P stays <= 256): the tile before hands its
-//            reference on through shared memory.  Each group sums its own tiles'
-//            rows.  At an item's end the group without the last tile hands over its
-//            sums, copies the next item's Q into tensor memory and goes on to that
-//            item's first tile, which is its own; the other one writes O / l.
-// (Two threads a row on the same tile, as the windowed prefill has them, do
-// their waits, maxima and exponentials all at the same time: 5 documents of up to
-// 4,096 tokens 820 us.)
-// Registers: the four control warps give theirs up to the softmax groups, which
-// hold a row's 128 scores.
+//            the key tiles with x & 1 = g, half a tile's time apart, so that one's
+//            waits, maximum and stores lie beside the other's exponentials.  Both
+//            express P and O in one reference a row, the running maximum with
+//            lazy rescaling (it moves only when the maximum grows by more than
+//            2^8, so P stays <= 256): the tile before hands its reference on
+//            through shared memory.  Each group sums its own tiles' rows.  At an
+//            item's end the group without the last tile hands over its sums and
+//            goes on to the next item's first tile, which is its own; the other
+//            one writes O / l.
+// 96 keys: two score buffers, two of P (so that a P is stored while the product of
+// the one before runs), O and all of Q take the 512 tensor-memory columns exactly,
+// and products of N = 96 from tensor memory run at the full rate (4,080 MAC a clock
+// measured; N = 64: 2,906).
+// What bounds it: the SM's shared memory.  A key tile is 60 KB, written once by
+// TMA and read once by the products, 960 cycles at 128 bytes a clock, which is
+// also what its products take (960 at 4,096 MAC a clock); an item adds Q and O,
+// 160 KB, 1,250 cycles.  Long documents take 1,060 cycles a tile.  With the K and V
+// copies left out (wrong results) 16 documents of up to 1,531 tokens took 185 us
+// where they take 241, 5 of up to 4,096 tokens 523 where they take 720 (0.7 of the
+// products' burst rate, 0.76 with the masked halves of diagonal tiles that run).
+// Measured on the way, GPU time: the windowed prefill's two threads a row on the same
+// tile 309 and 820 us; this form 248 and 745 with lane-0 loops and Q through
+// registers.  Two CTAs sharing K/V tiles by multicast 263 and 749 (the copies'
+// writes stay); warps of their own for the output 260 and 771.
+//
+// Code size: the roles' loops share one instruction cache.  At 81 KB of code (every
+// wait inlined with its clock) 5.4 of the stalls per instruction were for
+// instructions and the second case took 1,290 us; at 35 KB it takes 720.  Hence the
+// waits' counted tries, loops that are not unrolled, and the plan's own numbers of
+// key tiles.
 #include "common.cuh"
 #include "internal.h"
 
@@ -68,12 +85,14 @@ static_assert(kSmemBytes <= 232448, "document attention shared memory");
 constexpr uint32_t kTmS = 0, kTmO = 2 * kKeys, kTmP = kTmO + 128, kTmQ = kTmP + kKeys;
 static_assert(kTmQ + 96 == 512, "tensor memory columns");
 constexpr int kThreads = 384;
+constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on at a time (16 MB: the documents of one
+                                                 // new token 15.9 us where they take 14.7, 8 with a prefix 155 where 150)
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 constexpr int kItemRing = 4;
 
 // A warp's bounded wait, in few instructions: 2^21 tries (tens of milliseconds at
-// least, where the longest wait there is takes microseconds).  A role whose wait
-// gives up stops, and says so at its end.
+// least; a wait is for a few tiles' work, microseconds).  A role whose wait gives
+// up stops, and says so at its end.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   int tries = 1 << 21;
 #pragma unroll 1
@@ -95,14 +114,14 @@ struct Place {
 };
 
 struct Bars {
-  uint64_t q_full, q_tmem, qn_empty, q_free;
+  uint64_t q_full, q_empty, q_free;
   uint64_t item_full[kItemRing], item_empty[kItemRing];
-  uint64_t k_full[kKSlots], k_empty[kKSlots];
-  uint64_t v_full[kVSlots], v_empty[kVSlots], v_cut[kVSlots];
+  uint64_t k_full[3], k_empty[kKSlots];  // full: a whole tile, of those in flight; empty: a slot
+  uint64_t v_full[kVSlots], v_empty[kVSlots], v_cut[kVSlots];  // full and cut: a whole tile, by its first half's slot
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2], pv_done[2];
-  // per quarter of the rows (a warp of each group), so that a warp that does not
-  // wait for a phase has completed it itself
+  // per quarter of the rows (a warp of each group): every phase is one that a warp has
+  // waited for or completed itself, so that its parity cannot be mistaken
   uint64_t ref[2][4], sum[4], o_free[4], o_stored[4];
   uint64_t drain_s, drain_pv;
   uint32_t tmem_slot;
@@ -192,8 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
-    mbar_init(&bar->q_tmem, 128);
-    mbar_init(&bar->qn_empty, 4);
+    mbar_init(&bar->q_empty, 1);
     mbar_init(&bar->q_free, 1);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&bar->item_full[i], 1);
@@ -207,10 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < 4; ++q) mbar_init(&bar->ref[i][q], 32);
     }
 #pragma unroll 1
-    for (int i = 0; i < kKSlots; ++i) {
-      mbar_init(&bar->k_full[i], 1);
-      mbar_init(&bar->k_empty[i], 1);
-    }
+    for (int i = 0; i < kKSlots; ++i) mbar_init(&bar->k_empty[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&bar->k_full[i], 1);
 #pragma unroll 1
     for (int i = 0; i < kVSlots; ++i) {
       mbar_init(&bar->v_full[i], 1);
@@ -250,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int* tiles = reinterpret_cast<const int*>(plan + sizeof(DocPlan)) + min(lane, (int)sizeof(DocTile) / 4 - 1);
     DocTile* const ring = reinterpret_cast<DocTile*>(smem + kTileOff);
     Place<kKSlots> k;
+    Place<3> full;
     int q_loads = 0;
     // Item it + 1 is posted to the ring, where every role finds it, before item `it` is
     // loaded; its tile was fetched (a word a lane) after the item before, its index asked
@@ -276,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int j = 0; ok; ++j) {
         if (j == q_at && it >= -1 && next.rows > 0) {
-          if (it >= 0 && !(ok = wait_for(&bar->qn_empty, it & 1))) break;
+          if (it >= 0 && !(ok = wait_for(&bar->q_empty, it & 1))) break;
           if (elected()) {
             mbar_arrive_expect_tx(&bar->q_full, 3 * kAtom);
             for (int c = 0; c < 3; ++c)
@@ -291,11 +308,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 192; c += 64, k.next()) {
           if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
           if (elected()) {
-            mbar_arrive_expect_tx(&bar->k_full[k.slot], kKeyAtom);
-            tma_load_3d(smem + kKOff + k.slot * kKeyAtom, &tmK, &bar->k_full[k.slot], c, key, tile.head);
+            if (c == 0) mbar_arrive_expect_tx(&bar->k_full[full.slot], 3 * kKeyAtom);
+            tma_load_3d(smem + kKOff + k.slot * kKeyAtom, &tmK, &bar->k_full[full.slot], c, key, tile.head);
           }
           __syncwarp();
         }
+        full.next();
       }
       if (!ok) break;
       index = __shfl_sync(0xffffffffu, index, 0);
@@ -308,31 +326,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       index = after;
     }
-    // no copy may still be in flight into shared memory: the last round of the ring
+    // no copy may still be in flight into shared memory (a tile that was left half issued
+    // never arrives: its wait gives up)
     if (q_loads) ok &= wait_for(&bar->q_full, (q_loads - 1) & 1);
 #pragma unroll 1
-    for (int i = 0; i < kKSlots; ++i, k.next()) ok &= wait_for(&bar->k_full[k.slot], k.phase ^ 1);
+    for (int i = 0; i < 3; ++i, full.next()) ok &= wait_for(&bar->k_full[full.slot], full.phase ^ 1);
   } else if (warp == 1) {
     // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
     constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
     const uint32_t k_addr = smem_u32(smem + kKOff);
     int x = 0;
     Place<kKSlots> k;
+    Place<3> full;
 #pragma unroll 1
     for (int it = 0; ok; ++it) {
       DocTile tile;
       if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
-      if (!(ok = wait_for(&bar->q_tmem, it & 1))) break;  // this item's Q in tensor memory
+      // the item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory as bf16
+      // pairs, the A operand of every S, once the S of the item before are done
+      if (!(ok = wait_for(&bar->q_full, it & 1) && (it == 0 || wait_for(&bar->q_free, (it - 1) & 1)))) break;
+      tc_fence_after();
+      if (elected()) {
+#pragma unroll
+        for (int kk = 0; kk < 12; ++kk)
+          tmem_copy_128x256b(tmem + kTmQ + kk * 8,
+                             sdesc_sw128(smem_u32(smem + kQOff) + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024));
+        umma_commit(&bar->q_empty);  // the staging atoms may take the Q after it
+      }
+      __syncwarp();
 #pragma unroll 1
       for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
         const int sb = x & 1;
-        // the group has read the buffer's previous scores (tile x - 2)
-        if (x > 1 && !(ok = wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))) break;
-        // 64 dimensions at a time, as they arrive
-#pragma unroll 1
+        // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
+        if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
+                   (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
+          break;
+        full.next();
+        tc_fence_after();
+#pragma unroll
         for (int c = 0; c < 3; ++c, k.next()) {
-          if (!(ok = wait_for(&bar->k_full[k.slot], k.phase))) break;
-          tc_fence_after();
           const uint64_t kb = sdesc_sw128(k_addr + k.slot * kKeyAtom, 16, 1024);
           if (elected()) {
 #pragma unroll
@@ -355,83 +387,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // ---- V producer: half tiles, and clears what lies behind the last key ----
     Place<kVSlots> v;
+    uint32_t phases = 0;  // of each slot's full barrier
     if (elected()) tma_prefetch_desc(&tmV);
 #pragma unroll 1
     for (int it = 0; ok; ++it) {
       DocTile tile;
       if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
 #pragma unroll 1
-      for (int h = 0; h < 2 * tile.n_kv; ++h) {
-        // its keys; a second half that no query sees is left out
-        const int keys = tile.keys(h >> 1) - (h & 1) * kHalf;
-        if ((h & 1) && keys <= 0) continue;
-        uint8_t* const at = smem + kVOff + v.slot * 2 * kHalfAtom;
-        if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
-        if (elected()) {
-          mbar_arrive_expect_tx(&bar->v_full[v.slot], 2 * kHalfAtom);
-          const int key = tile.k_row + tile.key0(h >> 1) + (h & 1) * kHalf;
-          tma_load_3d(at, &tmV, &bar->v_full[v.slot], 0, key, tile.head);
-          tma_load_3d(at + kHalfAtom, &tmV, &bar->v_full[v.slot], 64, key, tile.head);
-        }
-        __syncwarp();
-        if (keys < kHalf && (keys == 0 || (keys & 15))) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
-          if (!(ok = wait_for(&bar->v_full[v.slot], v.phase))) break;
-          uint8_t* const mine = at + ((lane >> 3) & 1) * kHalfAtom + (lane & 7) * 16;
+      for (int j = 0; ok && j < tile.n_kv; ++j) {
+        // a second half that no query sees is left out
+        const int keys = tile.keys(j), halves = keys > kHalf ? 2 : 1, first = v.slot;
+        const int key = tile.k_row + tile.key0(j);
 #pragma unroll 1
-          for (int r = keys + (lane >> 4); r < max(16, (keys + 15) & ~15); r += 2)
+        for (int h = 0; h < halves; ++h, v.next()) {
+          if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
+          if (elected()) {
+            if (h == 0) mbar_arrive_expect_tx(&bar->v_full[first], halves * 2 * kHalfAtom);
+            uint8_t* const at = smem + kVOff + v.slot * 2 * kHalfAtom;
+            tma_load_3d(at, &tmV, &bar->v_full[first], 0, key + h * kHalf, tile.head);
+            tma_load_3d(at + kHalfAtom, &tmV, &bar->v_full[first], 64, key + h * kHalf, tile.head);
+          }
+          __syncwarp();
+        }
+        if (ok && (keys == 0 || (keys & 15))) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
+          if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+          const int last = halves == 1 ? first : (first + 1) % kVSlots, from = keys - (halves - 1) * kHalf;
+          uint8_t* const mine = smem + kVOff + (last * 2 + ((lane >> 3) & 1)) * kHalfAtom + (lane & 7) * 16;
+#pragma unroll 1
+          for (int r = from + (lane >> 4); r < max(16, (from + 15) & ~15); r += 2)
             *reinterpret_cast<uint4*>(mine + r * 128) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
-          if (elected()) mbar_arrive(&bar->v_cut[v.slot]);
+          if (elected()) mbar_arrive(&bar->v_cut[first]);
           __syncwarp();
         }
-        v.next();
+        phases ^= 1u << first;
       }
     }
+    // (every tile has arrived: its slot's barrier has left the phase before its next one)
 #pragma unroll 1
-    for (int i = 0; i < kVSlots; ++i, v.next()) ok &= wait_for(&bar->v_full[v.slot], v.phase ^ 1);
+    for (int i = 0; i < kVSlots; ++i) ok &= wait_for(&bar->v_full[i], ((phases >> i) & 1) ^ 1);
   } else if (warp == 3) {
     // ---- P.V issuer: O += P_x V_x ----
     constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
     const uint32_t v_addr = smem_u32(smem + kVOff);
     int x = 0;
     Place<kVSlots> v;
-    uint32_t cuts = 0;  // parity of each slot's cuts so far
+    uint32_t phases = 0, cuts = 0;  // of each slot's full and cut barriers
 #pragma unroll 1
     for (int it = 0; ok; ++it) {
       DocTile tile;
       if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
 #pragma unroll 1
-      for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
-        const int sb = x & 1;
+      for (int j = 0; j < tile.n_kv; ++j, ++x) {
+        const int sb = x & 1, first = v.slot;
+        // the 16-key steps that hold a key (one where there is none: O becomes zeros), the
+        // last one's other rows cleared
+        const int keys = tile.keys(j), steps = max(1, (keys + 15) >> 4);
+        if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+        phases ^= 1u << first;
+        if (keys == 0 || (keys & 15)) {
+          if (!(ok = wait_for(&bar->v_cut[first], (cuts >> first) & 1))) break;
+          cuts ^= 1u << first;
+        }
         // P_x is written (and, for an item's first tile, the previous item's O read)
         if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
-        // the 16-key steps that hold a key (one where there is none: O becomes zeros), half a
-        // tile at a time, the last step's other rows cleared
-        const int all = tile.keys(j);
-#pragma unroll 1
+        tc_fence_after();
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int keys = all - h * kHalf;
-          if (h && keys <= 0) break;
-          if (!(ok = wait_for(&bar->v_full[v.slot], v.phase))) break;
-          if (keys < kHalf && (keys == 0 || (keys & 15))) {
-            if (!(ok = wait_for(&bar->v_cut[v.slot], (cuts >> v.slot) & 1))) break;
-            cuts ^= 1u << v.slot;
-          }
-          tc_fence_after();
+          if (h && keys <= kHalf) break;
           const uint64_t vb = sdesc_sw128(v_addr + v.slot * 2 * kHalfAtom, kHalfAtom, 1024);
           if (elected()) {
 #pragma unroll
             for (int kk = 0; kk < kHalf / 16; ++kk)
-              if (kk * 16 < max(keys, 1))
+              if (h * (kHalf / 16) + kk < steps)
                 umma_bf16_ts(tmem + kTmO, tmem + kTmP + sb * kHalf + h * (kHalf / 2) + kk * 8, vb + kk * 128, idesc_pv,
                              (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
             umma_commit(&bar->v_empty[v.slot]);
-            if (h == 1 || all <= kHalf) umma_commit(&bar->pv_done[sb]);
           }
           __syncwarp();
           v.next();
         }
+        if (elected()) umma_commit(&bar->pv_done[sb]);
+        __syncwarp();
       }
     }
     if (elected()) umma_commit(&bar->drain_pv);
@@ -447,23 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2* const sums = reinterpret_cast<float2*>(smem + kSumOff) + row;
     auto wait = [&](uint64_t& b, int phase) { return wait_for(&b, phase & 1); };
     // Item by item, this group's tiles of each.  At an item's end the group with the
-    // last tile `ends` it: it writes O / l.  The other group has copied the next item's
-    // Q into tensor memory by then, while it worked on its own last tile (every S of the
-    // item is done or on its way at that time), and goes on to that item's first tile,
-    // which is its own.  The first pass (it = -1) has no tiles: its group 0 copies the
-    // first Q.
+    // last tile `ends` it: it writes O / l.  The other group goes on to the next item's
+    // first tile, which is its own.
     int x0 = 0;    // this CTA's key tiles before the item
-    DocTile tile{};
     bool stored = false;  // the staging atoms of O are still being read
 #pragma unroll 1
-    for (int it = -1;; ++it) {
-      const int last = x0 + (it < 0 ? 0 : tile.n_kv) - 1;
+    for (int it = 0;; ++it) {
+      DocTile tile;
+      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+      const int last = x0 + tile.n_kv - 1;
       const bool ends = (last & 1) == g;
       float m = -INFINITY, l = 0.f;  // this group's sum, relative to 2^m
-      const int next_slot = (it + 1) % kItemRing;
-      const DocTile& next = reinterpret_cast<const DocTile*>(smem + kTileOff)[next_slot];
-      if (!(ok = wait(bar->item_full[next_slot], (it + 1) / kItemRing))) break;
-      bool to_copy = !ends && next.rows > 0;
 #pragma unroll 1
       for (int x = x0 + ((x0 ^ g) & 1);; x += 2) {
         const bool here = x <= last;
@@ -488,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (in_sinks ? k0 + kKeys > tile.n_first
                        : k0 + kKeys > tile.prefix && (first + 31 - k0 >= window || k0 + kKeys - 1 > first)) {
             const int i = first + lane;
-            const int hi = in_sinks ? 0 : i + 1 - k0, lo = i + 1 - window - k0, near = max(tile.prefix, min(sinks, i + 1)) - k0;
+            const int hi = in_sinks ? 0 : i + 1 - k0, lo = i + 1 - window - k0;
+            const int near = max(tile.prefix, min(sinks, i + 1)) - k0;
 #pragma unroll
             for (int c0 = 0; c0 < kKeys; c0 += 32) {
               const uint32_t seen = (first_bits(hi - c0) & ~first_bits(lo - c0)) | first_bits(near - c0);
@@ -537,32 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           stored = false;
         }
-        if (to_copy && x + 2 > last) {
-          // the next item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory
-          // as bf16 pairs, the A operand of every S, once the S of this item are done
-          if (!(ok = (it < 0 || wait(bar->q_free, it)) && wait(bar->q_full, it + 1))) break;
-          tc_fence_after();
-          const uint8_t* qrow = smem + kQOff + row * 128;
-#pragma unroll 1
-          for (int c = 0; c < 3; ++c) {
-            uint32_t v[32];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kAtom + ((q ^ (row & 7)) << 4));
-              v[4 * q] = u.x;
-              v[4 * q + 1] = u.y;
-              v[4 * q + 2] = u.z;
-              v[4 * q + 3] = u.w;
-            }
-            tmem_st32(tmem + lanes + kTmQ + c * 32, v);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bar->q_tmem);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->qn_empty);  // the staging atoms may take the Q after it
-          to_copy = false;
-        }
         if (!here) break;
         // this group's tile before has been read: its P may be replaced
         if (x > 1 && !(ok = wait(bar->pv_done[g], (x - 2) >> 1))) break;
@@ -591,10 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar->p_full[g]);
       }
       if (!ok) break;
-      if (it >= 0 && !ends) {
+      if (!ends) {
         *sums = make_float2(l, m);
         mbar_arrive(&bar->sum[quarter]);
-      } else if (it >= 0) {
+      } else {
         // O / l through this row of the staging atoms, once the O before has left them, and a
         // TMA store; where the document ends among this warp's rows, each row that it has is
         // stored by itself
@@ -642,10 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         stored = true;
       }
       x0 = last + 1;
-      tile = next;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->item_empty[next_slot]);
-      if (tile.rows == 0) break;
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -661,20 +664,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- the documents' query tiles ------------------------------------------------
-constexpr int kDocPlanThreads = 1024;
-constexpr int kDocBuckets = 1024;  // tiles are ordered by their number of key tiles, up to this many
-constexpr int kDocsInSmem = 4096;
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = kPlanThreads;  // tiles are ordered by their number of key tiles, up to this many
+constexpr int kDocsInSmem = 1024;
 
-// Document d's rows and keys.
+// A document's rows and keys.
 struct Doc {
   int q0, n, k0, keys, prefix;
+  __device__ __forceinline__ Doc() {}
   __device__ __forceinline__ Doc(const DocAttnArgs& a, int d) {
     const int* ck = a.cu_k ? a.cu_k : a.cu_q;
+    const int q1 = a.cu_q[d + 1], k1 = ck[d + 1], p = a.prefix ? a.prefix[d] : 0;
     q0 = a.cu_q[d];
-    n = a.cu_q[d + 1] - q0;
     k0 = ck[d];
-    keys = ck[d + 1] - k0;
-    prefix = a.prefix ? max(0, min(a.prefix[d], keys)) : 0;
+    n = q1 - q0;
+    keys = k1 - k0;
+    prefix = max(0, min(p, keys));
+  }
+  __device__ __forceinline__ bool bad(const DocAttnArgs& a) const {
+    // (differences of numbers in range do not overflow; of others any answer but "in order" will do)
+    return q0 < 0 || q0 > a.N || n < 0 || n > a.N - q0 || k0 < 0 || k0 > a.cap || keys < 0 || keys > a.cap - k0;
   }
 };
 
@@ -689,49 +698,51 @@ __device__ __forceinline__ int block_before(int v, int& total, int* sh) {
   }
   if (lane == 31) sh[warp] = x;
   __syncthreads();
-  int before = x - v;
-  total = 0;
-#pragma unroll 8
-  for (int w = 0; w < kDocPlanThreads / 32; ++w) {
-    if (w < warp) before += sh[w];
-    total += sh[w];
+  int w = sh[lane];  // (as many warps as lanes)
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
   __syncthreads();
-  return before;
+  return before + x - v;
 }
+static_assert(kPlanThreads == 32 * 32, "a lane for each warp");
 
 // One CTA: the documents' numbers of query tiles, the tiles' numbers of key
 // tiles counted by value, and the tiles in that order, the heaviest first (the
 // order among equals is any: an item's result does not depend on it).  An
 // offset that is out of order or out of range leaves the plan empty.
-__global__ void __launch_bounds__(kDocPlanThreads, 1)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     doc_plan_kernel(const DocAttnArgs a, int window, int sinks, int grid, int* work, uint32_t* status) {
-  __shared__ int first_smem[kDocsInSmem + 1];
-  __shared__ int bucket[kDocBuckets];
-  __shared__ int sh[kDocPlanThreads / 32];
-  __shared__ unsigned long long all_key_tiles;
+  __shared__ Doc doc_smem[kDocsInSmem];
+  __shared__ int first_smem[kDocsInSmem];
+  __shared__ int bucket[kBuckets];
+  __shared__ int sh[32];
+  __shared__ unsigned long long key_tiles;
   __shared__ int heaviest;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
-  int* first = a.n_docs <= kDocsInSmem ? first_smem : a.first_tile;
+  const bool in_smem = a.n_docs <= kDocsInSmem;
+  int* first = in_smem ? first_smem : a.first_tile;
   bucket[tid] = 0;
   if (tid == 0) {
-    all_key_tiles = 0;
+    key_tiles = 0;
     heaviest = 1;
   }
   bool bad = false;
   int n_tiles = 0;
-  const int* ck = a.cu_k ? a.cu_k : a.cu_q;
-  for (int d0 = 0; d0 < a.n_docs; d0 += kDocPlanThreads) {
+  for (int d0 = 0; d0 < a.n_docs; d0 += kPlanThreads) {
     const int d = d0 + tid;
     int mine = 0, total;
     if (d < a.n_docs) {
-      const int q0 = a.cu_q[d], q1 = a.cu_q[d + 1], k0 = ck[d], k1 = ck[d + 1];
-      if (q0 < 0 || q1 < q0 || q1 > a.N || k0 < 0 || k1 < k0 || k1 > a.cap)
-        bad = true;
-      else
-        mine = (q1 - q0 + 127) / 128;
+      const Doc doc(a, d);
+      bad |= doc.bad(a);
+      mine = bad ? 0 : (doc.n + 127) / 128;
+      if (in_smem) doc_smem[d] = doc;
     }
     const int before = block_before(mine, total, sh);
     if (d < a.n_docs) first[d] = n_tiles + before;
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(kDocPlanThreads, 1)
     }
     return;
   }
-  // tile t: its document is the last one that begins at or before it (and has tiles)
+  // tile t: its document is the last one that begins at or before it
   auto tile_of = [&](int t) {
     int lo = 0, hi = a.n_docs - 1;
     while (lo < hi) {
@@ -762,7 +773,11 @@ __global__ void __launch_bounds__(kDocPlanThreads, 1)
       else
         hi = mid - 1;
     }
-    const Doc d(a, lo);
+    Doc d;
+    if (in_smem)
+      d = doc_smem[lo];
+    else
+      d = Doc(a, lo);
     const int at = (t - first[lo]) * 128;
     DocTile tile{};
     tile.q_row = d.q0 + at;
@@ -773,33 +788,48 @@ __global__ void __launch_bounds__(kDocPlanThreads, 1)
     tile.set_keys(window, sinks);
     return tile;
   };
-  for (int t = tid; t < n_tiles; t += kDocPlanThreads) {
-    const int n_kv = tile_of(t).n_kv;
-    atomicAdd(&bucket[kDocBuckets - 1 - min(n_kv, kDocBuckets - 1)], 1);
-    atomicAdd(&all_key_tiles, (unsigned long long)n_kv);
-    atomicMax(&heaviest, n_kv);
+  auto bucket_of = [&](const DocTile& t) { return &bucket[kBuckets - 1 - min(t.n_kv, kBuckets - 1)]; };
+  unsigned long long sum = 0;
+  int most = 0;
+  DocTile kept{};  // this thread's first tile
+  for (int t = tid; t < n_tiles; t += kPlanThreads) {
+    const DocTile tile = tile_of(t);
+    if (t == tid) kept = tile;
+    atomicAdd(bucket_of(tile), 1);
+    sum += tile.n_kv;
+    most = max(most, tile.n_kv);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  if ((tid & 31) == 0 && most > 0) {
+    atomicAdd(&key_tiles, sum);
+    atomicMax(&heaviest, most);
   }
   __syncthreads();
   {
     int total;
-    const int before = block_before(bucket[tid], total, sh);
-    bucket[tid] = before;
+    bucket[tid] = block_before(bucket[tid], total, sh);
   }
   __syncthreads();
-  for (int t = tid; t < n_tiles; t += kDocPlanThreads) {
-    const DocTile tile = tile_of(t);
-    const int n_kv = tile.n_kv;
-    tiles[atomicAdd(&bucket[kDocBuckets - 1 - min(n_kv, kDocBuckets - 1)], 1)] = tile;
+  for (int t = tid; t < n_tiles; t += kPlanThreads) {
+    const DocTile tile = t == tid ? kept : tile_of(t);
+    tiles[atomicAdd(bucket_of(tile), 1)] = tile;
   }
   if (tid == 0) {
-    // the head group, by the rule of launch_prefill_attention
-    const unsigned long long need = (3ull * grid * heaviest + 2 * all_key_tiles - 1) / (2 * all_key_tiles);
+    // Heads a group, a power of two: the smallest whose work is at least 1.5 times the CTA
+    // count times the heaviest item (the heavy tiles of the last group then start early
+    // enough), halved while its heads' K/V exceed kGroupBytes of L2
+    const unsigned long long need = (3ull * grid * heaviest + 2 * key_tiles - 1) / (2 * key_tiles);
+    const int* ck = a.cu_k ? a.cu_k : a.cu_q;
     const long long kv_head_bytes = ((long long)ck[a.n_docs] - ck[0]) * (192 + 128) * 2;
-    int G = 1;
-    while ((unsigned long long)G < need && G < 64) G *= 2;
-    while (G > 1 && G * kv_head_bytes > (16ll << 20)) G /= 2;
+    int log = 0;
+    while ((1ull << log) < need && log < 6) ++log;
+    while (log > 0 && (kv_head_bytes << log) > kGroupBytes) --log;
     head->n_tiles = n_tiles;
-    head->group_log = __ffs(G) - 1;
+    head->group_log = log;
   }
 }
 }  // namespace
@@ -820,7 +850,7 @@ cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost&
   int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
   const long long items = 64 * doc_tiles_at_most(a.N, a.n_docs);
   const int grid = items < num_sms ? (int)items : num_sms;
-  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kDocPlanThreads), 0, stream, a, window, sinks, grid,
+  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, window, sinks, grid,
                                    work, st.word);
   if (e != cudaSuccess) return e;
   DevStatus dst{st.word, st.wait_limit_ns};

@@ -270,6 +270,12 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// 128 rows x 32 bytes from shared memory (a matrix descriptor) into 8 tensor-memory
+// columns, row m in lane m; ordered ahead of this thread's products that follow.
+__device__ __forceinline__ void tmem_copy_128x256b(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // Arrive (once) on an mbarrier when all previously issued tcgen05 async
 // operations of this thread have completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
