@@ -44,32 +44,46 @@ __device__ __forceinline__ void store_status(uint32_t* status, int cta, int ctas
   status[kStatusExtraFirst + cta] = word;
 }
 
-// Exclusive sum over the block's threads (all of kPlanThreads), and the total.
-__device__ __forceinline__ long long block_sum(long long v, long long& total, long long* sh) {
+// Exclusive sums over the block's threads (all of kPlanThreads) of two numbers,
+// and the totals.
+__device__ __forceinline__ void block_sums(int& u, int& u_total, long long& v, long long& v_total, int* shu, long long* shv) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  int x = u;
+  long long y = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = sh[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
+    const int p = __shfl_up_sync(0xffffffffu, x, o);
+    const long long q = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += p;
+      y += q;
     }
-    sh[lane] = w;
+  }
+  if (lane == 31) {
+    shu[warp] = x;
+    shv[warp] = y;
   }
   __syncthreads();
-  total = sh[kPlanThreads / 32 - 1];
-  const long long before = x - v + (warp > 0 ? sh[warp - 1] : 0);
+  int wx = shu[lane];  // (as many warps as lanes)
+  long long wy = shv[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int p = __shfl_up_sync(0xffffffffu, wx, o);
+    const long long q = __shfl_up_sync(0xffffffffu, wy, o);
+    if (lane >= o) {
+      wx += p;
+      wy += q;
+    }
+  }
+  u_total = __shfl_sync(0xffffffffu, wx, 31);
+  v_total = __shfl_sync(0xffffffffu, wy, 31);
+  const int bx = __shfl_sync(0xffffffffu, wx, max(warp - 1, 0));
+  const long long by = __shfl_sync(0xffffffffu, wy, max(warp - 1, 0));
+  u = x - u + (warp > 0 ? bx : 0);
+  v = y - v + (warp > 0 ? by : 0);
   __syncthreads();
-  return before;
 }
+static_assert(kPlanThreads == 32 * 32, "a lane for each warp");
 
 // ---- giving pages back --------------------------------------------------------
 // Grid: items (list entry, 1,024 entries of its row) in turn.
@@ -115,21 +129,25 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagePool p, const
 }
 
 // ---- the plan -------------------------------------------------------------------
+// A variable of the cluster's first CTA, this CTA's of which is at `local`.
+__device__ __forceinline__ void put_first(int* local, int x) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_rank(smem_u32(local), 0)), "r"(x) : "memory");
+}
+__device__ __forceinline__ int get_first(const int* local) {
+  int x;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(mapa_rank(smem_u32(local), 0)) : "memory");
+  return x;
+}
+
 enum class PageOp { kReserve, kFork, kCompact };
 
-// What list entry i of a reservation or fork needs: pages, or -1 if it cannot
-// be carried out.  One warp.
+// What a list entry of a reservation or fork needs: pages, or -1 if it cannot be
+// carried out.  One warp.
 template <PageOp OP>
-__device__ __forceinline__ int pages_needed(const PagePlanArgs& a, int i, bool& bad) {
-  const PagePool& p = a.pool;
+__device__ __forceinline__ int pages_needed(const PagePool& p, int r, int parent, int pos, bool& bad) {
   const int lane = threadIdx.x & 31;
-  const int r = a.rows[i], pos = a.P[i];
-  int parent = 0;
   bool ok = r >= 0 && r < p.rows && pos >= 0 && pos <= p.max_pages * p.page;
-  if (OP == PageOp::kFork) {
-    parent = a.parents[i];
-    ok = ok && parent >= 0 && parent < p.rows;
-  }
+  if (OP == PageOp::kFork) ok = ok && parent >= 0 && parent < p.rows;
   if (!ok) {
     bad = true;
     return -1;
@@ -138,7 +156,7 @@ __device__ __forceinline__ int pages_needed(const PagePlanArgs& a, int i, bool& 
   const int* row = p.table + (size_t)r * p.max_pages;
   int missing = 0;
   if (OP == PageOp::kReserve) {
-#pragma unroll 4
+#pragma unroll 8
     for (int e0 = 0; e0 < want; e0 += 32) {
       const int x = e0 + lane < want ? row[e0 + lane] : 0;
       missing += __popc(__ballot_sync(0xffffffffu, x < 0));
@@ -164,107 +182,152 @@ __device__ __forceinline__ int pages_needed(const PagePlanArgs& a, int i, bool& 
 
 template <PageOp OP>
 __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PagePlanArgs a) {
-  __shared__ long long sums[32];
-  __shared__ int claims_smem[OP == PageOp::kCompact ? 1 : kClaimsInSmem];
+  constexpr bool kList = OP != PageOp::kCompact;
+  __shared__ int sums_seg[32];
+  __shared__ long long sums_need[32];
+  __shared__ int claims_smem[kList ? kClaimsInSmem : 1];
+  // the first CTA's: what the others tell it and what it tells them, of lists and pools that
+  // are not larger (else in the workspace)
+  __shared__ int need_smem[kList ? kPlanThreads : 1];
+  __shared__ int seg_smem[kPlanThreads];
+  __shared__ int head[2];
   pdl_launch_dependents();
   pdl_wait();
   const PagePool& p = a.pool;
   const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31;
-  const int warp = rank * (kPlanThreads / 32) + (tid >> 5), warps = kPlanCtas * (kPlanThreads / 32);
+  const int warp = (tid >> 5) * kPlanCtas + rank, warps = kPlanCtas * (kPlanThreads / 32);  // (the first few: one a CTA)
   const int n_seg = (p.n_pages + kSeg - 1) / kSeg;
+  const bool list_near = a.n <= kPlanThreads, seg_near = n_seg <= kPlanThreads;
   bool bad = false;
+  cluster_sync();  // (the first CTA's shared memory may be written from here on)
 
-  // 1. free pages as bits, their number in each segment; what the list needs
+  // 1. free pages as bits, their number in each segment; what the list needs (by the last
+  // warps first: the segments are the first ones')
+  uint32_t bits0 = 0;  // this warp's first segment
   for (int s = warp; s < n_seg; s += warps) {
     uint32_t mine = 0;
     int count = 0;
-#pragma unroll 8
+    bool free_at[32];
+#pragma unroll
     for (int j = 0; j < 32; ++j) {
       const int at = s * kSeg + j * 32 + lane;
-      const uint32_t b = __ballot_sync(0xffffffffu, at < p.n_pages && p.refs[at] <= 0);
+      free_at[j] = at < p.n_pages && p.refs[at] <= 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t b = __ballot_sync(0xffffffffu, free_at[j]);
       count += __popc(b);
       if (lane == j) mine = b;
     }
     a.bits[(size_t)s * 32 + lane] = mine;
-    if (lane == 0) a.seg[s] = count;
+    if (s == warp) bits0 = mine;
+    if (lane == 0) {
+      if (seg_near)
+        put_first(&seg_smem[s], count);
+      else
+        a.seg[s] = count;
+    }
   }
-  if (OP != PageOp::kCompact) {
-    for (int i = warp; i < a.n; i += warps) {
-      const int need = pages_needed<OP>(a, i, bad);
-      if (lane == 0) a.need[i] = need;
+  if (kList) {
+    // (a warp's next 32 entries at once, one a lane)
+    for (int i0 = warps - 1 - warp; i0 < a.n; i0 += 32 * warps) {
+      const int mine = i0 + lane * warps;
+      const bool in = mine < a.n;
+      const int row = in ? a.rows[mine] : 0, pos = in ? a.P[mine] : 0;
+      const int parent = OP == PageOp::kFork && in ? a.parents[mine] : 0;
+      int need = 0;
+      for (int k = 0; k < 32 && i0 + k * warps < a.n; ++k) {
+        const int x = pages_needed<OP>(p, __shfl_sync(0xffffffffu, row, k), __shfl_sync(0xffffffffu, parent, k),
+                                       __shfl_sync(0xffffffffu, pos, k), bad);
+        if (lane == k) need = x;
+      }
+      if (in) {
+        if (list_near)
+          put_first(&need_smem[mine], need);
+        else
+          a.need[mine] = need;
+      }
     }
   }
   cluster_sync();
 
   // 2. one CTA: list entries whose row an earlier one has taken; sums
   if (rank == 0) {
-    if (OP != PageOp::kCompact && a.n > 1) {
+    if (kList && a.n > 1) {
       int* claim = p.rows <= kClaimsInSmem ? claims_smem : a.claims;
       for (int i = tid; i < a.n; i += kPlanThreads)
-        if (__ldcg(a.need + i) >= 0) claim[a.rows[i]] = INT32_MAX;
+        if ((list_near ? need_smem[i] : __ldcg(a.need + i)) >= 0) claim[a.rows[i]] = INT32_MAX;
       __syncthreads();
       for (int i = tid; i < a.n; i += kPlanThreads)
-        if (__ldcg(a.need + i) >= 0) atomicMin(claim + a.rows[i], i);
+        if ((list_near ? need_smem[i] : __ldcg(a.need + i)) >= 0) atomicMin(claim + a.rows[i], i);
       __syncthreads();
       for (int i = tid; i < a.n; i += kPlanThreads)
-        if (__ldcg(a.need + i) >= 0 && *(volatile int*)(claim + a.rows[i]) != i) {
-          a.need[i] = -1;
+        if ((list_near ? need_smem[i] : __ldcg(a.need + i)) >= 0 && *(volatile int*)(claim + a.rows[i]) != i) {
+          if (list_near)
+            need_smem[i] = -1;
+          else
+            a.need[i] = -1;
           bad = true;
         }
-      __syncthreads();
     }
-    long long free_pages = 0, taken = 0, total = 0;
-    for (int s0 = 0; s0 < n_seg; s0 += kPlanThreads) {
-      const int s = s0 + tid;
-      const long long before = block_sum(s < n_seg ? __ldcg(a.seg + s) : 0, total, sums);
-      if (s < n_seg) a.seg[s] = (int)(free_pages + before);
-      free_pages += total;
-    }
-    if (OP != PageOp::kCompact) {
-      for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
-        const int i = i0 + tid, need = i < a.n ? __ldcg(a.need + i) : 0;
-        const long long before = block_sum(need > 0 ? need : 0, total, sums);
-        if (i < a.n) a.first[i] = need < 0 ? -1 : (int)min((long long)INT32_MAX, taken + before);
-        taken += total;
+    int free_pages = 0, seg_total;
+    long long taken = 0, need_total;
+    for (int i0 = 0; i0 < max(n_seg, kList ? a.n : 0); i0 += kPlanThreads) {
+      const int i = i0 + tid;
+      int seg = i < n_seg ? (seg_near ? seg_smem[i] : __ldcg(a.seg + i)) : 0;
+      const int need = kList && i < a.n ? (list_near ? need_smem[i] : __ldcg(a.need + i)) : 0;
+      long long before = max(need, 0);
+      block_sums(seg, seg_total, before, need_total, sums_seg, sums_need);
+      if (i < n_seg) {
+        if (seg_near)
+          seg_smem[i] = free_pages + seg;
+        else
+          a.seg[i] = free_pages + seg;
       }
+      if (kList && i < a.n) a.first[i] = need < 0 ? -1 : (int)min((long long)INT32_MAX, taken + before);
+      free_pages += seg_total;
+      taken += need_total;
+    }
+    __syncthreads();
+    if (kList) {
       if (tid == 0) {
-        a.head[0] = taken <= free_pages;
-        a.head[1] = taken <= free_pages ? (int)taken : 0;
+        head[0] = taken <= free_pages;
+        head[1] = taken <= free_pages ? (int)taken : 0;
       }
       if (taken > free_pages) {
         if (tid == 0) store_status(a.status, 0, kPlanCtas, kStatusNoPages);
         bad = false;
       }
-    } else {
-      const int n_live = p.n_pages - (int)free_pages;
-      __syncthreads();
-      if (tid < 32) {  // free pages below n_live: as many as there are live ones from it on
-        const int s = n_live / kSeg, in_seg = n_live - s * kSeg;
-        int below = 0;
-        if (s < n_seg) {
-          const uint32_t b = __ldcg(a.bits + (size_t)s * 32 + lane);
-          const int k = in_seg - lane * 32;  // bits of this word that lie below
-          below = __popc(k >= 32 ? b : k <= 0 ? 0u : b & ((1u << k) - 1u));
+    } else if (tid < 32) {  // free pages below n_live: as many as there are live ones from it on
+      const int n_live = p.n_pages - free_pages;
+      const int s = n_live / kSeg, in_seg = n_live - s * kSeg;
+      int below = 0;
+      if (s < n_seg) {
+        const uint32_t b = __ldcg(a.bits + (size_t)s * 32 + lane);
+        const int k = in_seg - lane * 32;  // bits of this word that lie below
+        below = __popc(k >= 32 ? b : k <= 0 ? 0u : b & ((1u << k) - 1u));
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
-        }
-        if (lane == 0) {
-          const int moves = s < n_seg ? *(volatile int*)(a.seg + s) + below : (int)free_pages;
-          a.head[0] = n_live;
-          a.head[1] = moves;
-          *a.n_live = n_live;
-        }
+        for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
       }
+      if (lane == 0) {
+        head[0] = n_live;
+        head[1] = s < n_seg ? (seg_near ? seg_smem[s] : *(volatile int*)(a.seg + s)) + below : free_pages;
+        *a.n_live = n_live;
+      }
+    }
+    if (tid == 0) {
+      a.head[0] = head[0];
+      a.head[1] = head[1];
     }
   }
   cluster_sync();
 
   // 3. the pages in question, by rank
-  const int h0 = __ldcg(a.head), h1 = __ldcg(a.head + 1);
+  const int h0 = get_first(&head[0]), h1 = get_first(&head[1]);
   for (int s = warp; s < n_seg; s += warps) {
-    const int before = __ldcg(a.seg + s);
-    if (OP != PageOp::kCompact && before >= h1) break;  // (the sums grow)
-    const uint32_t mine = __ldcg(a.bits + (size_t)s * 32 + lane);
+    const int before = seg_near ? get_first(&seg_smem[s]) : __ldcg(a.seg + s);
+    const uint32_t mine = s == warp ? bits0 : __ldcg(a.bits + (size_t)s * 32 + lane);
+    if (kList && before >= h1) break;  // (the sums grow)
     int at = __popc(mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -272,12 +335,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PageP
       if (lane >= o) at += y;
     }
     at += before - __popc(mine);  // free pages before this lane's word
+#pragma unroll 8
     for (int j = 0; j < 32; ++j) {
       const uint32_t b = __shfl_sync(0xffffffffu, mine, j);
       const int k = __shfl_sync(0xffffffffu, at, j) + __popc(b & ((1u << lane) - 1u));  // free pages before page q
       const int q = s * kSeg + j * 32 + lane;
       const bool is_free = (b >> lane) & 1u;
-      if (OP != PageOp::kCompact) {
+      if (kList) {
         if (is_free && k < h1) a.fresh[k] = q;
       } else if (q < p.n_pages) {
         if (is_free && q < h0) a.fresh[k] = q;
@@ -286,9 +350,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PageP
       }
     }
   }
+  cluster_sync();  // (the first CTA's shared memory is read no more)
   if (OP == PageOp::kCompact) {
     // 4. the moved pages' holds and new numbers
-    cluster_sync();
     for (int i = rank * kPlanThreads + tid; i < h1; i += kPlanCtas * kPlanThreads) {
       const int src = __ldcg(a.from + i), dst = __ldcg(a.fresh + i);
       a.moved[src] = dst;
@@ -297,13 +361,43 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PageP
     }
     // (the launch that follows reports on the table)
   } else {
+    if (OP == PageOp::kReserve && h0 && a.n <= kPlanCtas * (kPlanThreads / 32)) {
+      // 4. the rows of a short list, a warp each
+      const int i = warps - 1 - warp;
+      int at = i < a.n ? __ldcg(a.first + i) : -1;
+      if (at >= 0) {
+        const int want = pages_of(a.P[i], p.page);
+        int* row = p.table + (size_t)a.rows[i] * p.max_pages;
+        for (int e0 = 0; e0 < want; e0 += 256) {
+          bool none[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int e = e0 + c * 32 + lane;
+            none[c] = e < want && row[e] < 0;
+          }
+          int page[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t b = __ballot_sync(0xffffffffu, none[c]);
+            page[c] = none[c] ? __ldcg(a.fresh + at + __popc(b & ((1u << lane) - 1u))) : 0;
+            at += __popc(b);
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (none[c]) {
+              row[e0 + c * 32 + lane] = page[c];
+              p.refs[page[c]] = 1;
+            }
+        }
+      }
+    }
     bad = __syncthreads_or(bad);
     if (tid == 0 && (rank != 0 || h0)) store_status(a.status, rank, kPlanCtas, bad ? kStatusBadLength : 0u);
   }
 }
 
 // ---- the changes ----------------------------------------------------------------
-// A CTA a list entry in turn: 1,024 entries of the row at a time.
+// The rows of a long list: a CTA each in turn, 1,024 entries at a time.
 __global__ void __launch_bounds__(256) pages_reserve_kernel(const PagePlanArgs a) {
   __shared__ int counts[2][8];
   pdl_launch_dependents();
@@ -543,7 +637,9 @@ cudaError_t launch_pages_free(const PagePool& p, const int* rows, const int* P, 
 
 cudaError_t launch_pages_reserve(const PagePlanArgs& a, int num_sms, cudaStream_t stream) {
   const cudaError_t e = launch_plan<PageOp::kReserve>(a, stream);
-  if (e != cudaSuccess) return e;
+  // (a list of at most one row for each of the plan's warps is done: 64 rows, given back and
+  // taken again, 12.9 us with a second launch, 10.8 without; 600 rows 27.0 without, 21 with)
+  if (e != cudaSuccess || a.n <= kPlanCtas * (kPlanThreads / 32)) return e;
   const int grid = a.n < 4 * num_sms ? a.n : 4 * num_sms;
   return launch_pdl(pages_reserve_kernel, dim3(grid), dim3(256), 0, stream, a);
 }
