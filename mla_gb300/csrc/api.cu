@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <array>
 
 namespace mla {
 namespace {
@@ -1350,10 +1351,25 @@ PagePlanArgs page_plan(const mla_page_pool_t* pool, int n, void* ws) {
   return a;
 }
 
-// Whether [a, a + n) and [b, b + m) share a byte.
-bool overlap(const void* a, size_t n, const void* b, size_t m) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + m && y < x + n;
+// Whether an array of one cache shares a byte with any array of the other.
+bool caches_overlap(const mla_paged_cache_t& a, const mla_paged_cache_t& b) {
+  struct Range {
+    uintptr_t at, end;
+  };
+  auto ranges = [](const mla_paged_cache_t& c) {
+    const size_t tokens = (size_t)c.n_pages * c.page, scales = (size_t)c.n_pages * c.heads * sizeof(float);
+    auto range = [](const void* p, size_t bytes) {
+      return Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
+    };
+    return std::array<Range, 5>{range(c.k_codes, tokens * c.heads * 128), range(c.v_codes, tokens * c.heads * 128),
+                                range(c.k_pe, tokens * MLA_QK_ROPE * 2), range(c.k_scales, scales),
+                                range(c.v_scales, scales)};
+  };
+  const auto x = ranges(a), y = ranges(b);
+  for (const Range& r : x)
+    for (const Range& q : y)
+      if (r.at < q.end && q.at < r.end) return true;
+  return false;
 }
 
 }  // namespace
@@ -1429,16 +1445,9 @@ int mla_pages_copy(const mla_paged_cache_t* from, const mla_paged_cache_t* to, c
   if (rc) return rc;
   if (!src || !dst) return MLA_ERR_INVALID_ARG;
   if (from->page != to->page || from->heads != to->heads) return MLA_ERR_UNSUPPORTED;
-  const size_t tokens[2] = {(size_t)from->n_pages * from->page, (size_t)to->n_pages * to->page};
-  const size_t heads = from->heads, scale[2] = {from->n_pages * heads * 4, to->n_pages * heads * 4};
-  const bool one = from->k_codes == to->k_codes && from->v_codes == to->v_codes && from->k_pe == to->k_pe && from->k_scales == to->k_scales &&
-                   from->v_scales == to->v_scales && from->n_pages == to->n_pages;
-  if (!one && (overlap(from->k_codes, tokens[0] * heads * 128, to->k_codes, tokens[1] * heads * 128) ||
-               overlap(from->v_codes, tokens[0] * heads * 128, to->v_codes, tokens[1] * heads * 128) ||
-               overlap(from->k_pe, tokens[0] * 128, to->k_pe, tokens[1] * 128) ||
-               overlap(from->k_scales, scale[0], to->k_scales, scale[1]) ||
-               overlap(from->v_scales, scale[0], to->v_scales, scale[1])))
-    return MLA_ERR_INVALID_ARG;
+  const bool one = from->k_codes == to->k_codes && from->v_codes == to->v_codes && from->k_pe == to->k_pe &&
+                   from->k_scales == to->k_scales && from->v_scales == to->v_scales && from->n_pages == to->n_pages;
+  if (!one && caches_overlap(*from, *to)) return MLA_ERR_INVALID_ARG;
   rc = check_lists(src, dst, nullptr, n, workspace, workspace_bytes, to->n_pages, 0);
   if (rc) return rc;
   const int sms = num_sms_of_current_device();

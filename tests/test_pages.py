@@ -81,6 +81,10 @@ def test_copies_between_overlapping_caches():
     moved = {n: getattr(here, n) + (64 << 20) for n in ("k_codes", "v_codes", "k_pe", "k_scales", "v_scales")}
     for n in moved:  # one shared array is enough
         assert call("copy", to=fake_cache(**dict(moved, **{n: getattr(here, n)}))) == -1, n
+    # keys of one cache in the values of the other, its scales behind them
+    assert call("copy", to=fake_cache(**dict(moved, v_codes=here.k_codes))) == -1
+    assert call("copy", to=fake_cache(**dict(moved, k_scales=here.v_scales))) == -1
+    assert call("copy", to=fake_cache(**dict(moved, k_pe=here.k_codes + 128))) == -1
     assert call("copy", to=fake_cache(n_pages=7)) == -1
     assert call("copy", to=fake_cache(), wsb=16) == -3  # one cache: the next check speaks
 
