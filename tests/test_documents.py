@@ -288,3 +288,43 @@ def test_captured_and_on_two_streams(gpu_available):
             m.mla_document_attention(q, cus[i], k, v, outs[i], wss[i], stream=streams[i])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@gpu
+def test_rows_past_32_bit_offsets(gpu_available):
+    """Caches of more than 2^32 numbers and rows of q and out that lie as far apart: the same bits as packed ones."""
+    import torch
+    new, past, at, cap = [130, 1, 33], [50, 200, 0], 399000, 400000
+    cu_q, cu_k = starts(new), starts([a + b for a, b in zip(new, past)])
+    q, k, v = normal(1, cu_q[-1], 64 * 192), normal(2, 64, cu_k[-1], 192), normal(3, 64, cu_k[-1], 128)
+    want = run(q, k, v, cu_q, cu_k, [100, 0, 33])
+    far_k, far_v = (torch.empty((64, cap, n), dtype=torch.bfloat16, device="cuda") for n in (192, 128))
+    far_k[:, at:at + cu_k[-1]], far_v[:, at:at + cu_k[-1]] = k, v
+    far_q, far_o = (torch.empty((cu_q[-1], 1 << 25), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    far_q[:, :64 * 192] = q
+    ws = m.alloc_workspace(m.MODE_DOCUMENTS, 3, cu_q[-1])
+    m.mla_document_attention(far_q[:, :64 * 192], ints(cu_q), far_k, far_v, far_o[:, :64 * 128], ws,
+                             cu_k=ints([c + at for c in cu_k]), prefix=ints([100, 0, 33]))
+    assert m.mla_device_status(ws) == 0
+    assert torch.equal(far_o[:, :64 * 128], want)
+
+
+@gpu
+def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
+    import torch
+    q, k, v = normal(1, 30, 64 * 192), normal(2, 64, 40, 192), normal(3, 64, 40, 128)
+    good = dict(q=q, cu_q=ints([0, 10, 30]), k_cache=k, v_cache=v, out=torch.empty_like(q[:, :64 * 128].contiguous()),
+                workspace=m.alloc_workspace(m.MODE_DOCUMENTS, 2, 30), cu_k=ints([0, 20, 40]), prefix=ints([3, 4]))
+    m.mla_document_attention(**good)
+    for over in (dict(q=q[:29]), dict(q=q.float()), dict(q=q[:, :-8]), dict(q=q.cpu()), dict(q=q.t()),
+                 dict(out=good["out"][:29]), dict(out=good["out"].half()), dict(out=good["out"].cpu()),
+                 dict(k_cache=k[:63]), dict(k_cache=k[:, :39]), dict(k_cache=k.float()), dict(k_cache=k.transpose(0, 1)),
+                 dict(v_cache=v[..., :64]), dict(v_cache=v.cpu()), dict(cu_q=good["cu_q"].long()),
+                 dict(cu_q=ints([0, 1, 10, 30])), dict(cu_k=ints([0, 40])), dict(cu_k=good["cu_k"].cpu()),
+                 dict(prefix=ints([1, 2, 3])), dict(prefix=ints([1, 0, 2, 0])[::2]), dict(workspace=good["workspace"].cpu())):
+        with pytest.raises(ValueError):
+            m.mla_document_attention(**{**good, **over})
+    for over, status in ((dict(workspace=good["workspace"][:256]), -3), (dict(window=-1), -1)):
+        with pytest.raises(m.MlaError) as e:
+            m.mla_document_attention(**{**good, **over})
+        assert e.value.status == status

@@ -590,3 +590,102 @@ def test_forked_sequences_answer_alike(gpu_available):
     for r in range(B):
         last = book.table[[r, r + B], P[r] // page]
         assert last[0] != last[1] and not np.array_equal(k[last[0]], k[last[1]])
+
+
+@gpu
+def test_pages_past_32_bit_offsets(gpu_available):
+    """A cache of more than 2^32 bytes of codes: its last pages forked, copied to each other and moved to the front."""
+    import torch
+    heads, page, n_pages = 64, 128, 4400  # 1 MiB of key codes a page
+    t = m.alloc_paged_cache(n_pages, page, heads)
+    t["table"] = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    t["table"][0, :3] = ints([n_pages - 1, n_pages - 5, n_pages - 2])
+    refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    refs[[n_pages - 1, n_pages - 5, n_pages - 2]] = 1
+    refs[:4390] = 1  # (the user's own holds: the free pages lie behind them)
+    names = [n for n in m.PAGED_TENSORS]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for n in names:
+        x = torch.randint(1, 100, (10, *t[n].shape[1:]), device="cuda", generator=g)
+        t[n][-10:] = x.to(t[n].dtype)
+    was = {n: t[n][-10:].clone() for n in names}
+    cache, pool = m.make_paged_cache(t), m.make_page_pool(t["table"], refs, page)
+    ws = m.alloc_workspace(m.MODE_PAGES, 3, n_pages, cap=3)
+
+    def ok():
+        assert m.mla_device_status(ws) == 0
+
+    m.mla_pages_fork(cache, pool, ints([0]), ints([2]), ints([300]), ws)
+    ok()
+    assert t["table"][2].tolist() == [n_pages - 1, n_pages - 5, 4390, -1]
+    for n in ("k_codes", "v_codes"):
+        assert torch.equal(t[n][4390, :, :44], was[n][8, :, :44]) and torch.equal(t[n][4390, :, 44:], was[n][0, :, 44:])
+    assert torch.equal(t["k_pe"][4390, :44], was["k_pe"][8, :44])
+    m.mla_pages_copy(cache, cache, ints([n_pages - 1, n_pages - 2, 4390]), ints([4391, 4392, 7]), ws)
+    ok()
+    for n in names:
+        assert torch.equal(t[n][4391], was[n][9]) and torch.equal(t[n][4392], was[n][8])
+        assert torch.equal(t[n][7], t[n][4390])
+    tail = {n: t[n][4390].clone() for n in names}
+    refs[5:4390] = 0
+    moved, n_live = torch.empty(n_pages, dtype=torch.int32, device="cuda"), ints([0])
+    m.mla_pages_compact(cache, pool, moved, n_live, ws)
+    ok()
+    # held: 0-4, 4390 (the tail), 4395 (two rows), 4398, 4399 (two rows); they go to 5, 6, 7, 8
+    assert n_live.item() == 9 and t["table"].tolist() == [[8, 6, 7, -1], [-1] * 4, [8, 6, 5, -1]]
+    assert refs.tolist() == [1] * 6 + [2, 1, 2] + [0] * (n_pages - 9)
+    for n in names:
+        for to, x in ((5, tail[n]), (6, was[n][5]), (7, was[n][8]), (8, was[n][9])):
+            assert torch.equal(t[n][to], x), (n, to)
+
+
+@gpu
+def test_more_pages_than_one_block_sums_at_once(gpu_available):
+    """1.1 million pages (only the pool is touched): the sums over the segments go round twice, through the workspace."""
+    import torch
+    n_pages, rows = 1100000, 5
+    table = torch.full((rows, 4000), -1, dtype=torch.int32, device="cuda")
+    refs = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+    free = np.sort(np.random.default_rng(1).permutation(n_pages)[:3000])
+    refs[torch.from_numpy(free).cuda()] = 0
+    pool = m.make_page_pool(table, refs, 16)
+    lists = ints([4, 0, 2]), ints([16 * 900 - 3, 16 * 1300, 1])
+    ws = m.alloc_workspace(m.MODE_PAGES, 3, n_pages, cap=rows).fill_(0xa5)
+    m.mla_pages_reserve(pool, *lists, ws)
+    assert m.mla_device_status(ws) == OK
+    got = table.cpu().numpy()
+    assert np.array_equal(got[4, :900], free[:900]) and np.array_equal(got[0, :1300], free[900:2200])
+    assert got[2, 0] == free[2200] and (got >= 0).sum() == 2201 and int(refs.sum()) == n_pages - 3000 + 2201
+    m.mla_pages_reserve(pool, ints([1, 3]), ints([16 * 800, 1]), m.alloc_workspace(m.MODE_PAGES, 2, n_pages, cap=rows))
+    assert int((table >= 0).sum()) == 2201, "too few: nothing is changed"
+    m.mla_pages_free(pool, *[x[:2] for x in (lists[0], ints([0, 16]))], ws)
+    assert m.mla_device_status(ws) == OK and int(refs.sum()) == n_pages - 3000 + 2
+
+
+@gpu
+def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
+    import torch
+    book = Book(4, 4, 20, 16, 1)
+    dev = Device(book)
+    table, refs = dev.t["table"], dev.refs
+    for over in (dict(table=table.long()), dict(table=table[0]), dict(table=table[:, :2]), dict(refs=refs.float()),
+                 dict(refs=refs.cpu()), dict(refs=refs[::2]), dict(refs=refs[:0])):
+        with pytest.raises(ValueError):
+            m.make_page_pool(**{**dict(table=table, refs=refs, page=16), **over})
+    x, ws = ints([0, 1]), dev.ws(2)
+    calls = [lambda a=x, b=x, w=ws: m.mla_pages_free(dev.pool, a, b, w),
+             lambda a=x, b=x, w=ws: m.mla_pages_reserve(dev.pool, a, b, w),
+             lambda a=x, b=x, w=ws: m.mla_pages_fork(dev.cache, dev.pool, a, b, ints([0, 0]), w),
+             lambda a=x, b=x, w=ws: m.mla_pages_copy(dev.cache, dev.cache, a, b, w)]
+    for f in calls:
+        for over in (dict(a=x.long()), dict(a=x.cpu()), dict(b=x[:1]), dict(b=ints([0, 0, 1, 0])[::2]), dict(b=x.float()),
+                     dict(w=ws.cpu())):
+            with pytest.raises(ValueError):
+                f(**over)
+        with pytest.raises(m.MlaError) as e:
+            f(w=ws[:256])
+        assert e.value.status == -3
+    for over in (dict(moved=ints([0] * 19)), dict(n_live=ints([0, 0])), dict(moved=torch.zeros(20, device="cuda"))):
+        with pytest.raises(ValueError):
+            m.mla_pages_compact(dev.cache, dev.pool, **{**dict(moved=ints([0] * 20), n_live=ints([0]), workspace=ws), **over})
+    dev.same()
