@@ -563,7 +563,7 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
  *            place in the pack or in the document alike)
  *   out      bf16, row n at out + n * out_row: 64 x 128; out_row a multiple of
  *            8, >= 64 * 128.  Rows outside cu_q[0] .. cu_q[n_docs] are left as
- *            they were
+ *            they were.  Must not overlap q, k_cache or v_cache
  *   cu_q, cu_k  int [n_docs + 1] in DEVICE memory, 0 <= cu[0] <= cu[1] <= ..,
  *            cu_q[n_docs] <= N, cu_k[n_docs] <= cap; empty documents are
  *            allowed; cu_k NULL: cu_q
@@ -633,8 +633,8 @@ int mla_prefill_paged(const mla_weights_t* w, const mla_params_t* params, const 
  * Lists are int [n] in DEVICE memory (4-byte aligned), 1 <= n <= 2^20; P[i]
  * counts positions, ceil(P[i] / page) entries of a row hold P[i] of them.
  * Calls on one pool are ordered by their stream; two calls, or a call and one
- * that reads the cache, must not overlap.  One call of the list is one
- * transaction: it sees the pool as it was before the call.
+ * that reads the cache, must not overlap.  All entries of a list see the pool as
+ * it was before the call.
  * An entry that cannot be carried out (a row outside [0, rows), P[i] outside
  * [0, max_pages * page], what the calls name below) is skipped, and
  * mla_device_status then returns MLA_ERR_INVALID_ARG. */

@@ -8,19 +8,25 @@
 //
 // mla_pages_free is one launch: an entry is exchanged for -1 and the page that
 // came out of it loses one hold (a row that is listed twice loses each page
-// once).  The others are two launches:
-//   1. a plan by one cluster of 8 CTAs, which meet at the cluster's barrier
-//      between its steps: the free pages as a bitmap with their number before
-//      each 1,024 pages, what every list entry needs and whether it can be
-//      carried out; then sums over both, by one CTA; then the list of the
-//      pages that the call takes.  (One cluster, because its steps depend on
-//      each other: its barrier takes a fraction of a microsecond, a launch two
-//      to three.)
-//   2. the changes themselves, over the whole GPU.  Nothing is changed before
-//      the plan has found enough free pages, so a call without them changes
-//      nothing.
-// Bounds: free and reserve move a few bytes and take the launches' time; fork,
-// compact and copy move pages, and HBM bounds them from a few hundred pages on.
+// once).  The others begin with a plan by one cluster of 8 CTAs, which meet at the
+// cluster's barrier between its steps: the free pages as a bitmap with their
+// number before each 1,024 pages, what every list entry needs and whether it can
+// be carried out; then sums over both, by one CTA, in its shared memory; then the
+// list of the pages that the call takes.  (One cluster, because its steps depend
+// on each other: its barrier takes a fraction of a microsecond, a launch two to
+// three.  Handing the numbers over through global memory took 1 to 2 us more.)
+// Nothing is changed before the plan has found enough free pages, so a call
+// without them changes nothing.  The changes follow in a second launch over the
+// whole GPU; those of a short reservation end in the plan's own.
+// A copy has no plan but its pairs' claims on their destinations.
+//
+// Bounds and figures: free, reserve and fork move little and take their launches,
+// each 2 to 3 us, and the plan's chain of dependent reads: 64 rows given back and
+// taken again 10.6 us on the GPU, 600 rows of up to 2,048 more tokens 22.0, 1 row
+// forked into 4 and given back 12.0.  compact and copy move pages, and HBM bounds
+// them from a few hundred pages on: 1,531 pages of 32 tokens of 64 heads copied in
+// 258 us (6.28 TB/s, 0.93 of the measured copy rate), the 2,048 of 8,192 pages of
+// 16 tokens that a half-full pool has to move in 186 us (5.8 TB/s).
 #include "common.cuh"
 #include "internal.h"
 
@@ -585,8 +591,7 @@ __device__ __forceinline__ bool carried_out(const PageCopyArgs& a, int i, int s,
   return __ldcg(a.claims + d) == i && (!a.same || s == d || __ldcg(a.claims + s) < 0);
 }
 
-// claim[page] = the last pair that
-// writes the page, -1 for a source that none writes.
+// claim[page] = the last pair that writes the page, -1 for a source that none writes.
 __global__ void __launch_bounds__(kPlanThreads, 1) pages_claim_kernel(const PageCopyArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -638,7 +643,7 @@ cudaError_t launch_pages_free(const PagePool& p, const int* rows, const int* P, 
 cudaError_t launch_pages_reserve(const PagePlanArgs& a, int num_sms, cudaStream_t stream) {
   const cudaError_t e = launch_plan<PageOp::kReserve>(a, stream);
   // (a list of at most one row for each of the plan's warps is done: 64 rows, given back and
-  // taken again, 12.9 us with a second launch, 10.8 without; 600 rows 27.0 without, 21 with)
+  // taken again, 12.9 us with a second launch, 10.6 without; 600 rows 27.0 without, 22.0 with)
   if (e != cudaSuccess || a.n <= kPlanCtas * (kPlanThreads / 32)) return e;
   const int grid = a.n < 4 * num_sms ? a.n : 4 * num_sms;
   return launch_pdl(pages_reserve_kernel, dim3(grid), dim3(256), 0, stream, a);
