@@ -576,7 +576,7 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
  * Offsets out of range or order cannot be checked on the host: the kernel then
  * writes nothing and mla_device_status returns MLA_ERR_INVALID_ARG.
  * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
- * Keys behind the last one that a query of its tile of 128 sees are not used,
+ * Keys behind the last one that a query of its tile of up to 256 sees are not used,
  * whatever the caches hold; a NaN among the values of another key may also
  * reach queries of its document that do not see the key, but no other document.
  * Errors: INVALID_ARG (null pointer, N, cap < 1 or > 2^24, n_docs < 1 or > 2^20,

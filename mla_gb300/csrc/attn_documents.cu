@@ -20,8 +20,8 @@
 //   warp 0   work scheduler (counter -> a 4-slot ring of items), then TMA: K
 //            tiles, 64 dimensions at a time, into a ring of 7 such thirds (TMA
 //            takes 1,900 cycles under load: with a ring of two whole tiles, each
-//            slot idle for that long, a tile took 1,400 cycles, so 1,240), and
-//            the next item's Q tile
+//            slot idle for that long, a tile took 160 cycles more), and the next
+//            item's Q tile
 //   warp 1   TMEM allocation; an item's Q into tensor memory (tcgen05.cp), then
 //            S_x = Q K_x^T (M=128 N=96 K=192) into score buffer x & 1, x
 //            counting this CTA's key tiles
@@ -44,14 +44,25 @@
 // What bounds it: the SM's shared memory.  A key tile is 60 KB, written once by
 // TMA and read once by the products, 960 cycles at 128 bytes a clock, which is
 // also what its products take (960 at 4,096 MAC a clock); an item adds Q and O,
-// 160 KB, 1,250 cycles.  Long documents take 1,060 cycles a tile.  With the K and V
+// 160 KB.  Measured about 1,200 cycles a tile and 1,100 an item.  With the K and V
 // copies left out (wrong results) 16 documents of up to 1,531 tokens took 185 us
-// where they take 241, 5 of up to 4,096 tokens 523 where they take 720 (0.7 of the
-// products' burst rate, 0.76 with the masked halves of diagonal tiles that run).
+// where they take 241, 5 of up to 4,096 tokens 523 where they took 720.
+//
+// Pairs of CTAs (PAIR): for long documents a cluster of two takes two query tiles of a
+// document with one product of 256 rows (cta_group::2), of whose keys and values each
+// CTA holds half, so that a key tile costs an SM 30 KB in and 30 KB out: 5 documents
+// of up to 4,096 tokens take 700 us on the GPU instead of 731, 4 of 4,096 tokens 883
+// instead of 956, one of 16,384 tokens 2,890 instead of 3,043 (1.0 of the products'
+// burst rate).  The even CTA schedules and issues; each CTA loads its half and
+// does the softmax of its own 128 rows.  What it costs: the first tile's products
+// over the keys that only the second sees, and a tile of nothing behind an odd
+// number of them, 4% more tiles in the first case, 22% for 16 documents of up to
+// 1,531 tokens (262 us instead of 245).
 // Measured on the way, GPU time: the windowed prefill's two threads a row on the same
 // tile 309 and 820 us; this form 248 and 745 with lane-0 loops and Q through
-// registers.  Two CTAs sharing K/V tiles by multicast 263 and 749 (the copies'
-// writes stay); warps of their own for the output 260 and 771.
+// registers.  Two CTAs sharing K/V tiles by multicast, with products of their own, 263
+// and 749 (the copies' writes stay); warps of their own for the output 260 and 771;
+// pairs with a third of a K tile a copy 295 and 703.
 //
 // Code size: the roles' loops share one instruction cache.  At 81 KB of code (every
 // wait inlined with its clock) 5.4 of the stalls per instruction were for
@@ -72,10 +83,18 @@ constexpr uint32_t kQOff = 0;                    // Q: 3 atoms (staging)
 constexpr uint32_t kOOff = 3 * kAtom;            // O: 2 atoms (staging)
 constexpr int kHalf = kKeys / 2;
 constexpr uint32_t kHalfAtom = kHalf * 128;      // 48 rows x 64 bf16
-constexpr int kKSlots = 7, kVSlots = 5;          // of a third of a K tile (64 dimensions), of half a V tile (48 keys)
-constexpr uint32_t kKOff = 5 * kAtom;            // slots of a key atom
-constexpr uint32_t kVOff = kKOff + kKSlots * kKeyAtom;  // slots of 2 half atoms (vdim 0-63, 64-127)
-constexpr uint32_t kBarOff = kVOff + kVSlots * 2 * kHalfAtom;
+constexpr uint32_t kKOff = 5 * kAtom;            // K slots, then V slots
+// The rings' slots: a third of a K tile (64 dimensions) and half a V tile (48 keys).  In a
+// pair of CTAs: a whole tile, of which each CTA holds half, 48 keys of K and 64 dimensions of V.
+template <bool PAIR>
+struct Rings {
+  static constexpr int kKSlots = PAIR ? 4 : 7, kVSlots = PAIR ? 6 : 5;
+  static constexpr int kKTiles = PAIR ? kKSlots : 3;  // in flight at most
+  static constexpr uint32_t kKSlotBytes = PAIR ? 3 * kHalfAtom : kKeyAtom, kVSlotBytes = PAIR ? kKeyAtom : 2 * kHalfAtom;
+  static constexpr uint32_t kVOff = kKOff + kKSlots * kKSlotBytes, kEnd = kVOff + kVSlots * kVSlotBytes;
+};
+constexpr uint32_t kBarOff = Rings<false>::kEnd;
+static_assert(Rings<true>::kEnd <= kBarOff, "rings");
 constexpr uint32_t kRefOff = kBarOff + 768;      // references by tile parity, 2 x 128 fp32
 constexpr uint32_t kSumOff = kRefOff + 1024;     // sums and references handed over, 128 x 2 fp32
 constexpr uint32_t kTileOff = kSumOff + 1024;    // the query tiles of the item ring
@@ -89,14 +108,23 @@ constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on a
                                                  // new token 15.9 us where they take 14.7, 8 with a prefix 155 where 150)
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 constexpr int kItemRing = 4;
+// Pairs from this many rows of q a document on (8 documents of random lengths around a mean,
+// in us: 1,024 tokens 196 as single tiles, 207 in pairs; 1,280: 308, 311; 1,536: 422, 413;
+// 2,048: 730, 711; 6,000: 4,258, 4,030; a document's own length matters more near there,
+// 1,400 tokens are 11 tiles or 12 in pairs, 290 and 311), and under a window of this many
+// keys on (the pair's keys are its window's and 256, a tile's 128: 5 documents of 4,000
+// tokens under 512 keys 404, 433; 1,024: 602, 614; 1,536: 779, 782; 2,048: 918, 880).
+constexpr int kPairRows = 1536;
 
 // A warp's bounded wait, in few instructions: 2^21 tries (tens of milliseconds at
 // least; a wait is for a few tiles' work, microseconds).  A role whose wait gives
 // up stops, and says so at its end.
+// CLUSTER: for what the other CTA of a pair wrote to shared memory.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   int tries = 1 << 21;
 #pragma unroll 1
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+  while (!__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
     if (--tries == 0) return false;
   return true;
 }
@@ -113,10 +141,12 @@ struct Place {
   }
 };
 
+template <bool PAIR>
 struct Bars {
+  static constexpr int kKTiles = Rings<PAIR>::kKTiles, kKSlots = Rings<PAIR>::kKSlots, kVSlots = Rings<PAIR>::kVSlots;
   uint64_t q_full, q_empty, q_free;
   uint64_t item_full[kItemRing], item_empty[kItemRing];
-  uint64_t k_full[3], k_empty[kKSlots];  // full: a whole tile, of those in flight; empty: a slot
+  uint64_t k_full[kKTiles], k_empty[kKSlots];  // full: a whole tile, of those in flight; empty: a slot
   uint64_t v_full[kVSlots], v_empty[kVSlots], v_cut[kVSlots];  // full and cut: a whole tile, by its first half's slot
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2], pv_done[2];
@@ -127,7 +157,58 @@ struct Bars {
   uint32_t tmem_slot;
   int abort;  // the role whose wait gave up
 };
-static_assert(sizeof(Bars) <= 768, "barrier block");
+static_assert(sizeof(Bars<false>) <= 768 && sizeof(Bars<true>) <= 768, "barrier block");
+
+// What differs in a pair of CTAs (cta_group::2): the even one issues the products of
+// both, so that a role's signal goes to it, and a product's completion to both, or to it.
+// A signal that hands over tensor memory has the tcgen05 fences for its order and is a
+// plain arrival; one that hands over shared memory is released to the cluster.  (With
+// such releases for all, two a tile and warp, the softmax groups took twice as long a
+// tile: 5 documents of up to 4,096 tokens 1,138 us where they take 700.)
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  if (PAIR)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_rank(smem_u32(bar), 0)) : "memory");
+  else
+    mbar_arrive(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void release_leader(uint64_t* bar) {
+  if (PAIR)
+    mbar_arrive_cluster(mapa_rank(smem_u32(bar), 0));
+  else
+    mbar_arrive(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  if (PAIR)
+    umma_commit_pair(bar, 3);
+  else
+    umma_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit_leader(uint64_t* bar) {
+  if (PAIR)
+    umma_commit_pair(bar, 1);
+  else
+    umma_commit(bar);
+}
+// A box of rows and 64-number atoms, counted on the even CTA's barrier.
+template <bool PAIR>
+__device__ __forceinline__ void load_leader(void* dst, const CUtensorMap* map, uint64_t* bar, int row, int atom,
+                                            int outer) {
+  if (PAIR)
+    tma_load_4d_pair(dst, map, mapa_rank(smem_u32(bar), 0), 0, row, atom, outer);
+  else
+    tma_load_4d(dst, map, bar, 0, row, atom, outer);
+}
+template <bool PAIR>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (PAIR)
+    umma_bf16_ts_pair(d, a, b, idesc, accumulate);
+  else
+    umma_bf16_ts(d, a, b, idesc, accumulate);
+}
 
 // A document's query tile, as the plan lists it: its rows q_row .. q_row + rows
 // - 1 sit at positions pos .. (below 0: before the document's first key), its
@@ -183,13 +264,25 @@ __device__ __forceinline__ bool elected() {
 }
 
 // A warp reads item `it` from the ring, then releases the slot.  False: a wait gave up.
-__device__ __forceinline__ bool read_item(uint8_t* smem, Bars* bar, int it, DocTile& tile) {
+template <bool PAIR>
+__device__ __forceinline__ bool read_item(uint8_t* smem, Bars<PAIR>* bar, int it, DocTile& tile) {
   const int slot = it % kItemRing;
-  if (!wait_for(&bar->item_full[slot], (it / kItemRing) & 1)) return false;
+  if (!wait_for<PAIR>(&bar->item_full[slot], (it / kItemRing) & 1)) return false;
   tile = reinterpret_cast<const DocTile*>(smem + kTileOff)[slot];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bar->item_empty[slot]);
   return true;
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, int x) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void copy_q(uint32_t taddr, uint64_t desc) {
+  if (PAIR)
+    tmem_copy_128x256b_pair(taddr, desc);
+  else
+    tmem_copy_128x256b(taddr, desc);
 }
 
 // the lowest n bits of 32 (none for n < 0, all for n > 32)
@@ -199,15 +292,20 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
   return m;
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     document_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, float sl2, int window,
                      int sinks, int* __restrict__ work, const uint8_t* __restrict__ plan, __nv_bfloat16* __restrict__ o,
                      long long o_row, const DevStatus st) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  Bars* bar = reinterpret_cast<Bars*>(smem + kBarOff);
+  using R = Rings<PAIR>;
+  constexpr int kKSlots = R::kKSlots, kVSlots = R::kVSlots, kKTiles = R::kKTiles;
+  Bars<PAIR>* bar = reinterpret_cast<Bars<PAIR>*>(smem + kBarOff);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // (uniform to the compiler)
   const int lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
@@ -215,23 +313,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar->q_free, 1);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&bar->item_full[i], 1);
-      mbar_init(&bar->item_empty[i], 3 + 8);  // V producer, S issuer, P.V issuer, softmax warps
+      // V producer, S issuer, P.V issuer, softmax warps; in a pair the odd CTA's scheduler for its
+      // own V producer and softmax warps
+      mbar_init(&bar->item_empty[i], leader ? 11 + PAIR : 9);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar->p_full[i], 128);
+      mbar_init(&bar->p_full[i], PAIR ? 8 : 4);  // the group's warps, of both CTAs
       mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->s_free[i], 128);
+      mbar_init(&bar->s_free[i], PAIR ? 8 : 4);
       mbar_init(&bar->pv_done[i], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&bar->ref[i][q], 32);
     }
 #pragma unroll 1
     for (int i = 0; i < kKSlots; ++i) mbar_init(&bar->k_empty[i], 1);
-    for (int i = 0; i < 3; ++i) mbar_init(&bar->k_full[i], 1);
+    for (int i = 0; i < kKTiles; ++i) mbar_init(&bar->k_full[i], 1);
 #pragma unroll 1
     for (int i = 0; i < kVSlots; ++i) {
       mbar_init(&bar->v_full[i], 1);
       mbar_init(&bar->v_empty[i], 1);
-      mbar_init(&bar->v_cut[i], 1);
+      mbar_init(&bar->v_cut[i], PAIR ? 2 : 1);
     }
     for (int q = 0; q < 4; ++q) {
       mbar_init(&bar->sum[q], 32);
@@ -244,11 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&bar->tmem_slot, 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&bar->tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&bar->tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // both CTAs' barriers exist before any signal from the other
   tc_fence_after();
   const uint32_t tmem = bar->tmem_slot;
   pdl_launch_dependents();
@@ -266,26 +372,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int* tiles = reinterpret_cast<const int*>(plan + sizeof(DocPlan)) + min(lane, (int)sizeof(DocTile) / 4 - 1);
     DocTile* const ring = reinterpret_cast<DocTile*>(smem + kTileOff);
     Place<kKSlots> k;
-    Place<3> full;
+    Place<kKTiles> full;
     int q_loads = 0;
     // Item it + 1 is posted to the ring, where every role finds it, before item `it` is
     // loaded; its tile was fetched (a word a lane) after the item before, its index asked
     // for before that.
-    int index = lane == 0 ? atomicAdd(work, 1) : 0, word = 0;
+    int index = leader && lane == 0 ? atomicAdd(work, 1) : 0, word = 0;
 #pragma unroll 1
     for (int it = -2;; ++it) {
       const DocTile& tile = ring[(it + kItemRing) % kItemRing];
       DocTile& next = ring[(it + 1 + kItemRing) % kItemRing];
       if (it >= -1) {
         const int slot = (it + 1) % kItemRing;
-        if (it + 1 >= kItemRing && !(ok = wait_for(&bar->item_empty[slot], ((it + 1) / kItemRing - 1) & 1))) break;
-        if (lane < (int)sizeof(DocTile) / 4) reinterpret_cast<int*>(&next)[lane] = word;
-        __syncwarp();
-        if (elected()) mbar_arrive(&bar->item_full[slot]);  // release
-        __syncwarp();
+        if (leader) {
+          if (it + 1 >= kItemRing && !(ok = wait_for(&bar->item_empty[slot], ((it + 1) / kItemRing - 1) & 1))) break;
+          if (lane < (int)sizeof(DocTile) / 4) {
+            int* const at = reinterpret_cast<int*>(&next) + lane;
+            *at = word;
+            if (PAIR) st_cluster(mapa_rank(smem_u32(at), 1), word);
+          }
+          __syncwarp();
+          if (elected()) {  // release
+            mbar_arrive(&bar->item_full[slot]);
+            if (PAIR) mbar_arrive_cluster(mapa_rank(smem_u32(&bar->item_full[slot]), 1));
+          }
+          __syncwarp();
+        } else if (!(ok = wait_for<PAIR>(&bar->item_full[slot], ((it + 1) / kItemRing) & 1))) {
+          break;
+        }
       }
       if (it >= 0 && tile.rows == 0) break;
-      const int after = lane == 0 ? atomicAdd(work, 1) : 0;
+      const int after = leader && lane == 0 ? atomicAdd(work, 1) : 0;
       // K tiles, 64 dimensions at a time; behind the second one (at once, for the first item)
       // the next item's Q, into the staging atoms once this one's has been copied into tensor
       // memory: by then it has, and the copy has the rest of the item to arrive
@@ -295,27 +412,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == q_at && it >= -1 && next.rows > 0) {
           if (it >= 0 && !(ok = wait_for(&bar->q_empty, it & 1))) break;
           if (elected()) {
-            mbar_arrive_expect_tx(&bar->q_full, 3 * kAtom);
-            for (int c = 0; c < 3; ++c)
-              tma_load_3d(smem + kQOff + c * kAtom, &tmQ, &bar->q_full, next.head * 192 + 64 * c, next.q_row, 0);
+            if (leader) mbar_arrive_expect_tx(&bar->q_full, (PAIR ? 6 : 3) * kAtom);
+            load_leader<PAIR>(smem + kQOff, &tmQ, &bar->q_full, next.q_row + rank * 128, next.head * 3, 0);
           }
           __syncwarp();
           ++q_loads;
         }
         if (j == n_kv) break;
         const int key = tile.k_row + tile.key0(j);
-#pragma unroll 1
-        for (int c = 0; c < 192; c += 64, k.next()) {
+        if (PAIR) {
           if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
           if (elected()) {
-            if (c == 0) mbar_arrive_expect_tx(&bar->k_full[full.slot], 3 * kKeyAtom);
-            tma_load_3d(smem + kKOff + k.slot * kKeyAtom, &tmK, &bar->k_full[full.slot], c, key, tile.head);
+            if (leader) mbar_arrive_expect_tx(&bar->k_full[k.slot], 3 * kKeyAtom);
+            load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[k.slot], key + rank * kHalf, 0,
+                              tile.head);
           }
           __syncwarp();
+          k.next();
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 3; ++c, k.next()) {
+            if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
+            if (elected()) {
+              if (c == 0) mbar_arrive_expect_tx(&bar->k_full[full.slot], 3 * kKeyAtom);
+              load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[full.slot], key, c, tile.head);
+            }
+            __syncwarp();
+          }
         }
         full.next();
       }
       if (!ok) break;
+      if (!leader) {
+        __syncwarp();
+        if (it >= 2) {  // (two items back: they have been read by now)
+          if (!(ok = wait_for(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1))) break;
+          if (elected()) release_leader<PAIR>(&bar->item_empty[(it - 2) % kItemRing]);
+        }
+        __syncwarp();
+        continue;
+      }
       index = __shfl_sync(0xffffffffu, index, 0);
       word = 0;  // (no rows: the end)
       if (index < n_items) {
@@ -328,62 +464,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // no copy may still be in flight into shared memory (a tile that was left half issued
     // never arrives: its wait gives up)
-    if (q_loads) ok &= wait_for(&bar->q_full, (q_loads - 1) & 1);
+    if (leader && q_loads) ok &= wait_for(&bar->q_full, (q_loads - 1) & 1);
 #pragma unroll 1
-    for (int i = 0; i < 3; ++i, full.next()) ok &= wait_for(&bar->k_full[full.slot], full.phase ^ 1);
+    for (int i = 0; leader && i < kKTiles; ++i, full.next()) ok &= wait_for(&bar->k_full[full.slot], full.phase ^ 1);
   } else if (warp == 1) {
-    // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
-    constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
-    const uint32_t k_addr = smem_u32(smem + kKOff);
-    int x = 0;
-    Place<kKSlots> k;
-    Place<3> full;
+    if (leader) {
+      // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
+      constexpr uint32_t idesc_s = idesc_bf16(PAIR ? 256 : 128, kKeys, false, false);
+      const uint32_t k_addr = smem_u32(smem + kKOff);
+      int x = 0;
+      Place<kKSlots> k;
+      Place<kKTiles> full;
 #pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      DocTile tile;
-      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
-      // the item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory as bf16
-      // pairs, the A operand of every S, once the S of the item before are done
-      if (!(ok = wait_for(&bar->q_full, it & 1) && (it == 0 || wait_for(&bar->q_free, (it - 1) & 1)))) break;
-      tc_fence_after();
-      if (elected()) {
-#pragma unroll
-        for (int kk = 0; kk < 12; ++kk)
-          tmem_copy_128x256b(tmem + kTmQ + kk * 8,
-                             sdesc_sw128(smem_u32(smem + kQOff) + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024));
-        umma_commit(&bar->q_empty);  // the staging atoms may take the Q after it
-      }
-      __syncwarp();
-#pragma unroll 1
-      for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
-        const int sb = x & 1;
-        // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
-        if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
-                   (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
-          break;
-        full.next();
+      for (int it = 0; ok; ++it) {
+        DocTile tile;
+        if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
+        // the item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory as bf16
+        // pairs, the A operand of every S, once the S of the item before are done
+        if (!(ok = wait_for(&bar->q_full, it & 1) && (it == 0 || wait_for(&bar->q_free, (it - 1) & 1)))) break;
         tc_fence_after();
+        if (elected()) {
 #pragma unroll
-        for (int c = 0; c < 3; ++c, k.next()) {
-          const uint64_t kb = sdesc_sw128(k_addr + k.slot * kKeyAtom, 16, 1024);
-          if (elected()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_ts(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc_s,
-                           c > 0 || kk > 0 ? 1u : 0u);
-            umma_commit(&bar->k_empty[k.slot]);
-            if (c == 2) umma_commit(&bar->s_full[sb]);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 12; ++kk)
+            copy_q<PAIR>(tmem + kTmQ + kk * 8,
+                         sdesc_sw128(smem_u32(smem + kQOff) + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024));
+          commit_both<PAIR>(&bar->q_empty);  // the staging atoms may take the Q after it
         }
+        __syncwarp();
+#pragma unroll 1
+        for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
+          const int sb = x & 1;
+          // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
+          if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
+                     (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
+            break;
+          full.next();
+          tc_fence_after();
+          if (PAIR) {
+            const uint64_t kb = sdesc_sw128(k_addr + k.slot * R::kKSlotBytes, 16, 1024);
+            if (elected()) {
+#pragma unroll
+              for (int kk = 0; kk < 12; ++kk)
+                product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + kk * 8,
+                              kb + (kk >> 2) * (kHalfAtom >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
+              commit_both<PAIR>(&bar->k_empty[k.slot]);
+              commit_both<PAIR>(&bar->s_full[sb]);
+            }
+            __syncwarp();
+            k.next();
+          } else {
+#pragma unroll
+            for (int c = 0; c < 3; ++c, k.next()) {
+              const uint64_t kb = sdesc_sw128(k_addr + k.slot * R::kKSlotBytes, 16, 1024);
+              if (elected()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc_s,
+                                c > 0 || kk > 0 ? 1u : 0u);
+                commit_both<PAIR>(&bar->k_empty[k.slot]);
+                if (c == 2) commit_both<PAIR>(&bar->s_full[sb]);
+              }
+              __syncwarp();
+            }
+          }
+        }
+        if (!ok) break;
+        if (elected()) commit_leader<PAIR>(&bar->q_free);  // the item's S are done: its Q may be replaced
+        __syncwarp();
       }
-      if (!ok) break;
-      if (elected()) umma_commit(&bar->q_free);  // the item's S are done: its Q may be replaced
+      if (elected()) commit_leader<PAIR>(&bar->drain_s);
       __syncwarp();
+      ok &= wait_for(&bar->drain_s, 0);
     }
-    if (elected()) umma_commit(&bar->drain_s);
-    __syncwarp();
-    ok &= wait_for(&bar->drain_s, 0);
   } else if (warp == 2) {
     // ---- V producer: half tiles, and clears what lies behind the last key ----
     Place<kVSlots> v;
@@ -392,89 +544,98 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int it = 0; ok; ++it) {
       DocTile tile;
-      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+      if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
 #pragma unroll 1
       for (int j = 0; ok && j < tile.n_kv; ++j) {
-        // a second half that no query sees is left out
-        const int keys = tile.keys(j), halves = keys > kHalf ? 2 : 1, first = v.slot;
+        // (a second half that no query sees is left out)
+        const int keys = tile.keys(j), halves = PAIR || keys <= kHalf ? 1 : 2, first = v.slot;
         const int key = tile.k_row + tile.key0(j);
+        const bool cut = keys == 0 || (keys & 15);
 #pragma unroll 1
         for (int h = 0; h < halves; ++h, v.next()) {
           if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
           if (elected()) {
-            if (h == 0) mbar_arrive_expect_tx(&bar->v_full[first], halves * 2 * kHalfAtom);
-            uint8_t* const at = smem + kVOff + v.slot * 2 * kHalfAtom;
-            tma_load_3d(at, &tmV, &bar->v_full[first], 0, key + h * kHalf, tile.head);
-            tma_load_3d(at + kHalfAtom, &tmV, &bar->v_full[first], 64, key + h * kHalf, tile.head);
+            uint8_t* const at = smem + R::kVOff + v.slot * R::kVSlotBytes;
+            // (in a pair, a tile that is to be cut arrives on each CTA's own barrier)
+            if (h == 0 && (cut || leader))
+              mbar_arrive_expect_tx(&bar->v_full[first], PAIR ? (cut ? 1 : 2) * kKeyAtom : halves * R::kVSlotBytes);
+            if (PAIR && cut)
+              tma_load_4d(at, &tmV, &bar->v_full[first], 0, key, rank, tile.head);
+            else
+              load_leader<PAIR>(at, &tmV, &bar->v_full[first], key + h * kHalf, rank, tile.head);
           }
           __syncwarp();
         }
-        if (ok && (keys == 0 || (keys & 15))) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
+        if (ok && cut) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
           if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
           const int last = halves == 1 ? first : (first + 1) % kVSlots, from = keys - (halves - 1) * kHalf;
-          uint8_t* const mine = smem + kVOff + (last * 2 + ((lane >> 3) & 1)) * kHalfAtom + (lane & 7) * 16;
+          uint8_t* const mine =
+              smem + R::kVOff + last * R::kVSlotBytes + (PAIR ? 0 : ((lane >> 3) & 1) * kHalfAtom) + (lane & 7) * 16;
 #pragma unroll 1
-          for (int r = from + (lane >> 4); r < max(16, (from + 15) & ~15); r += 2)
+          for (int r = from + (PAIR ? lane >> 3 : lane >> 4); r < max(16, (from + 15) & ~15); r += PAIR ? 4 : 2)
             *reinterpret_cast<uint4*>(mine + r * 128) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
-          if (elected()) mbar_arrive(&bar->v_cut[first]);
+          if (elected()) release_leader<PAIR>(&bar->v_cut[first]);
           __syncwarp();
         }
-        phases ^= 1u << first;
+        if (leader || cut) phases ^= 1u << first;
       }
     }
     // (every tile has arrived: its slot's barrier has left the phase before its next one)
 #pragma unroll 1
     for (int i = 0; i < kVSlots; ++i) ok &= wait_for(&bar->v_full[i], ((phases >> i) & 1) ^ 1);
   } else if (warp == 3) {
-    // ---- P.V issuer: O += P_x V_x ----
-    constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
-    const uint32_t v_addr = smem_u32(smem + kVOff);
-    int x = 0;
-    Place<kVSlots> v;
-    uint32_t phases = 0, cuts = 0;  // of each slot's full and cut barriers
+    if (leader) {
+      // ---- P.V issuer: O += P_x V_x ----
+      constexpr uint32_t idesc_pv = idesc_bf16(PAIR ? 256 : 128, 128, false, true);
+      const uint32_t v_addr = smem_u32(smem + R::kVOff);
+      int x = 0;
+      Place<kVSlots> v;
+      uint32_t phases = 0, cuts = 0;  // of each slot's full and cut barriers
 #pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      DocTile tile;
-      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+      for (int it = 0; ok; ++it) {
+        DocTile tile;
+        if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
 #pragma unroll 1
-      for (int j = 0; j < tile.n_kv; ++j, ++x) {
-        const int sb = x & 1, first = v.slot;
-        // the 16-key steps that hold a key (one where there is none: O becomes zeros), the
-        // last one's other rows cleared
-        const int keys = tile.keys(j), steps = max(1, (keys + 15) >> 4);
-        if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
-        phases ^= 1u << first;
-        if (keys == 0 || (keys & 15)) {
-          if (!(ok = wait_for(&bar->v_cut[first], (cuts >> first) & 1))) break;
-          cuts ^= 1u << first;
-        }
-        // P_x is written (and, for an item's first tile, the previous item's O read)
-        if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h && keys <= kHalf) break;
-          const uint64_t vb = sdesc_sw128(v_addr + v.slot * 2 * kHalfAtom, kHalfAtom, 1024);
-          if (elected()) {
-#pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)
-              if (h * (kHalf / 16) + kk < steps)
-                umma_bf16_ts(tmem + kTmO, tmem + kTmP + sb * kHalf + h * (kHalf / 2) + kk * 8, vb + kk * 128, idesc_pv,
-                             (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bar->v_empty[v.slot]);
+        for (int j = 0; j < tile.n_kv; ++j, ++x) {
+          const int sb = x & 1, first = v.slot;
+          // the 16-key steps that hold a key (one where there is none: O becomes zeros), the
+          // last one's other rows cleared
+          const int keys = tile.keys(j), steps = max(1, (keys + 15) >> 4);
+          if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+          phases ^= 1u << first;
+          if (keys == 0 || (keys & 15)) {
+            if (!(ok = wait_for<PAIR>(&bar->v_cut[first], (cuts >> first) & 1))) break;
+            cuts ^= 1u << first;
           }
+          // P_x is written (and, for an item's first tile, the previous item's O read)
+          if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
+          tc_fence_after();
+          constexpr int kSlotsOfTile = PAIR ? 1 : 2, kSteps = kKeys / 16 / kSlotsOfTile;
+#pragma unroll
+          for (int h = 0; h < kSlotsOfTile; ++h) {
+            if (h && keys <= kHalf) break;
+            const uint64_t vb = sdesc_sw128(v_addr + v.slot * R::kVSlotBytes, kHalfAtom, 1024);
+            if (elected()) {
+#pragma unroll
+              for (int kk = 0; kk < kSteps; ++kk)
+                if (h * kSteps + kk < steps)
+                  product<PAIR>(tmem + kTmO, tmem + kTmP + sb * kHalf + (h * kSteps + kk) * 8, vb + kk * 128, idesc_pv,
+                                (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+              commit_both<PAIR>(&bar->v_empty[v.slot]);
+            }
+            __syncwarp();
+            v.next();
+          }
+          if (elected()) commit_both<PAIR>(&bar->pv_done[sb]);
           __syncwarp();
-          v.next();
         }
-        if (elected()) umma_commit(&bar->pv_done[sb]);
-        __syncwarp();
       }
+      if (elected()) commit_leader<PAIR>(&bar->drain_pv);
+      __syncwarp();
+      ok &= wait_for(&bar->drain_pv, 0);
     }
-    if (elected()) umma_commit(&bar->drain_pv);
-    __syncwarp();
-    ok &= wait_for(&bar->drain_pv, 0);
   } else {
     // ---- softmax groups, one thread a query row ----
     const int g = (warp >> 2) - 1;
@@ -484,6 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* const refs = reinterpret_cast<float*>(smem + kRefOff) + row;    // + 128 x parity of the tile
     float2* const sums = reinterpret_cast<float2*>(smem + kSumOff) + row;
     auto wait = [&](uint64_t& b, int phase) { return wait_for(&b, phase & 1); };
+    auto rows_done = [&](uint64_t& b) {
+      __syncwarp();
+      if (lane == 0) arrive_leader<PAIR>(&b);
+    };
     // Item by item, this group's tiles of each.  At an item's end the group with the
     // last tile `ends` it: it writes O / l.  The other group goes on to the next item's
     // first tile, which is its own.
@@ -492,7 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int it = 0;; ++it) {
       DocTile tile;
-      if (!(ok = read_item(smem, bar, it, tile)) || tile.rows == 0) break;
+      if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
+      if (PAIR) {  // this CTA's tile of the two (the odd one may have no rows)
+        tile.q_row += rank * 128;
+        tile.pos += rank * 128;
+        tile.rows -= rank * 128;
+      }
       const int last = x0 + tile.n_kv - 1;
       const bool ends = (last & 1) == g;
       float m = -INFINITY, l = 0.f;  // this group's sum, relative to 2^m
@@ -512,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tmem + lanes + kTmS + g * kKeys + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
           tmem_wait_ld();
           tc_fence_before();
-          mbar_arrive(&bar->s_free[g]);  // the score buffer may take S_{x+2}
+          rows_done(bar->s_free[g]);  // the score buffer may take S_{x+2}
           // where some row of the warp sees a part of the tile: the keys that this thread's
           // row sees, lo .. hi - 1 of the window and 0 .. near - 1 however far back, as bits
           const int k0 = tile.key0(j), first = tile.pos + quarter * 32;
@@ -595,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar->p_full[g]);
+        rows_done(bar->p_full[g]);
       }
       if (!ok) break;
       if (!ends) {
@@ -657,9 +827,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && bar->abort) report_timeout(st, bar->abort);
+  __syncwarp();
+  if (PAIR) cluster_sync();  // (the other CTA's products, copies and signals are done)
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
@@ -716,7 +891,7 @@ static_assert(kPlanThreads == 32 * 32, "a lane for each warp");
 // order among equals is any: an item's result does not depend on it).  An
 // offset that is out of order or out of range leaves the plan empty.
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    doc_plan_kernel(const DocAttnArgs a, int window, int sinks, int grid, int* work, uint32_t* status) {
+    doc_plan_kernel(const DocAttnArgs a, int tile_rows, int window, int sinks, int workers, int* work, uint32_t* status) {
   __shared__ Doc doc_smem[kDocsInSmem];
   __shared__ int first_smem[kDocsInSmem];
   __shared__ int bucket[kBuckets];
@@ -741,7 +916,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (d < a.n_docs) {
       const Doc doc(a, d);
       bad |= doc.bad(a);
-      mine = bad ? 0 : (doc.n + 127) / 128;
+      mine = bad ? 0 : (doc.n + tile_rows - 1) / tile_rows;
       if (in_smem) doc_smem[d] = doc;
     }
     const int before = block_before(mine, total, sh);
@@ -778,10 +953,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       d = doc_smem[lo];
     else
       d = Doc(a, lo);
-    const int at = (t - first[lo]) * 128;
+    const int at = (t - first[lo]) * tile_rows;
     DocTile tile{};
     tile.q_row = d.q0 + at;
-    tile.rows = min(128, d.n - at);
+    tile.rows = min(tile_rows, d.n - at);
     tile.k_row = d.k0;
     tile.pos = d.keys - d.n + at;
     tile.prefix = d.prefix;
@@ -822,7 +997,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     // Heads a group, a power of two: the smallest whose work is at least 1.5 times the CTA
     // count times the heaviest item (the heavy tiles of the last group then start early
     // enough), halved while its heads' K/V exceed kGroupBytes of L2
-    const unsigned long long need = (3ull * grid * heaviest + 2 * key_tiles - 1) / (2 * key_tiles);
+    const unsigned long long need = (3ull * workers * heaviest + 2 * key_tiles - 1) / (2 * key_tiles);
     const int* ck = a.cu_k ? a.cu_k : a.cu_q;
     const long long kv_head_bytes = ((long long)ck[a.n_docs] - ck[0]) * (192 + 128) * 2;
     int log = 0;
@@ -832,30 +1007,41 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     head->group_log = log;
   }
 }
-}  // namespace
 
-cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream) {
+template <bool PAIR>
+cudaError_t launch_tiles(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, to;
-  if (!make_tmap_bf16_3d(&tq, a.q, 12288, a.N, 1, (uint64_t)a.q_row * 2, (uint64_t)a.q_row * 2, 64, 128) ||
-      !make_tmap_bf16_3d(&tk, a.k, 192, a.cap, 64, 384, (uint64_t)a.cap * 384, 64, kKeys) ||
-      !make_tmap_bf16_3d(&tv, a.v, 128, a.cap, 64, 256, (uint64_t)a.cap * 256, 64, kHalf) ||
+  if (!make_tmap_bf16_atoms(&tq, a.q, a.N, 192, 1, (uint64_t)a.q_row * 2, (uint64_t)a.q_row * 2, 128, 3) ||
+      !make_tmap_bf16_atoms(&tk, a.k, a.cap, 3, 64, 384, (uint64_t)a.cap * 384, PAIR ? kHalf : kKeys, PAIR ? 3 : 1) ||
+      !make_tmap_bf16_atoms(&tv, a.v, a.cap, 2, 64, 256, (uint64_t)a.cap * 256, PAIR ? kKeys : kHalf, PAIR ? 1 : 2) ||
       !make_tmap_store_bf16_3d(&to, a.o, 8192, a.N, 1, (uint64_t)a.o_row * 2, (uint64_t)a.o_row * 2))
     return cudaErrorInvalidValue;
   static PerDevice<bool> allowed;
-  const cudaError_t attr_err = allow_smem(allowed, document_attn_tc, kSmemBytes);
+  const cudaError_t attr_err = allow_smem(allowed, document_attn_tc<PAIR>, kSmemBytes);
   if (attr_err != cudaSuccess) return attr_err;
   // no window: one that reaches behind every key (positions minus it stay in range)
   const int window = a.window > 0 && a.window < kNoWindow ? a.window : kNoWindow;
   const int sinks = a.window > 0 ? a.sinks : 0;
   int* work = reinterpret_cast<int*>(st.word) + kWorkCounterWord;
   const long long items = 64 * doc_tiles_at_most(a.N, a.n_docs);
-  const int grid = items < num_sms ? (int)items : num_sms;
-  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, window, sinks, grid,
-                                   work, st.word);
+  constexpr int kCtas = PAIR ? 2 : 1;  // that work on an item together
+  const int workers = items < num_sms / kCtas ? (int)items : num_sms / kCtas;
+  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kCtas * 128, window, sinks,
+                                   workers, work, st.word);
   if (e != cudaSuccess) return e;
   DevStatus dst{st.word, st.wait_limit_ns};
-  return launch_pdl(document_attn_tc, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, to,
-                    a.scale * 1.4426950408889634f, window, sinks, work, (const uint8_t*)a.plan, a.o, a.o_row, dst);
+  const float sl2 = a.scale * 1.4426950408889634f;
+  if (PAIR)
+    return launch_pdl_cluster2(document_attn_tc<PAIR>, dim3(2 * workers), dim3(kThreads), kSmemBytes, stream, tq, tk,
+                               tv, to, sl2, window, sinks, work, (const uint8_t*)a.plan, a.o, a.o_row, dst);
+  return launch_pdl(document_attn_tc<PAIR>, dim3(workers), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, to, sl2,
+                    window, sinks, work, (const uint8_t*)a.plan, a.o, a.o_row, dst);
+}
+}  // namespace
+
+cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream) {
+  const bool pairs = a.N >= kPairRows * (long long)a.n_docs && (a.window == 0 || a.window >= kPairRows);
+  return pairs ? launch_tiles<true>(a, st, num_sms, stream) : launch_tiles<false>(a, st, num_sms, stream);
 }
 
 }  // namespace mla

@@ -1804,7 +1804,7 @@ static bool encode(CUtensorMap* map, CUtensorMapDataType dt, int rank, const voi
                    const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint32_t estr[3] = {1, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, dt, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1837,6 +1837,14 @@ bool make_tmap_rows128_3d(CUtensorMap* map, const void* base, uint64_t rows, uin
   cuuint64_t strides[2] = {128, rows * 128};
   cuuint32_t box[3] = {64, box_rows, box_outer};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool make_tmap_bf16_atoms(CUtensorMap* map, const void* base, uint64_t rows, uint64_t atoms, uint64_t outer,
+                          uint64_t row_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_rows, uint32_t box_atoms) {
+  cuuint64_t dims[4] = {64, rows, atoms, outer};
+  cuuint64_t strides[3] = {row_stride_bytes, 128, outer_stride_bytes};
+  cuuint32_t box[4] = {64, box_rows, box_atoms, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,

@@ -124,6 +124,10 @@ bool make_tmap_store_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner,
 // outer, box {box_inner, box_mid, 1}, 128-byte swizzle.
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
                        uint64_t mid_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_inner, uint32_t box_mid);
+// bf16 rows of `atoms` x 64 numbers, `outer` of them; a box of box_rows rows and
+// box_atoms of their atoms arrives atom after atom, each box_rows x 128 bytes
+bool make_tmap_bf16_atoms(CUtensorMap* map, const void* base, uint64_t rows, uint64_t atoms, uint64_t outer,
+                          uint64_t row_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_rows, uint32_t box_atoms);
 
 // 3D view of [outer][rows][128 bytes] (contiguous), box {128 bytes, box_rows,
 // box_outer}, 128-byte swizzle: the paged cache's codes and rotary keys.

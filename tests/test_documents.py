@@ -328,3 +328,72 @@ def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
         with pytest.raises(m.MlaError) as e:
             m.mla_document_attention(**{**good, **over})
         assert e.value.status == status
+
+
+LONG = [
+    # rows enough a document on average for pairs of thread blocks with 256 queries
+    ([1536], [0], None, 0, 0),
+    ([1663], [0], None, 0, 0),
+    ([1537], [100], [900], 0, 0),
+    ([3000, 1400, 300], [0, 77, 500], [10, 1477, 0], 0, 0),
+    ([4700, 0, 5], [0, 40, 300], None, 0, 0),
+    ([2000, 1100], [100, 50], [10, 300], 300, 20),
+    ([1700], [30], None, 1, 0),
+    ([1900], [600], None, 1024, 100),
+    ([2600], [0], None, 2000, 4),
+    ([3200], [500], None, 1600, 130),
+    ([3500, 100], [0, 900], [200, 1000], 1700, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("new,past,prefix,window,sinks", LONG)
+def test_long_documents(gpu_available, new, past, prefix, window, sinks):
+    keys = [a + b for a, b in zip(new, past)]
+    cu_q, cu_k = starts(new), starts(keys)
+    q, k, v = normal(1, cu_q[-1], 64 * 192), normal(2, 64, cu_k[-1], 192), normal(3, 64, cu_k[-1], 128)
+    out = run(q, k, v, cu_q, cu_k, prefix, window, sinks)
+    check(f64(out), f64(q), f64(k), f64(v), cu_q, cu_k, prefix, window, sinks, heads=(0, 37, 63))
+
+
+@gpu
+def test_long_documents_and_their_neighbours(gpu_available):
+    """Long documents with more queries than keys, offsets, rows behind the last; NaN and infinities in the others, in
+    front and behind: the same bits; scores that grow along the keys; the same again from a graph, on two streams."""
+    import torch
+    new, keys = [1700, 1433, 1600], [1700, 1333, 2000]
+    cu_q, cu_k = starts(new, 3), starts(keys, 9)
+    N = cu_q[-1] + 20
+    q, k, v = normal(1, N, 64 * 192), normal(2, 64, cu_k[-1] + 20, 192), normal(3, 64, cu_k[-1] + 20, 128)
+    q.view(N, 64, 192)[..., 5] = 3.0
+    for d in range(3):
+        k[:, cu_k[d]:cu_k[d + 1], 5] = torch.linspace(-60, 60, keys[d], device="cuda").to(torch.bfloat16)
+    clean = run(q, k, v, cu_q, cu_k, fill=7.0)
+    check(f64(clean), f64(q), f64(k), f64(v), cu_q, cu_k, None, 0, 0, heads=(5, 60))
+    assert bool((clean[:3] == 7).all()) and bool((clean[cu_q[-1]:] == 7).all())
+    assert bool((clean[cu_q[1]:cu_q[1] + 100] == 0).all()), "rows before the document's first key"
+    for d in range(3):
+        for value in (float("nan"), float("inf")):
+            q2, k2, v2 = torch.full_like(q, value), torch.full_like(k, value), torch.full_like(v, value)
+            q2[cu_q[d]:cu_q[d + 1]] = q[cu_q[d]:cu_q[d + 1]]
+            for x2, x in ((k2, k), (v2, v)):
+                x2[:, cu_k[d]:cu_k[d + 1]] = x[:, cu_k[d]:cu_k[d + 1]]
+            got = run(q2, k2, v2, cu_q, cu_k)
+            assert torch.equal(got[cu_q[d]:cu_q[d + 1]], clean[cu_q[d]:cu_q[d + 1]]), (d, value)
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.full_like(clean, 7.0) for _ in range(2)]
+    cq, ck, wss = ints(cu_q), ints(cu_k), [m.alloc_workspace(m.MODE_DOCUMENTS, 3, N) for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for s, out, ws in zip(streams, outs, wss):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            for _ in range(3):
+                m.mla_document_attention(q, cq, k, v, out, ws, cu_k=ck)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert [m.mla_device_status(ws) for ws in wss] == [0, 0]
+    assert torch.equal(outs[0], clean) and torch.equal(outs[1], clean)
