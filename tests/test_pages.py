@@ -689,3 +689,31 @@ def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
         with pytest.raises(ValueError):
             m.mla_pages_compact(dev.cache, dev.pool, **{**dict(moved=ints([0] * 20), n_live=ints([0]), workspace=ws), **over})
     dev.same()
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 500, 9000])
+def test_copy_of_lists(gpu_available, n):
+    """Random pairs in one cache and between two, with sources that are written, repeated destinations and numbers
+    outside, in lists around the length of a warp and longer than a plan's threads."""
+    rng = np.random.default_rng(n)
+    a, b = Book(1, 1, 300, 16, 1), Book(1, 1, 200, 16, 2)
+    da, db = Device(a), Device(b)
+
+    def run(src, dst, x, dx, y, dy):
+        want = x.copy(y, src, dst)
+        ws = m.alloc_workspace(m.MODE_PAGES, len(src), y.n_pages).fill_(0xa5)
+        m.mla_pages_copy(dx.cache, dy.cache, ints(src), ints(dst), ws)
+        assert m.mla_device_status(ws) == want
+        dx.same()
+        dy.same()
+        return want
+
+    for _ in range(3):
+        run(rng.integers(-2, 302, n), rng.integers(-2, 202, n), a, da, b, db)
+        run(rng.integers(0, 300, n), rng.integers(0, 300, n), a, da, a, da)
+        run(rng.integers(0, 200, n), rng.integers(0, 300, n), b, db, a, da)
+    pages = rng.permutation(300)
+    k = min(n, 150)
+    assert run(pages[:k], pages[150:150 + k], a, da, a, da) == OK
+    assert run(pages[:k], pages[:k], a, da, a, da) == OK  # each onto itself
