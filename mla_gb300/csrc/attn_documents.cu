@@ -51,7 +51,8 @@
 // Pairs of CTAs (PAIR): for long documents a cluster of two takes two query tiles of a
 // document with one product of 256 rows (cta_group::2), of whose keys and values each
 // CTA holds half, so that a key tile costs an SM 30 KB in and 30 KB out: 5 documents
-// of up to 4,096 tokens take 700 us on the GPU instead of 731, 4 of 4,096 tokens 883
+// of up to 4,096 tokens take 708 us instead of 758 (back to back, at the power limit; one
+// cold launch 611, the tensor pipe busy in 89% of its cycles), 4 of 4,096 tokens 883
 // instead of 956, one of 16,384 tokens 2,890 instead of 3,043 (1.0 of the products'
 // burst rate).  The even CTA schedules and issues; each CTA loads its half and
 // does the softmax of its own 128 rows.  What it costs: the first tile's products
@@ -62,7 +63,8 @@
 // tile 309 and 820 us; this form 248 and 745 with lane-0 loops and Q through
 // registers.  Two CTAs sharing K/V tiles by multicast, with products of their own, 263
 // and 749 (the copies' writes stay); warps of their own for the output 260 and 771;
-// pairs with a third of a K tile a copy 295 and 703.
+// pairs with a third of a K tile a copy 295 and 703; O stored without staging 266 and
+// 753, and with its 32 KB as a third whole slot of K 253 and 737.
 //
 // Code size: the roles' loops share one instruction cache.  At 81 KB of code (every
 // wait inlined with its clock) 5.4 of the stalls per instruction were for
