@@ -16,12 +16,10 @@
 // of the next document in the Q tile are computed and not stored; a row that
 // sees no key has the sum zero and is stored as zeros.
 //
-// Warp roles (384 threads):
-//   warp 0   work scheduler (counter -> a 4-slot ring of items), then TMA: K
-//            tiles, 64 dimensions at a time, into a ring of 7 such thirds (TMA
+// Warp roles (512 threads):
+//   warp 0   TMA: K tiles, 64 dimensions at a time, into a ring of 7 such thirds (TMA
 //            takes 1,900 cycles under load: with a ring of two whole tiles, each
-//            slot idle for that long, a tile took 160 cycles more), and the next
-//            item's Q tile
+//            slot idle for that long, a tile took 160 cycles more)
 //   warp 1   TMEM allocation; an item's Q into tensor memory (tcgen05.cp), then
 //            S_x = Q K_x^T (M=128 N=96 K=192) into score buffer x & 1, x
 //            counting this CTA's key tiles
@@ -37,6 +35,12 @@
 //            item's end the group without the last tile hands over its sums and
 //            goes on to the next item's first tile, which is its own; the other
 //            one writes O / l.
+//   warp 12  work scheduler (counter -> a 4-slot ring of items), then TMA: the item's Q
+//            tile.  (Beside the K tiles in warp 0, with items taken three ahead: 8
+//            documents with a prefix 150 us where they take 128, 16 of up to 1,531
+//            tokens 240 where 232.  An SM then sat on up to 80 key tiles while others
+//            had none, and warp 0's own instructions held the K tiles up.)
+//   (warps 13..15 give their registers to the softmax groups)
 // 96 keys: two score buffers, two of P (so that a P is stored while the product of
 // the one before runs), O and all of Q take the 512 tensor-memory columns exactly,
 // and products of N = 96 from tensor memory run at the full rate (4,080 MAC a clock
@@ -46,19 +50,18 @@
 // also what its products take (960 at 4,096 MAC a clock); an item adds Q and O,
 // 160 KB.  Measured about 1,200 cycles a tile and 1,100 an item.  With the K and V
 // copies left out (wrong results) 16 documents of up to 1,531 tokens took 185 us
-// where they take 241, 5 of up to 4,096 tokens 523 where they took 720.
+// where they took 241, 5 of up to 4,096 tokens 523 where they took 720.
 //
 // Pairs of CTAs (PAIR): for long documents a cluster of two takes two query tiles of a
 // document with one product of 256 rows (cta_group::2), of whose keys and values each
 // CTA holds half, so that a key tile costs an SM 30 KB in and 30 KB out: 5 documents
-// of up to 4,096 tokens take 708 us instead of 758 (back to back, at the power limit; one
-// cold launch 611, the tensor pipe busy in 89% of its cycles), 4 of 4,096 tokens 883
-// instead of 956, one of 16,384 tokens 2,890 instead of 3,043 (1.0 of the products'
-// burst rate).  The even CTA schedules and issues; each CTA loads its half and
-// does the softmax of its own 128 rows.  What it costs: the first tile's products
-// over the keys that only the second sees, and a tile of nothing behind an odd
-// number of them, 4% more tiles in the first case, 22% for 16 documents of up to
-// 1,531 tokens (262 us instead of 245).
+// of up to 4,096 tokens take 711 us instead of 740 (back to back, at the power limit),
+// one of 16,384 tokens 2,730 instead of 2,874 (one cold launch), 8 of 512 new tokens
+// behind 4,096 464 instead of 507.  The tensor pipe is then busy in 89% of its cycles.  The
+// even CTA schedules and issues; each CTA loads its half and does the softmax of its own
+// 128 rows.  What it costs: the first tile's products over the keys that only the second
+// sees, and a tile of nothing behind an odd number of them, 4% more tiles in the first
+// case, 22% for 16 documents of up to 1,531 tokens (307 us instead of 277).
 // Measured on the way, GPU time: the windowed prefill's two threads a row on the same
 // tile 309 and 820 us; this form 248 and 745 with lane-0 loops and Q through
 // registers.  Two CTAs sharing K/V tiles by multicast, with products of their own, 263
@@ -92,7 +95,8 @@ template <bool PAIR>
 struct Rings {
   static constexpr int kKSlots = PAIR ? 4 : 7, kVSlots = PAIR ? 6 : 5;
   static constexpr int kKTiles = PAIR ? kKSlots : 3;  // in flight at most
-  static constexpr uint32_t kKSlotBytes = PAIR ? 3 * kHalfAtom : kKeyAtom, kVSlotBytes = PAIR ? kKeyAtom : 2 * kHalfAtom;
+  static constexpr uint32_t kKSlotBytes = PAIR ? 3 * kHalfAtom : kKeyAtom;
+  static constexpr uint32_t kVSlotBytes = PAIR ? kKeyAtom : 2 * kHalfAtom;
   static constexpr uint32_t kVOff = kKOff + kKSlots * kKSlotBytes, kEnd = kVOff + kVSlots * kVSlotBytes;
 };
 constexpr uint32_t kBarOff = Rings<false>::kEnd;
@@ -105,18 +109,18 @@ static_assert(kSmemBytes <= 232448, "document attention shared memory");
 // tensor memory columns: S_0, S_1 (fp32), O (fp32), P_0, P_1 (bf16 pairs), Q (bf16 pairs)
 constexpr uint32_t kTmS = 0, kTmO = 2 * kKeys, kTmP = kTmO + 128, kTmQ = kTmP + kKeys;
 static_assert(kTmQ + 96 == 512, "tensor memory columns");
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on at a time (16 MB: the documents of one
                                                  // new token 15.9 us where they take 14.7, 8 with a prefix 155 where 150)
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 constexpr int kItemRing = 4;
+constexpr int kAhead = 4;                        // key tiles left of an item when the next is asked for (3 to 12 alike)
 // Pairs from this many rows of q a document on (8 documents of random lengths around a mean,
-// in us: 1,024 tokens 196 as single tiles, 207 in pairs; 1,280: 308, 311; 1,536: 422, 413;
-// 2,048: 730, 711; 6,000: 4,258, 4,030; a document's own length matters more near there,
-// 1,400 tokens are 11 tiles or 12 in pairs, 290 and 311), and under a window of this many
-// keys on (the pair's keys are its window's and 256, a tile's 128: 5 documents of 4,000
-// tokens under 512 keys 404, 433; 1,024: 602, 614; 1,536: 779, 782; 2,048: 918, 880).
-constexpr int kPairRows = 1536;
+// in us: 1,024 tokens 209 as single tiles, 220 in pairs; 1,536: 406, 417; 2,048: 656, 661;
+// 3,000: 1,277, 1,276; 6,000: 4,578, 4,410; 5 of 2,000 to 4,096: 740, 711), and under a window
+// of this many keys on (the pair's keys are its window's and 256, a tile's 128: 5 documents
+// of 4,000 tokens under 512 keys 470, 520; 1,536: 795, 805; 2,048: 940, 932).
+constexpr int kPairRows = 2048;
 
 // A warp's bounded wait, in few instructions: 2^21 tries (tens of milliseconds at
 // least; a wait is for a few tiles' work, microseconds).  A role whose wait gives
@@ -155,7 +159,7 @@ struct Bars {
   // per quarter of the rows (a warp of each group): every phase is one that a warp has
   // waited for or completed itself, so that its parity cannot be mistaken
   uint64_t ref[2][4], sum[4], o_free[4], o_stored[4];
-  uint64_t drain_s, drain_pv;
+  uint64_t near_end, drain_s, drain_pv;
   uint32_t tmem_slot;
   int abort;  // the role whose wait gave up
 };
@@ -255,6 +259,16 @@ __device__ __forceinline__ void doc_item(int w, int n_tiles, int log, int& tile,
   head = (g << log) + (r & ((1 << log) - 1));
 }
 
+// A warpgroup's registers a thread, from those of the launch (65,536 / 512 threads = 128).
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // One lane of a whole warp.  The control warps run their loops as warps and let one
 // lane issue, so that the operands of the copies and products are uniform values:
 // with the loops in lane 0 alone the twelve products of a tile's scores took 1,255
@@ -315,9 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar->q_free, 1);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&bar->item_full[i], 1);
-      // V producer, S issuer, P.V issuer, softmax warps; in a pair the odd CTA's scheduler for its
-      // own V producer and softmax warps
-      mbar_init(&bar->item_empty[i], leader ? 11 + PAIR : 9);
+      // producers, issuers and softmax warps; in a pair the odd CTA's scheduler for its own
+      mbar_init(&bar->item_empty[i], leader ? 12 + PAIR : 10);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->p_full[i], PAIR ? 8 : 4);  // the group's warps, of both CTAs
@@ -340,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar->o_free[q], 32);
       mbar_init(&bar->o_stored[q], 1);
     }
+    mbar_init(&bar->near_end, 1);
     mbar_init(&bar->drain_s, 1);
     mbar_init(&bar->drain_pv, 1);
     bar->abort = 0;
@@ -363,33 +377,248 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
 
   bool ok = true;
-  if (warp == 0) {
-    // ---- work scheduler, Q and K producer ----
-    if (elected()) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-    }
-    const DocPlan* head = reinterpret_cast<const DocPlan*>(plan);
-    const int n_tiles = head->n_tiles, group_log = head->group_log, n_items = 64 * n_tiles;
-    const int* tiles = reinterpret_cast<const int*>(plan + sizeof(DocPlan)) + min(lane, (int)sizeof(DocTile) / 4 - 1);
-    DocTile* const ring = reinterpret_cast<DocTile*>(smem + kTileOff);
-    Place<kKSlots> k;
-    Place<kKTiles> full;
-    int q_loads = 0;
-    // Item it + 1 is posted to the ring, where every role finds it, before item `it` is
-    // loaded; its tile was fetched (a word a lane) after the item before, its index asked
-    // for before that.
-    int index = leader && lane == 0 ? atomicAdd(work, 1) : 0, word = 0;
+  if (warp < 4) {
+    registers_down<96>();
+    if (warp == 0) {
+      // ---- K producer ----
+      if (elected()) tma_prefetch_desc(&tmK);
+      Place<kKSlots> k;
+      Place<kKTiles> full;
 #pragma unroll 1
-    for (int it = -2;; ++it) {
-      const DocTile& tile = ring[(it + kItemRing) % kItemRing];
-      DocTile& next = ring[(it + 1 + kItemRing) % kItemRing];
-      if (it >= -1) {
-        const int slot = (it + 1) % kItemRing;
+      for (int it = 0; ok; ++it) {
+        DocTile tile;
+        if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
+#pragma unroll 1
+        for (int j = 0; ok && j < tile.n_kv; ++j) {
+          if (leader && j > 0 && j == tile.n_kv - kAhead) {
+            if (elected()) mbar_arrive(&bar->near_end);
+            __syncwarp();
+          }
+          const int key = tile.k_row + tile.key0(j);
+          if (PAIR) {
+            if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
+            if (elected()) {
+              if (leader) mbar_arrive_expect_tx(&bar->k_full[k.slot], 3 * kKeyAtom);
+              load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[k.slot],
+                                key + rank * kHalf, 0, tile.head);
+            }
+            __syncwarp();
+            k.next();
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 3; ++c, k.next()) {
+              if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
+              if (elected()) {
+                if (c == 0) mbar_arrive_expect_tx(&bar->k_full[full.slot], 3 * kKeyAtom);
+                load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[full.slot], key, c,
+                                  tile.head);
+              }
+              __syncwarp();
+            }
+          }
+          full.next();
+        }
+      }
+      // no copy may still be in flight into shared memory (a tile that was left half issued
+      // never arrives: its wait gives up)
+#pragma unroll 1
+      for (int i = 0; leader && i < kKTiles; ++i, full.next()) ok &= wait_for(&bar->k_full[full.slot], full.phase ^ 1);
+    } else if (warp == 1) {
+      if (leader) {
+        // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
+        constexpr uint32_t idesc_s = idesc_bf16(PAIR ? 256 : 128, kKeys, false, false);
+        const uint32_t k_addr = smem_u32(smem + kKOff);
+        int x = 0;
+        Place<kKSlots> k;
+        Place<kKTiles> full;
+#pragma unroll 1
+        for (int it = 0; ok; ++it) {
+          DocTile tile;
+          if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
+          // the item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory as bf16
+          // pairs, the A operand of every S, once the S of the item before are done
+          if (!(ok = wait_for(&bar->q_full, it & 1) && (it == 0 || wait_for(&bar->q_free, (it - 1) & 1)))) break;
+          tc_fence_after();
+          if (elected()) {
+#pragma unroll
+            for (int kk = 0; kk < 12; ++kk)
+              copy_q<PAIR>(tmem + kTmQ + kk * 8,
+                           sdesc_sw128(smem_u32(smem + kQOff) + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024));
+            commit_both<PAIR>(&bar->q_empty);  // the staging atoms may take the Q after it
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
+            const int sb = x & 1;
+            // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
+            if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
+                       (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
+              break;
+            full.next();
+            tc_fence_after();
+            if (PAIR) {
+              const uint64_t kb = sdesc_sw128(k_addr + k.slot * R::kKSlotBytes, 16, 1024);
+              if (elected()) {
+#pragma unroll
+                for (int kk = 0; kk < 12; ++kk)
+                  product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + kk * 8,
+                                kb + (kk >> 2) * (kHalfAtom >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
+                commit_both<PAIR>(&bar->k_empty[k.slot]);
+                commit_both<PAIR>(&bar->s_full[sb]);
+              }
+              __syncwarp();
+              k.next();
+            } else {
+#pragma unroll
+              for (int c = 0; c < 3; ++c, k.next()) {
+                const uint64_t kb = sdesc_sw128(k_addr + k.slot * R::kKSlotBytes, 16, 1024);
+                if (elected()) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc_s,
+                                  c > 0 || kk > 0 ? 1u : 0u);
+                  commit_both<PAIR>(&bar->k_empty[k.slot]);
+                  if (c == 2) commit_both<PAIR>(&bar->s_full[sb]);
+                }
+                __syncwarp();
+              }
+            }
+          }
+          if (!ok) break;
+          if (elected()) commit_leader<PAIR>(&bar->q_free);  // the item's S are done: its Q may be replaced
+          __syncwarp();
+        }
+        if (elected()) commit_leader<PAIR>(&bar->drain_s);
+        __syncwarp();
+        ok &= wait_for(&bar->drain_s, 0);
+      }
+    } else if (warp == 2) {
+      // ---- V producer: half tiles, and clears what lies behind the last key ----
+      Place<kVSlots> v;
+      uint32_t phases = 0;  // of each slot's full barrier
+      if (elected()) tma_prefetch_desc(&tmV);
+#pragma unroll 1
+      for (int it = 0; ok; ++it) {
+        DocTile tile;
+        if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
+#pragma unroll 1
+        for (int j = 0; ok && j < tile.n_kv; ++j) {
+          // (a second half that no query sees is left out)
+          const int keys = tile.keys(j), halves = PAIR || keys <= kHalf ? 1 : 2, first = v.slot;
+          const int key = tile.k_row + tile.key0(j);
+          const bool cut = keys == 0 || (keys & 15);
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h, v.next()) {
+            if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
+            if (elected()) {
+              uint8_t* const at = smem + R::kVOff + v.slot * R::kVSlotBytes;
+              // (in a pair, a tile that is to be cut arrives on each CTA's own barrier)
+              if (h == 0 && (cut || leader))
+                mbar_arrive_expect_tx(&bar->v_full[first], PAIR ? (cut ? 1 : 2) * kKeyAtom : halves * R::kVSlotBytes);
+              if (PAIR && cut)
+                tma_load_4d(at, &tmV, &bar->v_full[first], 0, key, rank, tile.head);
+              else
+                load_leader<PAIR>(at, &tmV, &bar->v_full[first], key + h * kHalf, rank, tile.head);
+            }
+            __syncwarp();
+          }
+          if (ok && cut) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
+            if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+            const int last = halves == 1 ? first : (first + 1) % kVSlots, from = keys - (halves - 1) * kHalf;
+            uint8_t* const mine =
+                smem + R::kVOff + last * R::kVSlotBytes + (PAIR ? 0 : ((lane >> 3) & 1) * kHalfAtom) + (lane & 7) * 16;
+#pragma unroll 1
+            for (int r = from + (PAIR ? lane >> 3 : lane >> 4); r < max(16, (from + 15) & ~15); r += PAIR ? 4 : 2)
+              *reinterpret_cast<uint4*>(mine + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elected()) release_leader<PAIR>(&bar->v_cut[first]);
+            __syncwarp();
+          }
+          if (leader || cut) phases ^= 1u << first;
+        }
+      }
+      // (every tile has arrived: its slot's barrier has left the phase before its next one)
+#pragma unroll 1
+      for (int i = 0; i < kVSlots; ++i) ok &= wait_for(&bar->v_full[i], ((phases >> i) & 1) ^ 1);
+    } else if (warp == 3) {
+      if (leader) {
+        // ---- P.V issuer: O += P_x V_x ----
+        constexpr uint32_t idesc_pv = idesc_bf16(PAIR ? 256 : 128, 128, false, true);
+        const uint32_t v_addr = smem_u32(smem + R::kVOff);
+        int x = 0;
+        Place<kVSlots> v;
+        uint32_t phases = 0, cuts = 0;  // of each slot's full and cut barriers
+#pragma unroll 1
+        for (int it = 0; ok; ++it) {
+          DocTile tile;
+          if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
+#pragma unroll 1
+          for (int j = 0; j < tile.n_kv; ++j, ++x) {
+            const int sb = x & 1, first = v.slot;
+            // the 16-key steps that hold a key (one where there is none: O becomes zeros), the
+            // last one's other rows cleared
+            const int keys = tile.keys(j), steps = max(1, (keys + 15) >> 4);
+            if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+            phases ^= 1u << first;
+            if (keys == 0 || (keys & 15)) {
+              if (!(ok = wait_for<PAIR>(&bar->v_cut[first], (cuts >> first) & 1))) break;
+              cuts ^= 1u << first;
+            }
+            // P_x is written (and, for an item's first tile, the previous item's O read)
+            if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
+            tc_fence_after();
+            constexpr int kSlotsOfTile = PAIR ? 1 : 2, kSteps = kKeys / 16 / kSlotsOfTile;
+#pragma unroll
+            for (int h = 0; h < kSlotsOfTile; ++h) {
+              if (h && keys <= kHalf) break;
+              const uint64_t vb = sdesc_sw128(v_addr + v.slot * R::kVSlotBytes, kHalfAtom, 1024);
+              if (elected()) {
+#pragma unroll
+                for (int kk = 0; kk < kSteps; ++kk)
+                  if (h * kSteps + kk < steps)
+                    product<PAIR>(tmem + kTmO, tmem + kTmP + sb * kHalf + (h * kSteps + kk) * 8, vb + kk * 128, idesc_pv,
+                                  (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                commit_both<PAIR>(&bar->v_empty[v.slot]);
+              }
+              __syncwarp();
+              v.next();
+            }
+            if (elected()) commit_both<PAIR>(&bar->pv_done[sb]);
+            __syncwarp();
+          }
+        }
+        if (elected()) commit_leader<PAIR>(&bar->drain_pv);
+        __syncwarp();
+        ok &= wait_for(&bar->drain_pv, 0);
+      }
+    }
+  } else if (warp >= 12) {
+    registers_down<64>();
+    if (warp == 12) {
+      // ---- work scheduler and Q producer ----
+      const DocPlan* head = reinterpret_cast<const DocPlan*>(plan);
+      const int n_tiles = head->n_tiles, group_log = head->group_log, n_items = 64 * n_tiles;
+      const int* tiles = reinterpret_cast<const int*>(plan + sizeof(DocPlan)) + min(lane, (int)sizeof(DocTile) / 4 - 1);
+      DocTile* const ring = reinterpret_cast<DocTile*>(smem + kTileOff);
+      if (elected()) tma_prefetch_desc(&tmQ);
+      int index = leader && lane == 0 ? atomicAdd(work, 1) : 0, it = 0, n_long = 0;
+#pragma unroll 1
+      for (; ok; ++it) {
+        // the item's tile (a word a lane) into the ring, where every role finds it
+        const int slot = it % kItemRing, turn = it / kItemRing;
         if (leader) {
-          if (it + 1 >= kItemRing && !(ok = wait_for(&bar->item_empty[slot], ((it + 1) / kItemRing - 1) & 1))) break;
+          index = __shfl_sync(0xffffffffu, index, 0);
+          int word = 0;  // (no rows: the end)
+          if (index < n_items) {
+            int at, of;
+            doc_item(index, n_tiles, group_log, at, of);
+            word = tiles[at * (int)(sizeof(DocTile) / 4)];
+            if (lane == (int)offsetof(DocTile, head) / 4) word = of;
+          }
+          if (turn > 0 && !(ok = wait_for(&bar->item_empty[slot], (turn - 1) & 1))) break;
           if (lane < (int)sizeof(DocTile) / 4) {
-            int* const at = reinterpret_cast<int*>(&next) + lane;
+            int* const at = reinterpret_cast<int*>(&ring[slot]) + lane;
             *at = word;
             if (PAIR) st_cluster(mapa_rank(smem_u32(at), 1), word);
           }
@@ -399,246 +628,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (PAIR) mbar_arrive_cluster(mapa_rank(smem_u32(&bar->item_full[slot]), 1));
           }
           __syncwarp();
-        } else if (!(ok = wait_for<PAIR>(&bar->item_full[slot], ((it + 1) / kItemRing) & 1))) {
+        } else if (!(ok = wait_for<PAIR>(&bar->item_full[slot], turn & 1))) {
           break;
         }
-      }
-      if (it >= 0 && tile.rows == 0) break;
-      const int after = leader && lane == 0 ? atomicAdd(work, 1) : 0;
-      // K tiles, 64 dimensions at a time; behind the second one (at once, for the first item)
-      // the next item's Q, into the staging atoms once this one's has been copied into tensor
-      // memory: by then it has, and the copy has the rest of the item to arrive
-      const int n_kv = it < 0 ? 0 : tile.n_kv, q_at = min(2, n_kv);
-#pragma unroll 1
-      for (int j = 0; ok; ++j) {
-        if (j == q_at && it >= -1 && next.rows > 0) {
-          if (it >= 0 && !(ok = wait_for(&bar->q_empty, it & 1))) break;
-          if (elected()) {
-            if (leader) mbar_arrive_expect_tx(&bar->q_full, (PAIR ? 6 : 3) * kAtom);
-            load_leader<PAIR>(smem + kQOff, &tmQ, &bar->q_full, next.q_row + rank * 128, next.head * 3, 0);
-          }
-          __syncwarp();
-          ++q_loads;
+        const int rows = ring[slot].rows, n_kv = ring[slot].n_kv, q_row = ring[slot].q_row, of = ring[slot].head;
+        if (rows == 0) break;
+        // A long item's successor is asked for when its last key tiles are being loaded, so that
+        // no SM sits on work while others have none; a short one's at once, for its latency
+        const bool is_long = n_kv > kAhead;
+        if (leader && !is_long) index = lane == 0 ? atomicAdd(work, 1) : 0;
+        // its Q, into the staging atoms once the one before has been copied into tensor memory
+        if (it > 0 && !(ok = wait_for(&bar->q_empty, (it - 1) & 1))) break;
+        if (elected()) {
+          if (leader) mbar_arrive_expect_tx(&bar->q_full, (PAIR ? 6 : 3) * kAtom);
+          load_leader<PAIR>(smem + kQOff, &tmQ, &bar->q_full, q_row + rank * 128, of * 3, 0);
         }
-        if (j == n_kv) break;
-        const int key = tile.k_row + tile.key0(j);
-        if (PAIR) {
-          if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
-          if (elected()) {
-            if (leader) mbar_arrive_expect_tx(&bar->k_full[k.slot], 3 * kKeyAtom);
-            load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[k.slot], key + rank * kHalf, 0,
-                              tile.head);
-          }
-          __syncwarp();
-          k.next();
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < 3; ++c, k.next()) {
-            if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
-            if (elected()) {
-              if (c == 0) mbar_arrive_expect_tx(&bar->k_full[full.slot], 3 * kKeyAtom);
-              load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[full.slot], key, c, tile.head);
-            }
-            __syncwarp();
-          }
-        }
-        full.next();
-      }
-      if (!ok) break;
-      if (!leader) {
         __syncwarp();
-        if (it >= 2) {  // (two items back: they have been read by now)
+        if (leader && is_long) {
+          if (!(ok = wait_for(&bar->near_end, n_long++ & 1))) {
+            ++it;  // (its Q is on the way)
+            break;
+          }
+          index = lane == 0 ? atomicAdd(work, 1) : 0;
+        }
+        if (!leader && it >= 2) {  // two items back: it has been read by now
           if (!(ok = wait_for(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1))) break;
           if (elected()) release_leader<PAIR>(&bar->item_empty[(it - 2) % kItemRing]);
-        }
-        __syncwarp();
-        continue;
-      }
-      index = __shfl_sync(0xffffffffu, index, 0);
-      word = 0;  // (no rows: the end)
-      if (index < n_items) {
-        int at, of;
-        doc_item(index, n_tiles, group_log, at, of);
-        word = tiles[at * (int)(sizeof(DocTile) / 4)];
-        if (lane == (int)offsetof(DocTile, head) / 4) word = of;
-      }
-      index = after;
-    }
-    // no copy may still be in flight into shared memory (a tile that was left half issued
-    // never arrives: its wait gives up)
-    if (leader && q_loads) ok &= wait_for(&bar->q_full, (q_loads - 1) & 1);
-#pragma unroll 1
-    for (int i = 0; leader && i < kKTiles; ++i, full.next()) ok &= wait_for(&bar->k_full[full.slot], full.phase ^ 1);
-  } else if (warp == 1) {
-    if (leader) {
-      // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
-      constexpr uint32_t idesc_s = idesc_bf16(PAIR ? 256 : 128, kKeys, false, false);
-      const uint32_t k_addr = smem_u32(smem + kKOff);
-      int x = 0;
-      Place<kKSlots> k;
-      Place<kKTiles> full;
-#pragma unroll 1
-      for (int it = 0; ok; ++it) {
-        DocTile tile;
-        if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
-        // the item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory as bf16
-        // pairs, the A operand of every S, once the S of the item before are done
-        if (!(ok = wait_for(&bar->q_full, it & 1) && (it == 0 || wait_for(&bar->q_free, (it - 1) & 1)))) break;
-        tc_fence_after();
-        if (elected()) {
-#pragma unroll
-          for (int kk = 0; kk < 12; ++kk)
-            copy_q<PAIR>(tmem + kTmQ + kk * 8,
-                         sdesc_sw128(smem_u32(smem + kQOff) + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024));
-          commit_both<PAIR>(&bar->q_empty);  // the staging atoms may take the Q after it
-        }
-        __syncwarp();
-#pragma unroll 1
-        for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
-          const int sb = x & 1;
-          // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
-          if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
-                     (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
-            break;
-          full.next();
-          tc_fence_after();
-          if (PAIR) {
-            const uint64_t kb = sdesc_sw128(k_addr + k.slot * R::kKSlotBytes, 16, 1024);
-            if (elected()) {
-#pragma unroll
-              for (int kk = 0; kk < 12; ++kk)
-                product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + kk * 8,
-                              kb + (kk >> 2) * (kHalfAtom >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
-              commit_both<PAIR>(&bar->k_empty[k.slot]);
-              commit_both<PAIR>(&bar->s_full[sb]);
-            }
-            __syncwarp();
-            k.next();
-          } else {
-#pragma unroll
-            for (int c = 0; c < 3; ++c, k.next()) {
-              const uint64_t kb = sdesc_sw128(k_addr + k.slot * R::kKSlotBytes, 16, 1024);
-              if (elected()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc_s,
-                                c > 0 || kk > 0 ? 1u : 0u);
-                commit_both<PAIR>(&bar->k_empty[k.slot]);
-                if (c == 2) commit_both<PAIR>(&bar->s_full[sb]);
-              }
-              __syncwarp();
-            }
-          }
-        }
-        if (!ok) break;
-        if (elected()) commit_leader<PAIR>(&bar->q_free);  // the item's S are done: its Q may be replaced
-        __syncwarp();
-      }
-      if (elected()) commit_leader<PAIR>(&bar->drain_s);
-      __syncwarp();
-      ok &= wait_for(&bar->drain_s, 0);
-    }
-  } else if (warp == 2) {
-    // ---- V producer: half tiles, and clears what lies behind the last key ----
-    Place<kVSlots> v;
-    uint32_t phases = 0;  // of each slot's full barrier
-    if (elected()) tma_prefetch_desc(&tmV);
-#pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      DocTile tile;
-      if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
-#pragma unroll 1
-      for (int j = 0; ok && j < tile.n_kv; ++j) {
-        // (a second half that no query sees is left out)
-        const int keys = tile.keys(j), halves = PAIR || keys <= kHalf ? 1 : 2, first = v.slot;
-        const int key = tile.k_row + tile.key0(j);
-        const bool cut = keys == 0 || (keys & 15);
-#pragma unroll 1
-        for (int h = 0; h < halves; ++h, v.next()) {
-          if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
-          if (elected()) {
-            uint8_t* const at = smem + R::kVOff + v.slot * R::kVSlotBytes;
-            // (in a pair, a tile that is to be cut arrives on each CTA's own barrier)
-            if (h == 0 && (cut || leader))
-              mbar_arrive_expect_tx(&bar->v_full[first], PAIR ? (cut ? 1 : 2) * kKeyAtom : halves * R::kVSlotBytes);
-            if (PAIR && cut)
-              tma_load_4d(at, &tmV, &bar->v_full[first], 0, key, rank, tile.head);
-            else
-              load_leader<PAIR>(at, &tmV, &bar->v_full[first], key + h * kHalf, rank, tile.head);
-          }
-          __syncwarp();
-        }
-        if (ok && cut) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
-          if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
-          const int last = halves == 1 ? first : (first + 1) % kVSlots, from = keys - (halves - 1) * kHalf;
-          uint8_t* const mine =
-              smem + R::kVOff + last * R::kVSlotBytes + (PAIR ? 0 : ((lane >> 3) & 1) * kHalfAtom) + (lane & 7) * 16;
-#pragma unroll 1
-          for (int r = from + (PAIR ? lane >> 3 : lane >> 4); r < max(16, (from + 15) & ~15); r += PAIR ? 4 : 2)
-            *reinterpret_cast<uint4*>(mine + r * 128) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elected()) release_leader<PAIR>(&bar->v_cut[first]);
-          __syncwarp();
-        }
-        if (leader || cut) phases ^= 1u << first;
-      }
-    }
-    // (every tile has arrived: its slot's barrier has left the phase before its next one)
-#pragma unroll 1
-    for (int i = 0; i < kVSlots; ++i) ok &= wait_for(&bar->v_full[i], ((phases >> i) & 1) ^ 1);
-  } else if (warp == 3) {
-    if (leader) {
-      // ---- P.V issuer: O += P_x V_x ----
-      constexpr uint32_t idesc_pv = idesc_bf16(PAIR ? 256 : 128, 128, false, true);
-      const uint32_t v_addr = smem_u32(smem + R::kVOff);
-      int x = 0;
-      Place<kVSlots> v;
-      uint32_t phases = 0, cuts = 0;  // of each slot's full and cut barriers
-#pragma unroll 1
-      for (int it = 0; ok; ++it) {
-        DocTile tile;
-        if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
-#pragma unroll 1
-        for (int j = 0; j < tile.n_kv; ++j, ++x) {
-          const int sb = x & 1, first = v.slot;
-          // the 16-key steps that hold a key (one where there is none: O becomes zeros), the
-          // last one's other rows cleared
-          const int keys = tile.keys(j), steps = max(1, (keys + 15) >> 4);
-          if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
-          phases ^= 1u << first;
-          if (keys == 0 || (keys & 15)) {
-            if (!(ok = wait_for<PAIR>(&bar->v_cut[first], (cuts >> first) & 1))) break;
-            cuts ^= 1u << first;
-          }
-          // P_x is written (and, for an item's first tile, the previous item's O read)
-          if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
-          tc_fence_after();
-          constexpr int kSlotsOfTile = PAIR ? 1 : 2, kSteps = kKeys / 16 / kSlotsOfTile;
-#pragma unroll
-          for (int h = 0; h < kSlotsOfTile; ++h) {
-            if (h && keys <= kHalf) break;
-            const uint64_t vb = sdesc_sw128(v_addr + v.slot * R::kVSlotBytes, kHalfAtom, 1024);
-            if (elected()) {
-#pragma unroll
-              for (int kk = 0; kk < kSteps; ++kk)
-                if (h * kSteps + kk < steps)
-                  product<PAIR>(tmem + kTmO, tmem + kTmP + sb * kHalf + (h * kSteps + kk) * 8, vb + kk * 128, idesc_pv,
-                                (j > 0 || h > 0 || kk > 0) ? 1u : 0u);
-              commit_both<PAIR>(&bar->v_empty[v.slot]);
-            }
-            __syncwarp();
-            v.next();
-          }
-          if (elected()) commit_both<PAIR>(&bar->pv_done[sb]);
           __syncwarp();
         }
       }
-      if (elected()) commit_leader<PAIR>(&bar->drain_pv);
-      __syncwarp();
-      ok &= wait_for(&bar->drain_pv, 0);
+      if (leader && it > 0) ok &= wait_for(&bar->q_full, (it - 1) & 1);
     }
   } else {
+    registers_up<168>();
     // ---- softmax groups, one thread a query row ----
     const int g = (warp >> 2) - 1;
     const int quarter = warp & 3;

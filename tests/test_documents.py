@@ -397,3 +397,70 @@ def test_long_documents_and_their_neighbours(gpu_available):
     torch.cuda.synchronize()
     assert [m.mla_device_status(ws) for ws in wss] == [0, 0]
     assert torch.equal(outs[0], clean) and torch.equal(outs[1], clean)
+
+
+PAIRS = [
+    # 2,048 rows a document on average and more, where pairs of thread blocks take 256 queries at a time
+    ([2048], [0], None, 0, 0),
+    ([2175], [0], None, 0, 0),
+    ([2177], [100], [900], 0, 0),
+    ([4100, 2100, 300], [0, 77, 500], [10, 2177, 0], 0, 0),
+    ([6200, 0, 5], [0, 40, 300], None, 0, 0),
+    ([2900], [500], None, 2048, 130),
+    ([2500, 2000], [0, 1500], [200, 3500], 2400, 7),
+]
+
+
+@gpu
+@pytest.mark.parametrize("new,past,prefix,window,sinks", PAIRS)
+def test_documents_in_pairs(gpu_available, new, past, prefix, window, sinks):
+    test_long_documents(gpu_available, new, past, prefix, window, sinks)
+
+
+@gpu
+def test_pairs_and_their_neighbours(gpu_available):
+    """As the test of long documents and their neighbours, with more queries than keys."""
+    import torch
+    new, keys = [2300, 2033, 2200], [2300, 333, 2600]
+    cu_q, cu_k = starts(new, 3), starts(keys, 9)
+    N = cu_q[-1] + 20
+    q, k, v = normal(1, N, 64 * 192), normal(2, 64, cu_k[-1] + 20, 192), normal(3, 64, cu_k[-1] + 20, 128)
+    q.view(N, 64, 192)[..., 5] = 3.0
+    for d in range(3):
+        k[:, cu_k[d]:cu_k[d + 1], 5] = torch.linspace(-60, 60, keys[d], device="cuda").to(torch.bfloat16)
+    clean = run(q, k, v, cu_q, cu_k, fill=7.0)
+    check(f64(clean), f64(q), f64(k), f64(v), cu_q, cu_k, None, 0, 0, heads=(5, 60))
+    assert bool((clean[:3] == 7).all()) and bool((clean[cu_q[-1]:] == 7).all())
+    assert bool((clean[cu_q[1]:cu_q[1] + 1700] == 0).all()), "rows before the document's first key"
+    for d in range(3):
+        for value in (float("nan"), float("inf")):
+            q2, k2, v2 = torch.full_like(q, value), torch.full_like(k, value), torch.full_like(v, value)
+            q2[cu_q[d]:cu_q[d + 1]] = q[cu_q[d]:cu_q[d + 1]]
+            for x2, x in ((k2, k), (v2, v)):
+                x2[:, cu_k[d]:cu_k[d + 1]] = x[:, cu_k[d]:cu_k[d + 1]]
+            got = run(q2, k2, v2, cu_q, cu_k)
+            assert torch.equal(got[cu_q[d]:cu_q[d + 1]], clean[cu_q[d]:cu_q[d + 1]]), (d, value)
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.full_like(clean, 7.0) for _ in range(2)]
+    cq, ck, wss = ints(cu_q), ints(cu_k), [m.alloc_workspace(m.MODE_DOCUMENTS, 3, N) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, out, ws in zip(streams, outs, wss):
+            m.mla_document_attention(q, cq, k, v, out, ws, cu_k=ck, stream=s)
+    torch.cuda.synchronize()
+    assert [m.mla_device_status(ws) for ws in wss] == [0, 0]
+    assert torch.equal(outs[0], clean) and torch.equal(outs[1], clean)
+
+
+@gpu
+@pytest.mark.parametrize("cu,status", [([5, 5], 0), ([2100, 2100], 0), ([7, 8], 0), ([0, 2101], -1), ([-1, 2000], -1),
+                                       ([50, 40], -1)])
+def test_room_for_many_rows_that_are_not_there(gpu_available, cu, status):
+    """Rows enough for pairs, offsets that use hardly any or none of them, or that are refused."""
+    q, k, v = normal(1, 2100, 64 * 192), normal(2, 64, 2100, 192), normal(3, 64, 2100, 128)
+    out = run(q, k, v, cu, None, status=status, fill=5.0)
+    if status == 0:
+        check(f64(out), f64(q), f64(k), f64(v), cu, cu, None, 0, 0)
+    rest = out.clone()
+    if status == 0:
+        rest[cu[0]:cu[1]] = 5
+    assert bool((rest == 5).all())
