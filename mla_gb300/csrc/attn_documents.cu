@@ -67,7 +67,9 @@
 // registers.  Two CTAs sharing K/V tiles by multicast, with products of their own, 263
 // and 749 (the copies' writes stay); warps of their own for the output 260 and 771;
 // pairs with a third of a K tile a copy 295 and 703; O stored without staging 266 and
-// 753, and with its 32 KB as a third whole slot of K 253 and 737.
+// 753, and with its 32 KB as a third whole slot of K 253 and 737.  (All of them graphs of
+// a few passes; a second of them runs into the power limit, 1.36 kW at 1.47 GHz, and takes
+// 277 and 711 us where a single launch takes 237 and 611.)
 //
 // Code size: the roles' loops share one instruction cache.  At 81 KB of code (every
 // wait inlined with its clock) 5.4 of the stalls per instruction were for
