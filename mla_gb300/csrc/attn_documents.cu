@@ -5,8 +5,8 @@
 // after the other, each seeing its own keys only (mla_document_attention).
 // Computed in the flash form: online softmax over tiles of 96 keys.
 //
-// A plan kernel lists the documents' query tiles of up to 128 rows, a tile
-// never holding rows of two documents, heaviest first.  Persistent: one CTA per
+// A plan kernel (or, for a few tiles, one warp of each CTA) lists the documents' query tiles of
+// up to 128 rows, a tile never holding rows of two documents, heaviest first.  Persistent: one CTA per
 // SM takes items (tile, head) from an atomic counter, in groups of heads whose
 // K/V stay in L2.  An item's key tiles begin at the document's (or the window's)
 // first key.  V rows behind the last key that the tile's queries see would be
@@ -123,6 +123,10 @@ constexpr int kAhead = 4;                        // key tiles left of an item wh
 // of this many keys on (the pair's keys are its window's and 256, a tile's 128: 5 documents
 // of 4,000 tokens under 512 keys 470, 520; 1,536: 795, 805; 2,048: 940, 932).
 constexpr int kPairRows = 2048;
+// Up to this many query tiles each CTA makes the plan itself and takes every so many-th item,
+// which saves the plan's launch (4 documents of a token 14.3 us, 11.8 without; one of 900
+// tokens 26.5, 23.0; 1,000 tokens behind 8,000, where the turns balance worse, 231, 238).
+constexpr int kFewTiles = 16;
 
 // A warp's bounded wait, in few instructions: 2^21 tries (tens of milliseconds at
 // least; a wait is for a few tiles' work, microseconds).  A role whose wait gives
@@ -253,6 +257,51 @@ struct DocPlan {
 };
 static_assert(sizeof(DocPlan) == kDocTileBytes, "the plan's head is as long as a tile");
 
+// A document's rows and keys.
+struct Doc {
+  int q0, n, k0, keys, prefix;
+  __device__ __forceinline__ Doc() {}
+  __device__ __forceinline__ Doc(const DocAttnArgs& a, int d) {
+    const int* ck = a.cu_k ? a.cu_k : a.cu_q;
+    const int q1 = a.cu_q[d + 1], k1 = ck[d + 1], p = a.prefix ? a.prefix[d] : 0;
+    q0 = a.cu_q[d];
+    k0 = ck[d];
+    n = q1 - q0;
+    keys = k1 - k0;
+    prefix = max(0, min(p, keys));
+  }
+  __device__ __forceinline__ bool bad(const DocAttnArgs& a) const {
+    // (differences of numbers in range do not overflow; of others any answer but "in order" will do)
+    return q0 < 0 || q0 > a.N || n < 0 || n > a.N - q0 || k0 < 0 || k0 > a.cap || keys < 0 || keys > a.cap - k0;
+  }
+};
+
+// The query tile of `rows` at most that begins at row `at` of a document.
+__device__ __forceinline__ DocTile tile_at(const Doc& d, int at, int rows, int window, int sinks) {
+  DocTile tile{};
+  tile.q_row = d.q0 + at;
+  tile.rows = min(rows, d.n - at);
+  tile.k_row = d.k0;
+  tile.pos = d.keys - d.n + at;
+  tile.prefix = d.prefix;
+  tile.set_keys(window, sinks);
+  return tile;
+}
+
+// Heads a group, a power of two: the smallest whose work is at least 1.5 times the
+// workers times the heaviest item (the heavy tiles of the last group then start early
+// enough), halved while its heads' K/V exceed kGroupBytes of L2.
+__device__ __forceinline__ int group_log_of(const DocAttnArgs& a, unsigned long long key_tiles, int heaviest,
+                                            int workers) {
+  const unsigned long long need = (3ull * workers * heaviest + 2 * key_tiles - 1) / (2 * key_tiles);
+  const int* ck = a.cu_k ? a.cu_k : a.cu_q;
+  const long long kv_head_bytes = ((long long)ck[a.n_docs] - ck[0]) * (192 + 128) * 2;
+  int log = 0;
+  while ((1ull << log) < need && log < 6) ++log;
+  while (log > 0 && (kv_head_bytes << log) > kGroupBytes) --log;
+  return log;
+}
+
 // The query tile and head of work item w: groups of 2^log heads, in a group tile
 // after tile, in a tile head after head.
 __device__ __forceinline__ void doc_item(int w, int n_tiles, int log, int& tile, int& head) {
@@ -310,12 +359,73 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
   return m;
 }
 
+// Word `lane` of the tile that lane `from` holds.
+__device__ __forceinline__ int word_of(const DocTile& mine, int from) {
+  int word = 0;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(DocTile) / 4; ++i) {
+    const int x = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&mine)[i], from);
+    if ((int)(threadIdx.x & 31) == i) word = x;
+  }
+  return word;
+}
+
+// The plan of a few documents by one warp of every CTA, a tile a lane: `mine`, of the
+// place-th most key tiles (-1: none).  Offsets out of order or range leave no tiles.
+__device__ __forceinline__ void few_tiles(const DocAttnArgs& a, int window, int sinks, int& n_tiles, int& group_log,
+                                       DocTile& mine, int& place, const DevStatus& st) {
+  const int lane = threadIdx.x & 31;
+  Doc doc;
+  doc.q0 = doc.n = doc.k0 = doc.keys = doc.prefix = 0;
+  if (lane < a.n_docs) doc = Doc(a, lane);
+  const bool bad = __any_sync(0xffffffffu, doc.bad(a));
+  if (blockIdx.x == 0 && lane == 0) {
+    st.word[0] = bad ? kStatusBadLength : 0u;
+    st.word[kStatusExtraWord] = 0u;
+  }
+  const int count = bad ? 0 : (doc.n + 127) / 128;
+  int behind = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, behind, o);
+    if (lane >= o) behind += y;
+  }
+  n_tiles = __shfl_sync(0xffffffffu, behind, 31);
+  int d = 0;  // this lane's tile's document: the first one that ends behind it
+  for (int k = 0; k < a.n_docs; ++k) d += __shfl_sync(0xffffffffu, behind, k) <= lane;
+  d = min(d, 31);
+  const int first = __shfl_sync(0xffffffffu, behind - count, d);
+  Doc of;
+  of.q0 = __shfl_sync(0xffffffffu, doc.q0, d);
+  of.n = __shfl_sync(0xffffffffu, doc.n, d);
+  of.k0 = __shfl_sync(0xffffffffu, doc.k0, d);
+  of.keys = __shfl_sync(0xffffffffu, doc.keys, d);
+  of.prefix = __shfl_sync(0xffffffffu, doc.prefix, d);
+  const bool some = lane < n_tiles;
+  if (some) mine = tile_at(of, (lane - first) * 128, 128, window, sinks);
+  const int n_kv = some ? mine.n_kv : 0;
+  int heaviest = n_kv, before = 0;
+  unsigned long long key_tiles = n_kv;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    heaviest = max(heaviest, __shfl_xor_sync(0xffffffffu, heaviest, o));
+    key_tiles += __shfl_xor_sync(0xffffffffu, key_tiles, o);
+  }
+#pragma unroll 1
+  for (int k = 0; k < n_tiles; ++k) {
+    const int y = __shfl_sync(0xffffffffu, n_kv, k);
+    before += y > n_kv || (y == n_kv && k < lane);
+  }
+  place = some ? before : -1;
+  group_log = n_tiles ? group_log_of(a, key_tiles, heaviest, gridDim.x) : 0;
+}
+
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     document_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, float sl2, int window,
-                     int sinks, int* __restrict__ work, const uint8_t* __restrict__ plan, __nv_bfloat16* __restrict__ o,
-                     long long o_row, const DevStatus st) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, float sl2,
+                     int window, int sinks, int* __restrict__ work, const uint8_t* __restrict__ plan, const DocAttnArgs a,
+                     const DevStatus st) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using R = Rings<PAIR>;
   constexpr int kKSlots = R::kKSlots, kVSlots = R::kVSlots, kKTiles = R::kKTiles;
@@ -600,11 +710,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 12) {
       // ---- work scheduler and Q producer ----
       const DocPlan* head = reinterpret_cast<const DocPlan*>(plan);
-      const int n_tiles = head->n_tiles, group_log = head->group_log, n_items = 64 * n_tiles;
       const int* tiles = reinterpret_cast<const int*>(plan + sizeof(DocPlan)) + min(lane, (int)sizeof(DocTile) / 4 - 1);
+      int n_tiles, group_log, place = -1;  // (few: this lane's tile is the place-th heaviest)
+      DocTile mine{};
+      const bool few = !PAIR && !plan;
+      if (few)
+        few_tiles(a, window, sinks, n_tiles, group_log, mine, place, st);
+      else
+        n_tiles = head->n_tiles, group_log = head->group_log;
+      const int n_items = 64 * n_tiles;
       DocTile* const ring = reinterpret_cast<DocTile*>(smem + kTileOff);
       if (elected()) tma_prefetch_desc(&tmQ);
-      int index = leader && lane == 0 ? atomicAdd(work, 1) : 0, it = 0, n_long = 0;
+      // the next item: the counter's, or of few tiles every CTA's in turn, there and back
+      auto ask = [&](int it) {
+        if (few) return it * (int)gridDim.x + (it & 1 ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+        return lane == 0 ? atomicAdd(work, 1) : 0;
+      };
+      int index = leader ? ask(0) : 0, it = 0, n_long = 0;
 #pragma unroll 1
       for (; ok; ++it) {
         // the item's tile (a word a lane) into the ring, where every role finds it
@@ -615,7 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (index < n_items) {
             int at, of;
             doc_item(index, n_tiles, group_log, at, of);
-            word = tiles[at * (int)(sizeof(DocTile) / 4)];
+            if (few)
+              word = word_of(mine, __ffs(__ballot_sync(0xffffffffu, place == at)) - 1);
+            else
+              word = tiles[at * (int)(sizeof(DocTile) / 4)];
             if (lane == (int)offsetof(DocTile, head) / 4) word = of;
           }
           if (turn > 0 && !(ok = wait_for(&bar->item_empty[slot], (turn - 1) & 1))) break;
@@ -638,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A long item's successor is asked for when its last key tiles are being loaded, so that
         // no SM sits on work while others have none; a short one's at once, for its latency
         const bool is_long = n_kv > kAhead;
-        if (leader && !is_long) index = lane == 0 ? atomicAdd(work, 1) : 0;
+        if (leader && !is_long) index = ask(it + 1);
         // its Q, into the staging atoms once the one before has been copied into tensor memory
         if (it > 0 && !(ok = wait_for(&bar->q_empty, (it - 1) & 1))) break;
         if (elected()) {
@@ -651,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++it;  // (its Q is on the way)
             break;
           }
-          index = lane == 0 ? atomicAdd(work, 1) : 0;
+          index = ask(it + 1);
         }
         if (!leader && it >= 2) {  // two items back: it has been read by now
           if (!(ok = wait_for(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1))) break;
@@ -811,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = quarter * 32 + 32 <= tile.rows, mine = row < tile.rows;
         // 16-byte unit u of the row: base + (u / 8) * atom + ((u % 8) ^ flip) * 16
         uint8_t* base = whole ? smem + kOOff + row * 128
-                              : reinterpret_cast<uint8_t*>(o + (long long)(tile.q_row + row) * o_row + tile.head * 128);
+                              : reinterpret_cast<uint8_t*>(a.o + (long long)(tile.q_row + row) * a.o_row + tile.head * 128);
         const int atom = whole ? (int)kAtom : 128, flip = whole ? row & 7 : 0;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
@@ -868,25 +993,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = kPlanThreads;  // tiles are ordered by their number of key tiles, up to this many
 constexpr int kDocsInSmem = 1024;
-
-// A document's rows and keys.
-struct Doc {
-  int q0, n, k0, keys, prefix;
-  __device__ __forceinline__ Doc() {}
-  __device__ __forceinline__ Doc(const DocAttnArgs& a, int d) {
-    const int* ck = a.cu_k ? a.cu_k : a.cu_q;
-    const int q1 = a.cu_q[d + 1], k1 = ck[d + 1], p = a.prefix ? a.prefix[d] : 0;
-    q0 = a.cu_q[d];
-    k0 = ck[d];
-    n = q1 - q0;
-    keys = k1 - k0;
-    prefix = max(0, min(p, keys));
-  }
-  __device__ __forceinline__ bool bad(const DocAttnArgs& a) const {
-    // (differences of numbers in range do not overflow; of others any answer but "in order" will do)
-    return q0 < 0 || q0 > a.N || n < 0 || n > a.N - q0 || k0 < 0 || k0 > a.cap || keys < 0 || keys > a.cap - k0;
-  }
-};
 
 // Exclusive sums over the block, and the total (sh: one int a warp).
 __device__ __forceinline__ int block_before(int v, int& total, int* sh) {
@@ -980,14 +1086,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     else
       d = Doc(a, lo);
     const int at = (t - first[lo]) * tile_rows;
-    DocTile tile{};
-    tile.q_row = d.q0 + at;
-    tile.rows = min(tile_rows, d.n - at);
-    tile.k_row = d.k0;
-    tile.pos = d.keys - d.n + at;
-    tile.prefix = d.prefix;
-    tile.set_keys(window, sinks);
-    return tile;
+    return tile_at(d, at, tile_rows, window, sinks);
   };
   auto bucket_of = [&](const DocTile& t) { return &bucket[kBuckets - 1 - min(t.n_kv, kBuckets - 1)]; };
   unsigned long long sum = 0;
@@ -1020,17 +1119,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     tiles[atomicAdd(bucket_of(tile), 1)] = tile;
   }
   if (tid == 0) {
-    // Heads a group, a power of two: the smallest whose work is at least 1.5 times the CTA
-    // count times the heaviest item (the heavy tiles of the last group then start early
-    // enough), halved while its heads' K/V exceed kGroupBytes of L2
-    const unsigned long long need = (3ull * workers * heaviest + 2 * key_tiles - 1) / (2 * key_tiles);
-    const int* ck = a.cu_k ? a.cu_k : a.cu_q;
-    const long long kv_head_bytes = ((long long)ck[a.n_docs] - ck[0]) * (192 + 128) * 2;
-    int log = 0;
-    while ((1ull << log) < need && log < 6) ++log;
-    while (log > 0 && (kv_head_bytes << log) > kGroupBytes) --log;
     head->n_tiles = n_tiles;
-    head->group_log = log;
+    head->group_log = group_log_of(a, key_tiles, heaviest, workers);
   }
 }
 
@@ -1052,16 +1142,20 @@ cudaError_t launch_tiles(const DocAttnArgs& a, const DevStatusHost& st, int num_
   const long long items = 64 * doc_tiles_at_most(a.N, a.n_docs);
   constexpr int kCtas = PAIR ? 2 : 1;  // that work on an item together
   const int workers = items < num_sms / kCtas ? (int)items : num_sms / kCtas;
-  const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kCtas * 128, window, sinks,
-                                   workers, work, st.word);
-  if (e != cudaSuccess) return e;
+  const bool few = !PAIR && a.n_docs <= 32 && doc_tiles_at_most(a.N, a.n_docs) <= kFewTiles;
+  if (!few) {
+    const cudaError_t e = launch_pdl(doc_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kCtas * 128, window,
+                                     sinks, workers, work, st.word);
+    if (e != cudaSuccess) return e;
+  }
+  const uint8_t* plan = few ? nullptr : a.plan;
   DevStatus dst{st.word, st.wait_limit_ns};
   const float sl2 = a.scale * 1.4426950408889634f;
   if (PAIR)
     return launch_pdl_cluster2(document_attn_tc<PAIR>, dim3(2 * workers), dim3(kThreads), kSmemBytes, stream, tq, tk,
-                               tv, to, sl2, window, sinks, work, (const uint8_t*)a.plan, a.o, a.o_row, dst);
+                               tv, to, sl2, window, sinks, work, plan, a, dst);
   return launch_pdl(document_attn_tc<PAIR>, dim3(workers), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, to, sl2,
-                    window, sinks, work, (const uint8_t*)a.plan, a.o, a.o_row, dst);
+                    window, sinks, work, plan, a, dst);
 }
 }  // namespace
 

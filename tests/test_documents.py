@@ -464,3 +464,26 @@ def test_room_for_many_rows_that_are_not_there(gpu_available, cu, status):
     if status == 0:
         rest[cu[0]:cu[1]] = 5
     assert bool((rest == 5).all())
+
+
+@gpu
+@pytest.mark.parametrize("n,rows", [(32, 16), (33, 16), (32, 17), (17, 16), (5, 1400), (5, 1500)])
+def test_few_tiles_and_more(gpu_available, n, rows):
+    """Around the numbers of documents and rows up to which the thread blocks plan by themselves; many documents empty."""
+    rng = np.random.default_rng(n + rows)
+    cut = np.sort(rng.integers(0, rows + 1, n - 1))
+    cu_q = [int(c) for c in [0, *cut, rows]]
+    past = rng.integers(0, 300, n)
+    cu_k = starts([b - a + int(p) for a, b, p in zip(cu_q, cu_q[1:], past)])
+    prefix = [int(x) for x in rng.integers(-3, 200, n)]
+    q, k, v = normal(1, rows, 64 * 192), normal(2, 64, cu_k[-1], 192), normal(3, 64, cu_k[-1], 128)
+    for kw in (dict(prefix=prefix, window=0, sinks=0), dict(prefix=None, window=50, sinks=3)):
+        out = run(q, k, v, cu_q, cu_k, **kw)
+        check(f64(out), f64(q), f64(k), f64(v), cu_q, cu_k, heads=(0, 63), **kw)
+
+
+@gpu
+@pytest.mark.parametrize("cu", [[0, 500, 400, 2000], [0, 500, 600, 2001], [-1, 500, 600, 2000]])
+def test_offsets_out_of_range_of_more_tiles(gpu_available, cu):
+    q, k, v = normal(1, 2000, 64 * 192), normal(2, 64, 2000, 192), normal(3, 64, 2000, 128)
+    assert bool((run(q, k, v, cu, None, status=-1, fill=5.0) == 5).all())
