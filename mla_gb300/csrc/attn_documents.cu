@@ -5,10 +5,10 @@
 // after the other, each seeing its own keys only (mla_document_attention).
 // Computed in the flash form: online softmax over tiles of 96 keys.
 //
-// A plan kernel (or, for a few tiles, one warp of each CTA) lists the documents' query tiles of
-// up to 128 rows, a tile never holding rows of two documents, heaviest first.  Persistent: one CTA per
-// SM takes items (tile, head) from an atomic counter, in groups of heads whose
-// K/V stay in L2.  An item's key tiles begin at the document's (or the window's)
+// A plan kernel (or, for a few tiles, one warp of each CTA) lists the documents'
+// query tiles of up to 128 rows, a tile never holding rows of two documents,
+// heaviest first.  Persistent: one CTA per SM takes items (tile, head) from an
+// atomic counter, in groups of heads whose K/V stay in L2.  An item's key tiles begin at the document's (or the window's)
 // first key.  V rows behind the last key that the tile's queries see would be
 // another document's: the P.V product takes only the 16-key steps up to that
 // key, and the V producer's warp clears the rows behind it in the last step, so
@@ -112,8 +112,9 @@ static_assert(kSmemBytes <= 232448, "document attention shared memory");
 constexpr uint32_t kTmS = 0, kTmO = 2 * kKeys, kTmP = kTmO + 128, kTmQ = kTmP + kKeys;
 static_assert(kTmQ + 96 == 512, "tensor memory columns");
 constexpr int kThreads = 512;
-constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on at a time (16 MB: the documents of one
-                                                 // new token 15.9 us where they take 14.7, 8 with a prefix 155 where 150)
+constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on at a time (at 16 MB 8 documents with a
+                                                 // prefix take 144 us, at 64 140, at 160 141; 5 of up to 4,096 tokens
+                                                 // 698, 696, 705)
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 constexpr int kItemRing = 4;
 constexpr int kAhead = 4;                        // key tiles left of an item when the next is asked for (3 to 12 alike)
