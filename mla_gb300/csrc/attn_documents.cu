@@ -562,7 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll 1
           for (int j = 0; ok && j < tile.n_kv; ++j, ++x) {
-            const int sb = x & 1;
+            const int sb = x & 1, keys = tile.keys(j);
+            // (a tile's last columns, behind the last key, are masked whatever they hold: a shorter
+            // product takes as long and less power, 16 documents of up to 1,531 tokens 270 us, so 267)
+            const uint32_t idesc = PAIR || keys > 64 ? idesc_s : idesc_bf16(128, 64, false, false);
             // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
             if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
                        (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 12; ++kk)
                   product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + kk * 8,
-                                kb + (kk >> 2) * (kHalfAtom >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
+                                kb + (kk >> 2) * (kHalfAtom >> 4) + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
                 commit_both<PAIR>(&bar->k_empty[k.slot]);
                 commit_both<PAIR>(&bar->s_full[sb]);
               }
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elected()) {
 #pragma unroll
                   for (int kk = 0; kk < 4; ++kk)
-                    product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc_s,
+                    product<PAIR>(tmem + kTmS + sb * kKeys, tmem + kTmQ + c * 32 + kk * 8, kb + kk * 2, idesc,
                                   c > 0 || kk > 0 ? 1u : 0u);
                   commit_both<PAIR>(&bar->k_empty[k.slot]);
                   if (c == 2) commit_both<PAIR>(&bar->s_full[sb]);
