@@ -22,8 +22,8 @@
 //
 // Bounds and figures: free, reserve and fork move little and take their launches,
 // each 2 to 3 us, and the plan's chain of dependent reads: 64 rows given back and
-// taken again 10.6 us on the GPU, 600 rows of up to 2,048 more tokens 22.0, 1 row
-// forked into 4 and given back 12.0.  compact and copy move pages, and HBM bounds
+// taken again 9.8 us on the GPU, 600 rows of up to 2,048 more tokens 21.9, 1 row
+// forked into 4 and given back 12.2.  compact and copy move pages, and HBM bounds
 // them from a few hundred pages on: 1,531 pages of 32 tokens of 64 heads copied in
 // 258 us (6.28 TB/s, 0.93 of the measured copy rate), the 2,048 of 8,192 pages of
 // 16 tokens that a half-full pool has to move in 186 us (5.8 TB/s).
@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PageP
   __shared__ int seg_smem[kPlanThreads];
   __shared__ int head[2];
   pdl_launch_dependents();
+  cluster_sync();  // (the first CTA's shared memory may be written from here on; ahead of the
+                   // wait for the launch before: 64 rows 9.8 us on the GPU, behind it 10.1)
   pdl_wait();
   const PagePool& p = a.pool;
   const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31;
@@ -205,7 +207,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_plan_kernel(const PageP
   const int n_seg = (p.n_pages + kSeg - 1) / kSeg;
   const bool list_near = a.n <= kPlanThreads, seg_near = n_seg <= kPlanThreads;
   bool bad = false;
-  cluster_sync();  // (the first CTA's shared memory may be written from here on)
 
   // 1. free pages as bits, their number in each segment; what the list needs (by the last
   // warps first: the segments are the first ones')
