@@ -142,6 +142,16 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// The scheduler's waits: for an item's work, which a document of millions of keys makes
+// long.  A role that has given up ends them.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_for_item(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < 64 && !*abort; ++i)
+    if (wait_for<CLUSTER>(bar, parity)) return true;
+  return false;
+}
+
 // A role's place in a ring of N slots.
 template <int N>
 struct Place {
@@ -747,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               word = tiles[at * (int)(sizeof(DocTile) / 4)];
             if (lane == (int)offsetof(DocTile, head) / 4) word = of;
           }
-          if (turn > 0 && !(ok = wait_for(&bar->item_empty[slot], (turn - 1) & 1))) break;
+          if (turn > 0 && !(ok = wait_for_item(&bar->item_empty[slot], (turn - 1) & 1, &bar->abort))) break;
           if (lane < (int)sizeof(DocTile) / 4) {
             int* const at = reinterpret_cast<int*>(&ring[slot]) + lane;
             *at = word;
@@ -759,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (PAIR) mbar_arrive_cluster(mapa_rank(smem_u32(&bar->item_full[slot]), 1));
           }
           __syncwarp();
-        } else if (!(ok = wait_for<PAIR>(&bar->item_full[slot], turn & 1))) {
+        } else if (!(ok = wait_for_item<PAIR>(&bar->item_full[slot], turn & 1, &bar->abort))) {
           break;
         }
         const int rows = ring[slot].rows, n_kv = ring[slot].n_kv, q_row = ring[slot].q_row, of = ring[slot].head;
@@ -769,21 +779,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool is_long = n_kv > kAhead;
         if (leader && !is_long) index = ask(it + 1);
         // its Q, into the staging atoms once the one before has been copied into tensor memory
-        if (it > 0 && !(ok = wait_for(&bar->q_empty, (it - 1) & 1))) break;
+        if (it > 0 && !(ok = wait_for_item(&bar->q_empty, (it - 1) & 1, &bar->abort))) break;
         if (elected()) {
           if (leader) mbar_arrive_expect_tx(&bar->q_full, (PAIR ? 6 : 3) * kAtom);
           load_leader<PAIR>(smem + kQOff, &tmQ, &bar->q_full, q_row + rank * 128, of * 3, 0);
         }
         __syncwarp();
         if (leader && is_long) {
-          if (!(ok = wait_for(&bar->near_end, n_long++ & 1))) {
+          if (!(ok = wait_for_item(&bar->near_end, n_long++ & 1, &bar->abort))) {
             ++it;  // (its Q is on the way)
             break;
           }
           index = ask(it + 1);
         }
         if (!leader && it >= 2) {  // two items back: it has been read by now
-          if (!(ok = wait_for(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1))) break;
+          if (!(ok = wait_for_item(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1,
+                                   &bar->abort))) break;
           if (elected()) release_leader<PAIR>(&bar->item_empty[(it - 2) % kItemRing]);
           __syncwarp();
         }

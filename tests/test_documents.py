@@ -487,3 +487,22 @@ def test_few_tiles_and_more(gpu_available, n, rows):
 def test_offsets_out_of_range_of_more_tiles(gpu_available, cu):
     q, k, v = normal(1, 2000, 64 * 192), normal(2, 64, 2000, 192), normal(3, 64, 2000, 128)
     assert bool((run(q, k, v, cu, None, status=-1, fill=5.0) == 5).all())
+
+
+@gpu
+def test_a_document_of_millions_of_keys(gpu_available):
+    """An item that takes tens of milliseconds, by itself, in pairs and among short ones; every key alike, so that each
+    row's answer is the mean of the values it sees."""
+    import torch
+    keys, short = 3_000_000, 40
+    k = torch.zeros((64, keys + short, 192), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty((64, keys + short, 128), dtype=torch.bfloat16, device="cuda")
+    value = (torch.arange(64, device="cuda") % 3).to(torch.bfloat16)  # (its sums stay below 2^24)
+    v[:] = value[:, None, None]
+    want = value.repeat_interleave(128)
+    for cu_q in ([0, 1, 6], [0, 130, 2500]):  # (a few rows; rows enough for pairs)
+        q = normal(1, 6 if cu_q[2] == 6 else 4100, 64 * 192)
+        out = run(q, k, v, cu_q, [0, keys, keys + short], window=0)
+        seen = out[cu_q[1]:cu_q[2]][-short:]
+        for got in (out[:cu_q[1]], seen):
+            assert bool((got == want).all())
