@@ -71,7 +71,8 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> None:
             extra = ["-Xptxas", "-v"] if ptxas_verbose else []
             jobs.append([cc, *ARCH, *CFLAGS, *extra, "-c", src, "-o", obj])
     hooks_obj = os.path.join(BUILD, "mla_debug_hooks.o")
-    hooks_deps = [HOOKS_SRC, os.path.join(ROOT, "tests", "hooks", "mla_debug.h")] + headers
+    hooks_deps = [HOOKS_SRC] + headers
+    hooks_deps += [os.path.join(ROOT, "tests", "hooks", f) for f in ("mla_debug.h", "mla_debug_waits.h")]
     if os.path.exists(HOOKS_SRC) and (_stale(hooks_obj, hooks_deps) or ptxas_verbose):
         jobs.append([cc, *ARCH, *CFLAGS, "-c", HOOKS_SRC, "-o", hooks_obj])
     synth_job = None

@@ -40,7 +40,9 @@
 //            documents with a prefix 150 us where they take 128, 16 of up to 1,531
 //            tokens 240 where 232.  An SM then sat on up to 80 key tiles while others
 //            had none, and warp 0's own instructions held the K tiles up.)
-//   (warps 13..15 give their registers to the softmax groups)
+//   warp 13  watches that the roles get on: no key tile for the call's time limit ends
+//            every wait, and the call reports it
+//   (warps 14 and 15 give their registers to the softmax groups)
 // 96 keys: two score buffers, two of P (so that a P is stored while the product of
 // the one before runs), O and all of Q take the 512 tensor-memory columns exactly,
 // and products of N = 96 from tensor memory run at the full rate (4,080 MAC a clock
@@ -73,9 +75,10 @@
 //
 // Code size: the roles' loops share one instruction cache.  At 81 KB of code (every
 // wait inlined with its clock) 5.4 of the stalls per instruction were for
-// instructions and the second case took 1,290 us; at 35 KB it takes 720.  Hence the
-// waits' counted tries, loops that are not unrolled, and the plan's own numbers of
-// key tiles.
+// instructions and the second case took 1,290 us; at 35 KB, before few documents were
+// planned here, it took 720, and as much at the 51 of now.  Hence waits of a try and a
+// flag, with the clock in a warp of its own (the same times as waits that counted their
+// tries, at 48 KB), loops that are not unrolled, and the plan's own numbers of key tiles.
 #include "common.cuh"
 #include "internal.h"
 
@@ -112,6 +115,7 @@ static_assert(kSmemBytes <= 232448, "document attention shared memory");
 constexpr uint32_t kTmS = 0, kTmO = 2 * kKeys, kTmP = kTmO + 128, kTmQ = kTmP + kKeys;
 static_assert(kTmQ + 96 == 512, "tensor memory columns");
 constexpr int kThreads = 512;
+constexpr int kRoles = 13;                       // warps 0..12; warp 13 watches that they get on
 constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on at a time (at 16 MB 8 documents with a
                                                  // prefix take 144 us, at 64 140, at 160 141; 5 of up to 4,096 tokens
                                                  // 698, 696, 705)
@@ -128,29 +132,6 @@ constexpr int kPairRows = 2048;
 // which saves the plan's launch (4 documents of a token 14.3 us, 11.8 without; one of 900
 // tokens 26.5, 23.0; 1,000 tokens behind 8,000, where the turns balance worse, 231, 238).
 constexpr int kFewTiles = 16;
-
-// A warp's bounded wait, in few instructions: 2^21 tries (tens of milliseconds at
-// least; a wait is for a few tiles' work, microseconds).  A role whose wait gives
-// up stops, and says so at its end.
-// CLUSTER: for what the other CTA of a pair wrote to shared memory.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-  int tries = 1 << 21;
-#pragma unroll 1
-  while (!__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
-    if (--tries == 0) return false;
-  return true;
-}
-
-// The scheduler's waits: for an item's work, which a document of millions of keys makes
-// long.  A role that has given up ends them.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_for_item(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-#pragma unroll 1
-  for (int i = 0; i < 64 && !*abort; ++i)
-    if (wait_for<CLUSTER>(bar, parity)) return true;
-  return false;
-}
 
 // A role's place in a ring of N slots.
 template <int N>
@@ -177,8 +158,21 @@ struct Bars {
   // waited for or completed itself, so that its parity cannot be mistaken
   uint64_t ref[2][4], sum[4], o_free[4], o_stored[4];
   uint64_t near_end, drain_s, drain_pv;
+  uint64_t ended;  // the roles' warps
   uint32_t tmem_slot;
-  int abort;  // the role whose wait gave up
+  int progress;    // key tiles of the first softmax group
+  int abort;       // set: every role gives up (the watching warp, or a drain that gave up)
+
+  // A role's wait.  After giving up a role issues nothing more and waits (`drain`) for its own
+  // copies and products in flight.  A tile whose copies were issued in part never completes
+  // its barrier: that drain ends at the limit, long after they have arrived, and with it the
+  // warp's others.  (The copies of a pair's odd CTA are counted by the even one: both have
+  // stood still for the limit when they give up, so that these have arrived, too.)
+  // CLUSTER: for what the other CTA of a pair wrote to shared memory.
+  template <bool CLUSTER = false>
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    return mbar_wait_or<CLUSTER>(bar, parity, &abort);
+  }
 };
 static_assert(sizeof(Bars<false>) <= 768 && sizeof(Bars<true>) <= 768, "barrier block");
 
@@ -345,7 +339,7 @@ __device__ __forceinline__ bool elected() {
 template <bool PAIR>
 __device__ __forceinline__ bool read_item(uint8_t* smem, Bars<PAIR>* bar, int it, DocTile& tile) {
   const int slot = it % kItemRing;
-  if (!wait_for<PAIR>(&bar->item_full[slot], (it / kItemRing) & 1)) return false;
+  if (!bar->template wait<PAIR>(&bar->item_full[slot], (it / kItemRing) & 1)) return false;
   tile = reinterpret_cast<const DocTile*>(smem + kTileOff)[slot];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bar->item_empty[slot]);
@@ -479,6 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar->near_end, 1);
     mbar_init(&bar->drain_s, 1);
     mbar_init(&bar->drain_pv, 1);
+    mbar_init(&bar->ended, kRoles);
+    bar->progress = 0;
     bar->abort = 0;
     fence_barrier_init();
   }
@@ -500,6 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
 
   bool ok = true;
+  auto drain = [&](uint64_t& b, uint32_t parity) {
+    const bool done = mbar_drain(&b, parity, st.wait_limit_ns);
+    if (!done && lane == 0) *static_cast<volatile int*>(&bar->abort) = warp + 1;
+    return done;
+  };
   if (warp < 4) {
     registers_down<96>();
     if (warp == 0) {
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int key = tile.k_row + tile.key0(j);
           if (PAIR) {
-            if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
+            if (!(ok = bar->wait(&bar->k_empty[k.slot], k.phase ^ 1))) break;
             if (elected()) {
               if (leader) mbar_arrive_expect_tx(&bar->k_full[k.slot], 3 * kKeyAtom);
               load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[k.slot],
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll 1
             for (int c = 0; c < 3; ++c, k.next()) {
-              if (!(ok = wait_for(&bar->k_empty[k.slot], k.phase ^ 1))) break;
+              if (!(ok = bar->wait(&bar->k_empty[k.slot], k.phase ^ 1))) break;
               if (elected()) {
                 if (c == 0) mbar_arrive_expect_tx(&bar->k_full[full.slot], 3 * kKeyAtom);
                 load_leader<PAIR>(smem + kKOff + k.slot * R::kKSlotBytes, &tmK, &bar->k_full[full.slot], key, c,
@@ -542,10 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           full.next();
         }
       }
-      // no copy may still be in flight into shared memory (a tile that was left half issued
-      // never arrives: its wait gives up)
+      // no copy may still be in flight into shared memory
 #pragma unroll 1
-      for (int i = 0; leader && i < kKTiles; ++i, full.next()) ok &= wait_for(&bar->k_full[full.slot], full.phase ^ 1);
+      for (int i = 0; leader && i < kKTiles; ++i, full.next())
+        if (!drain(bar->k_full[full.slot], full.phase ^ 1)) break;
     } else if (warp == 1) {
       if (leader) {
         // ---- S issuer: S_x = Q K_x^T into score buffer x & 1 ----
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = read_item<PAIR>(smem, bar, it, tile)) || tile.rows == 0) break;
           // the item's Q rows (three 128-byte-swizzled 64-column atoms) into tensor memory as bf16
           // pairs, the A operand of every S, once the S of the item before are done
-          if (!(ok = wait_for(&bar->q_full, it & 1) && (it == 0 || wait_for(&bar->q_free, (it - 1) & 1)))) break;
+          if (!(ok = bar->wait(&bar->q_full, it & 1) && (it == 0 || bar->wait(&bar->q_free, (it - 1) & 1)))) break;
           tc_fence_after();
           if (elected()) {
 #pragma unroll
@@ -577,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // product takes as long and less power, 16 documents of up to 1,531 tokens 270 us, so 267)
             const uint32_t idesc = PAIR || keys > 64 ? idesc_s : idesc_bf16(128, 64, false, false);
             // the tile is there, and the group has read the buffer's previous scores (tile x - 2)
-            if (!(ok = wait_for(&bar->k_full[full.slot], full.phase) &&
-                       (x < 2 || wait_for(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
+            if (!(ok = bar->wait(&bar->k_full[full.slot], full.phase) &&
+                       (x < 2 || bar->wait(&bar->s_free[sb], ((x - 2) >> 1) & 1))))
               break;
             full.next();
             tc_fence_after();
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elected()) commit_leader<PAIR>(&bar->drain_s);
         __syncwarp();
-        ok &= wait_for(&bar->drain_s, 0);
+        drain(bar->drain_s, 0);
       }
     } else if (warp == 2) {
       // ---- V producer: half tiles, and clears what lies behind the last key ----
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool cut = keys == 0 || (keys & 15);
 #pragma unroll 1
           for (int h = 0; h < halves; ++h, v.next()) {
-            if (!(ok = wait_for(&bar->v_empty[v.slot], v.phase ^ 1))) break;
+            if (!(ok = bar->wait(&bar->v_empty[v.slot], v.phase ^ 1))) break;
             if (elected()) {
               uint8_t* const at = smem + R::kVOff + v.slot * R::kVSlotBytes;
               // (in a pair, a tile that is to be cut arrives on each CTA's own barrier)
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (ok && cut) {  // rows `keys` .. of the last 16-key step: eight lanes a row and atom
-            if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+            if (!(ok = bar->wait(&bar->v_full[first], (phases >> first) & 1))) break;
             const int last = halves == 1 ? first : (first + 1) % kVSlots, from = keys - (halves - 1) * kHalf;
             uint8_t* const mine =
                 smem + R::kVOff + last * R::kVSlotBytes + (PAIR ? 0 : ((lane >> 3) & 1) * kHalfAtom) + (lane & 7) * 16;
@@ -666,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // (every tile has arrived: its slot's barrier has left the phase before its next one)
 #pragma unroll 1
-      for (int i = 0; i < kVSlots; ++i) ok &= wait_for(&bar->v_full[i], ((phases >> i) & 1) ^ 1);
+      for (int i = 0; i < kVSlots; ++i)
+        if (!drain(bar->v_full[i], ((phases >> i) & 1) ^ 1)) break;
     } else if (warp == 3) {
       if (leader) {
         // ---- P.V issuer: O += P_x V_x ----
@@ -685,14 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the 16-key steps that hold a key (one where there is none: O becomes zeros), the
             // last one's other rows cleared
             const int keys = tile.keys(j), steps = max(1, (keys + 15) >> 4);
-            if (!(ok = wait_for(&bar->v_full[first], (phases >> first) & 1))) break;
+            if (!(ok = bar->wait(&bar->v_full[first], (phases >> first) & 1))) break;
             phases ^= 1u << first;
             if (keys == 0 || (keys & 15)) {
-              if (!(ok = wait_for<PAIR>(&bar->v_cut[first], (cuts >> first) & 1))) break;
+              if (!(ok = bar->template wait<PAIR>(&bar->v_cut[first], (cuts >> first) & 1))) break;
               cuts ^= 1u << first;
             }
             // P_x is written (and, for an item's first tile, the previous item's O read)
-            if (!(ok = wait_for(&bar->p_full[sb], (x >> 1) & 1))) break;
+            if (!(ok = bar->wait(&bar->p_full[sb], (x >> 1) & 1))) break;
             tc_fence_after();
             constexpr int kSlotsOfTile = PAIR ? 1 : 2, kSteps = kKeys / 16 / kSlotsOfTile;
 #pragma unroll
@@ -716,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elected()) commit_leader<PAIR>(&bar->drain_pv);
         __syncwarp();
-        ok &= wait_for(&bar->drain_pv, 0);
+        drain(bar->drain_pv, 0);
       }
     }
   } else if (warp >= 12) {
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               word = tiles[at * (int)(sizeof(DocTile) / 4)];
             if (lane == (int)offsetof(DocTile, head) / 4) word = of;
           }
-          if (turn > 0 && !(ok = wait_for_item(&bar->item_empty[slot], (turn - 1) & 1, &bar->abort))) break;
+          if (turn > 0 && !(ok = bar->wait(&bar->item_empty[slot], (turn - 1) & 1))) break;
           if (lane < (int)sizeof(DocTile) / 4) {
             int* const at = reinterpret_cast<int*>(&ring[slot]) + lane;
             *at = word;
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (PAIR) mbar_arrive_cluster(mapa_rank(smem_u32(&bar->item_full[slot]), 1));
           }
           __syncwarp();
-        } else if (!(ok = wait_for_item<PAIR>(&bar->item_full[slot], turn & 1, &bar->abort))) {
+        } else if (!(ok = bar->template wait<PAIR>(&bar->item_full[slot], turn & 1))) {
           break;
         }
         const int rows = ring[slot].rows, n_kv = ring[slot].n_kv, q_row = ring[slot].q_row, of = ring[slot].head;
@@ -779,28 +781,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool is_long = n_kv > kAhead;
         if (leader && !is_long) index = ask(it + 1);
         // its Q, into the staging atoms once the one before has been copied into tensor memory
-        if (it > 0 && !(ok = wait_for_item(&bar->q_empty, (it - 1) & 1, &bar->abort))) break;
+        if (it > 0 && !(ok = bar->wait(&bar->q_empty, (it - 1) & 1))) break;
         if (elected()) {
           if (leader) mbar_arrive_expect_tx(&bar->q_full, (PAIR ? 6 : 3) * kAtom);
           load_leader<PAIR>(smem + kQOff, &tmQ, &bar->q_full, q_row + rank * 128, of * 3, 0);
         }
         __syncwarp();
         if (leader && is_long) {
-          if (!(ok = wait_for_item(&bar->near_end, n_long++ & 1, &bar->abort))) {
+          if (!(ok = bar->wait(&bar->near_end, n_long++ & 1))) {
             ++it;  // (its Q is on the way)
             break;
           }
           index = ask(it + 1);
         }
         if (!leader && it >= 2) {  // two items back: it has been read by now
-          if (!(ok = wait_for_item(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1,
-                                   &bar->abort))) break;
+          if (!(ok = bar->wait(&bar->item_empty[(it - 2) % kItemRing], ((it - 2) / kItemRing) & 1))) break;
           if (elected()) release_leader<PAIR>(&bar->item_empty[(it - 2) % kItemRing]);
           __syncwarp();
         }
       }
-      if (leader && it > 0) ok &= wait_for(&bar->q_full, (it - 1) & 1);
+      if (leader && it > 0) drain(bar->q_full, (it - 1) & 1);
     }
+    if (warp == kRoles) mbar_watch(&bar->ended, &bar->progress, st.wait_limit_ns, &bar->abort, kRoles + 1);
   } else {
     registers_up<168>();
     // ---- softmax groups, one thread a query row ----
@@ -810,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float* const refs = reinterpret_cast<float*>(smem + kRefOff) + row;    // + 128 x parity of the tile
     float2* const sums = reinterpret_cast<float2*>(smem + kSumOff) + row;
-    auto wait = [&](uint64_t& b, int phase) { return wait_for(&b, phase & 1); };
+    auto wait = [&](uint64_t& b, int phase) { return bar->wait(&b, phase & 1); };
     auto rows_done = [&](uint64_t& b) {
       __syncwarp();
       if (lane == 0) arrive_leader<PAIR>(&b);
@@ -841,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[kKeys / 2];
         if (here) {
           if (!(ok = wait(bar->s_full[g], x >> 1))) break;
+          if (warp == 4 && lane == 0) *static_cast<volatile int*>(&bar->progress) = x;
           tc_fence_after();
           uint32_t s[kKeys];
 #pragma unroll
@@ -988,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_all();
   }
-  if (!ok && lane == 0) bar->abort = warp + 1;
+  if (warp < kRoles && lane == 0) mbar_arrive(&bar->ended);
 
   tc_fence_before();
   __syncthreads();

@@ -5,6 +5,7 @@
 #include "../../mla_gb300/csrc/internal.h"
 #include "../../include/mla.h"
 #include "mla_debug.h"
+#include "mla_debug_waits.h"
 
 namespace mla {
 namespace {
@@ -18,6 +19,52 @@ __global__ void wait_timeout_kernel(uint32_t* word, uint64_t limit_ns) {
   __syncthreads();
   DevStatus st{word, limit_ns};
   if (threadIdx.x == 0) mbar_wait(&bar, 0, st, nullptr, 99);  // nothing ever arrives
+}
+
+// Warps 0 and 1 wait for what never comes (if `stall`), warp 2 gets on for ten steps of half
+// the limit, warp 3 watches.
+__global__ void __launch_bounds__(128) watched_waits_kernel(uint64_t* out, uint64_t limit_ns, int stall) {
+  __shared__ uint64_t never, done, ended;
+  __shared__ int progress, abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&never, 1);
+    mbar_init(&done, 1);
+    mbar_init(&ended, 3);
+    progress = abort = 0;
+    fence_barrier_init();
+    mbar_arrive(&done);
+  }
+  __syncthreads();
+  const uint64_t t0 = globaltimer_ns();
+  bool there = true, waited = false, drained = true;
+  if (warp == 0) {
+    there = mbar_wait_or<false>(&done, 0, &abort);
+    if (stall) waited = mbar_wait_or<false>(&never, 0, &abort);
+  } else if (warp == 1) {
+    there = mbar_wait_or<true>(&done, 0, &abort);
+    if (stall) waited = mbar_wait_or<true>(&never, 0, &abort);
+  } else if (warp == 2) {
+    for (int i = 1; stall && i <= 10; ++i) {
+      while (globaltimer_ns() - t0 < limit_ns / 2 * i) __nanosleep(1000);
+      if (lane == 0) *(volatile int*)&progress = i;
+      __syncwarp();
+    }
+  } else {
+    mbar_watch(&ended, &progress, limit_ns, &abort, 7);
+  }
+  const uint64_t t1 = globaltimer_ns();
+  if (warp < 2) {
+    there = mbar_drain(&done, 0, limit_ns) && there;
+    if (stall) drained = mbar_drain(&never, 0, limit_ns);
+  }
+  if (warp < 3 && lane == 0) mbar_arrive(&ended);
+  if (lane == 0) {
+    out[warp * 4] = t1 - t0;
+    out[warp * 4 + 1] = globaltimer_ns() - t1;
+    out[warp * 4 + 2] = (there ? 1 : 0) | (waited ? 2 : 0) | (drained ? 4 : 0);
+    out[warp * 4 + 3] = (uint64_t)*(volatile int*)&abort;
+  }
 }
 
 // element (r, k) of a K-major tile with 64-element (128-byte) rows, 128-byte swizzle
@@ -127,6 +174,12 @@ int mla_debug_wait_timeout(void* status_word, uint64_t limit_ns, void* stream) {
   if (!status_word) return MLA_ERR_INVALID_ARG;
   wait_timeout_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint32_t*>(status_word),
                                                                        limit_ns);
+  return cuda_rc(cudaGetLastError());
+}
+
+int mla_debug_watched_waits(uint64_t* out, uint64_t limit_ns, int stall, void* stream) {
+  if (!out || limit_ns > 1000000000ull) return MLA_ERR_INVALID_ARG;
+  watched_waits_kernel<<<1, 128, 0, static_cast<cudaStream_t>(stream)>>>(out, limit_ns, stall);
   return cuda_rc(cudaGetLastError());
 }
 

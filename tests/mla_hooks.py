@@ -13,6 +13,7 @@ _SIGS = {
     "mla_debug_gemm": (_I, [_VP, _I, _VP, _I, _I, _VP, _I, _I, _I, _I, _VP]),
     "mla_debug_wait_timeout": (_I, [_VP, ctypes.c_uint64, _VP]),
     "mla_debug_umma_probe": (_I, [_VP, _I, _VP]),
+    "mla_debug_watched_waits": (_I, [_VP, ctypes.c_uint64, _I, _VP]),
 }
 _lib = None
 
@@ -59,3 +60,7 @@ def mla_debug_wait_timeout(status_word, limit_ns: int):
 
 def mla_debug_umma_probe(out, m: int):
     _check(lib().mla_debug_umma_probe(_ptr(out), m, _stream()), "mla_debug_umma_probe")
+
+
+def mla_debug_watched_waits(out, limit_ns: int, stall: bool):
+    _check(lib().mla_debug_watched_waits(_ptr(out), limit_ns, int(stall), _stream()), "mla_debug_watched_waits")
