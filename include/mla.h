@@ -649,6 +649,13 @@ typedef struct {
  * becomes -1 and its page loses one hold.  A row may be listed more than once
  * (the smallest P counts); P[i] past the row's end gives nothing back.  Reported:
  * entries that are no page (they become -1), pages held by nobody (they stay free).
+ * A row may be cut inside a page that others hold too (refs above 1: whole pages
+ * that a fork shares, the parent's as well as the child's, or a hold of the user's
+ * own).  It can then be read and forked, but must not be appended to as it is: its
+ * next token would go into the others' page, and neither this call nor the reserve
+ * or the append looks at that (a row that keeps what it had at its forks, as with
+ * drafts that came after them, never ends in such a page).  mla_pages_fork of its
+ * P[i] positions into an empty row gives that row a copy of the page of its own.
  *   workspace mla_workspace_size(MLA_MODE_PAGES, n, n_pages, rows), as in the
  *            calls below; not shared by calls that may run concurrently
  * Errors: INVALID_ARG (null pointer, n < 1 or > 2^20, rows < 1 or > 2^24,
@@ -671,7 +678,8 @@ int mla_pages_reserve(const mla_page_pool_t* pool, const int* rows, const int* P
  * parents[i]: the whole pages are shared (one more hold each), and where P[i]
  * ends inside a page, its first P[i] % page tokens, in all heads and with the
  * page's scales, are copied into a new page, so that both sequences can go on
- * appending.  The other slots of the new page are left as they were.  With too
+ * appending behind what they hold then (cut back further, into a page that they
+ * share, see mla_pages_free).  The other slots of the new page are left as they were.  With too
  * few free pages nothing is changed (MLA_ERR_NO_PAGES, as mla_pages_reserve).
  * Skipped and reported: a child whose first ceil(P[i] / page) entries are not
  * all -1 or that an earlier entry of the list names, a parent that does not

@@ -550,7 +550,8 @@ def make_page_pool(table, refs, page: int = 64) -> MlaPagePool:
 
 def mla_pages_free(pool: MlaPagePool, rows, P, workspace, stream=None):
     """Gives back the pages of each of the rows behind its first P positions; rows, P: int32 [n]; workspace of
-    MODE_PAGES(n, n_pages, cap=rows of the table) here and below."""
+    MODE_PAGES(n, n_pages, cap=rows of the table) here and below.  A row that then ends inside a page that others hold
+    too (refs above 1) must not be appended to: fork its P positions into an empty row, which gets a page of its own."""
     dev, n = pool._device, rows.shape[0]
     s = _stream_on(dev, stream)
     rc = lib().mla_pages_free(pool._ref, _ints(rows, "rows", n, dev), _ints(P, "P", n, dev), n, _bytes(workspace, dev),

@@ -717,3 +717,41 @@ def test_copy_of_lists(gpu_available, n):
     k = min(n, 150)
     assert run(pages[:k], pages[150:150 + k], a, da, a, da) == OK
     assert run(pages[:k], pages[:k], a, da, a, da) == OK  # each onto itself
+
+
+@gpu
+@pytest.mark.parametrize("page,cut", [(64, 150), (16, 47), (32, 1)])
+def test_back_into_a_shared_page(gpu_available, page, cut):
+    """A row that is cut inside a page it shares shows it in refs; its positions forked into an empty row go on by
+    themselves, and the other row keeps its bits, whichever of the two was cut."""
+    import torch
+    heads, whole = 8, cut // page + 1
+    for who in (0, 1):  # the parent is cut, the child is
+        book = Book(4, whole + 3, 4 * whole + 8, page, cut, heads)
+        for n in ("k_codes", "v_codes"):
+            book.data[n] &= 0xb7     # no NaN codes
+        dev = Device(book)
+        both(book, dev, "reserve", [0], [whole * page + 5])
+        both(book, dev, "fork", [0], [1], [whole * page])
+        other, spare = 1 - who, 3
+        assert both(book, dev, "free", [who], [cut]) == OK
+        assert book.refs[book.table[who, cut // page]] == 2, "its last page is not its own"
+        assert both(book, dev, "fork", [who], [spare], [cut]) == OK
+        assert both(book, dev, "free", [who], [0]) == OK
+        assert both(book, dev, "reserve", [spare], [cut + 4]) == OK
+        last = book.table[spare, cut // page]
+        assert book.refs[last] == 1 and last not in book.table[other]
+        # four tokens far larger than what is there, so that the page's scale has to grow
+        P = [-1] * 4
+        P[spare] = cut
+        kv = torch.full((16, heads, 256), 3e4, dtype=torch.bfloat16, device="cuda")
+        pe = torch.ones((16, 64), dtype=torch.bfloat16, device="cuda")
+        ws = m.alloc_workspace(m.MODE_PAGED_APPEND, 4, 4)
+        m.mla_paged_append(dev.cache, kv[..., :128], kv[..., 128:], pe, ints(P), 4, ws)
+        assert m.mla_device_status(ws) == 0
+        written = {int(x) for x in book.table[spare, cut // page:] if x >= 0}
+        same = [x for x in range(book.n_pages) if x not in written]
+        for n, x in book.data.items():
+            got = dev.t[n].view(torch.int16) if n == "k_pe" else dev.t[n]
+            assert np.array_equal(got.cpu().numpy()[same], x[same]), n
+        assert not np.array_equal(dev.t["k_codes"].cpu().numpy()[last], book.data["k_codes"][last])
