@@ -331,7 +331,7 @@ def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
 
 
 LONG = [
-    # rows enough a document on average for pairs of thread blocks with 256 queries
+    # many key tiles an item, query tiles of 128 (below 2,048 rows a document on average, or a narrower window)
     ([1536], [0], None, 0, 0),
     ([1663], [0], None, 0, 0),
     ([1537], [100], [900], 0, 0),
@@ -506,3 +506,74 @@ def test_a_document_of_millions_of_keys(gpu_available):
         seen = out[cu_q[1]:cu_q[2]][-short:]
         for got in (out[:cu_q[1]], seen):
             assert bool((got == want).all())
+
+
+@gpu
+def test_pairs_captured_and_replayed(gpu_available):
+    """Rows enough for pairs: three calls of one graph after one another, two of them on one workspace, replayed with
+    other offsets (short documents in the room of long ones, none, such as are refused) on two streams at once."""
+    import torch
+    N, cap = 6300, 7000
+    q, k, v = normal(1, N, 64 * 192), normal(2, 64, cap, 192), normal(3, 64, cap, 128)
+    plans = [([0, 2300, 4100, 6300], [0, 2900, 4700, 7000], 0), ([5, 5, 6200, 6291], [3, 40, 6700, 6791], 0),
+             ([0, 300, 301, 429], [0, 300, 3000, 3128], 0), ([0, 2000, 1000, 6300], [0, 2000, 4000, 7000], -1),
+             ([70, 70, 70, 70], [0, 0, 0, 0], 0), ([0, 2300, 4100, 6300], [0, 2900, 4700, 7001], -1)]
+    kw = [dict(), dict(window=2100, sinks=33), dict(prefix=[100, 3000, 0])]
+    want = [[run(q, k, v, cq, ck, status=status, fill=1.0, **w) for w in kw] for cq, ck, status in plans]
+    for cq, ck, status in plans[:3]:
+        check(f64(want[plans.index((cq, ck, status))][0]), f64(q), f64(k), f64(v), cq, ck, None, 0, 0, heads=(11,))
+    streams, sides = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams:
+        cu_q, cu_k, prefix = ints(plans[0][0]), ints(plans[0][1]), ints(kw[2]["prefix"])
+        outs = [torch.empty((N, 64 * 128), dtype=torch.bfloat16, device="cuda") for _ in kw]
+        wss = [m.alloc_workspace(m.MODE_DOCUMENTS, 3, N) for _ in range(2)]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for i in range(3):
+                m.mla_document_attention(q, cu_q, k, v, outs[i], wss[i // 2], cu_k=cu_k, window=kw[i].get("window", 0),
+                                         sinks=kw[i].get("sinks", 0), prefix=prefix if i == 2 else None)
+        sides.append((graph, cu_q, cu_k, outs, wss, prefix))  # (what the graph reads is kept)
+    for turn in ((0, 1), (1, 2), (3, 0), (2, 4), (5, 5), (0, 0)):
+        for i, (_, cu_q, cu_k, outs, *_) in zip(turn, sides):
+            cu_q.copy_(ints(plans[i][0]))
+            cu_k.copy_(ints(plans[i][1]))
+            for out in outs:
+                out.fill_(1.0)
+        torch.cuda.synchronize()
+        for s, side in zip(streams, sides):
+            with torch.cuda.stream(s):
+                side[0].replay()
+        torch.cuda.synchronize()
+        for i, (_, _, _, outs, wss, _) in zip(turn, sides):
+            assert [m.mla_device_status(ws) for ws in wss] == [plans[i][2]] * 2
+            for j, out in enumerate(outs):
+                assert torch.equal(out, want[i][j]), (i, j)
+
+
+@gpu
+@pytest.mark.parametrize("cu_q,N", [([0, 1, 6], 6), ([0, 200, 2500], 2500), ([0, 130, 4100], 4100)])
+def test_each_key_tile_of_a_long_document_counts_once(gpu_available, cu_q, N):
+    """Keys alike, so that a row's answer is the mean of its values; a value is 1 in one dimension of 128 and 0 in the
+    others, the next dimension every 96 keys (another first one in each head).  A tile left out, taken twice or from
+    elsewhere moves a dimension by 4%; what is rounded is the answer, and the quotient by 2^-20 before."""
+    import torch
+    keys, short = 300_007, 40
+    total = keys + short
+    if torch.cuda.mem_get_info()[0] < 2 * 64 * total * (192 + 128) * 2:
+        pytest.skip("too little free memory")
+    j, h = torch.arange(total, device="cuda"), torch.arange(64, device="cuda")
+    k = torch.zeros((64, total, 192), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros((64, total, 128), dtype=torch.bfloat16, device="cuda")
+    at = (j[None] // 96 + 5 * h[:, None]) % 128
+    v.scatter_(2, at[..., None], 1.0)
+    q = normal(1, N, 64 * 192)
+    out = run(q, k, v, cu_q, [0, keys, total])
+    for d, row in ((0, 0), (0, cu_q[1] - 1), (1, cu_q[2] - 1)):
+        first = 0 if d == 0 else keys
+        last = (keys if d == 0 else total) - (cu_q[d + 1] - 1 - row)  # behind the row's own key
+        seen = torch.zeros((64, 128), dtype=torch.float64, device="cuda")
+        seen.scatter_add_(1, at[:, first:last], torch.ones_like(at[:, first:last], dtype=torch.float64))
+        ref = seen / (last - first)
+        got = out[row].double().view(64, 128)
+        assert bool(((got - ref).abs() <= (2.0 ** -8 + 2.0 ** -20) * ref).all()), (d, row)
