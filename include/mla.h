@@ -575,6 +575,11 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
  *   workspace mla_workspace_size(MLA_MODE_DOCUMENTS, n_docs, N, 0)
  * Offsets out of range or order cannot be checked on the host: the kernel then
  * writes nothing and mla_device_status returns MLA_ERR_INVALID_ARG.
+ * N and n_docs, all of the pack that the host knows, also choose the kernel: rows
+ * for long documents (2,816 each on average; no window, or one of 2,048 keys) are
+ * taken 256 at a time, which suits these and costs shorter ones up to a quarter, so
+ * a captured call is best sized for the packs that it gets.  Results are within the
+ * same bounds either way.
  * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
  * Keys behind the last one that a query of its tile of up to 256 sees are not used,
  * whatever the caches hold; a NaN among the values of another key may also

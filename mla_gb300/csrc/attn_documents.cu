@@ -57,10 +57,9 @@
 // Pairs of CTAs (PAIR): for long documents a cluster of two takes two query tiles of a
 // document with one product of 256 rows (cta_group::2), of whose keys and values each
 // CTA holds half, so that a key tile costs an SM 30 KB in and 30 KB out: 5 documents
-// of up to 4,096 tokens take 711 us instead of 740 (back to back, at the power limit),
-// one of 16,384 tokens 2,730 instead of 2,874 (one cold launch), 8 of 512 new tokens
-// behind 4,096 464 instead of 507.  The tensor pipe is then busy in 89% of its cycles.  The
-// even CTA schedules and issues; each CTA loads its half and does the softmax of its own
+// of up to 4,096 tokens take 678 us instead of 697 (back to back, at the power limit),
+// one of 16,384 tokens 2,733 instead of 2,902 (one cold launch).  The even CTA schedules
+// and issues; each CTA loads its half and does the softmax of its own
 // 128 rows.  What it costs: the first tile's products over the keys that only the second
 // sees, and a tile of nothing behind an odd number of them, 4% more tiles in the first
 // case, 22% for 16 documents of up to 1,531 tokens (307 us instead of 277).
@@ -123,14 +122,22 @@ constexpr float kRescaleThreshold = 8.0f;        // log2 units
 constexpr int kItemRing = 4;
 constexpr int kAhead = 4;                        // key tiles left of an item when the next is asked for (3 to 12 alike)
 // Pairs from this many rows of q a document on (8 documents of random lengths around a mean,
-// in us: 1,024 tokens 209 as single tiles, 220 in pairs; 1,536: 406, 417; 2,048: 656, 661;
-// 3,000: 1,277, 1,276; 6,000: 4,578, 4,410; 5 of 2,000 to 4,096: 740, 711), and under a window
-// of this many keys on (the pair's keys are its window's and 256, a tile's 128: 5 documents
-// of 4,000 tokens under 512 keys 470, 520; 1,536: 795, 805; 2,048: 940, 932).
-constexpr int kPairRows = 2048;
+// two draws, back to back in us: 1,536 tokens 384 and 405 as single tiles, 391 and 431 in
+// pairs; 2,048: 624 and 667, 652 and 671; 2,500: 885 and 958, 908 and 980; 3,000: 1,216 and
+// 1,337, 1,204 and 1,304; 4,000: 2,055 and 2,224, 1,999 and 2,198; one of 16,384: 3,257,
+// 3,048), where a document's odd last tile of 128, a whole one of 256 here, counts less (8 of
+// 2,176: 582, 624; of 2,304: 640, 638).  N and n_docs are what the host knows: cached keys
+// gain from pairs with fewer rows too (8 of 512 tokens behind 4,096 517, 493, not taken).
+constexpr int kPairRows = 2816;
+// ... and under a window of this many keys on (the pair's keys are its window's and 256, a
+// tile's 128: 5 documents of 4,000 tokens under 512 keys 414, 433; 1,024: 615, 648; 1,536:
+// 786, 788; 2,048: 917, 892).
+constexpr int kPairWindow = 2048;
 // Up to this many query tiles each CTA makes the plan itself and takes every so many-th item,
 // which saves the plan's launch (4 documents of a token 14.3 us, 11.8 without; one of 900
-// tokens 26.5, 23.0; 1,000 tokens behind 8,000, where the turns balance worse, 231, 238).
+// tokens 26.5, 23.0) and costs balance where an SM's turns are few and long (1,000 tokens
+// behind 8,000 231, 238).  Up to 32: 8 documents of 300 tokens 46.5 -> 43.7 and 3 of 600
+// 47.9 -> 44.3, but one of 1,900 61.1 -> 62.9 and 2 of 1,000 behind 8,000 469 -> 471.
 constexpr int kFewTiles = 16;
 
 // A role's place in a ring of N slots.
@@ -1178,7 +1185,7 @@ cudaError_t launch_tiles(const DocAttnArgs& a, const DevStatusHost& st, int num_
 }  // namespace
 
 cudaError_t launch_document_attention(const DocAttnArgs& a, const DevStatusHost& st, int num_sms, cudaStream_t stream) {
-  const bool pairs = a.N >= kPairRows * (long long)a.n_docs && (a.window == 0 || a.window >= kPairRows);
+  const bool pairs = a.N >= kPairRows * (long long)a.n_docs && (a.window == 0 || a.window >= kPairWindow);
   return pairs ? launch_tiles<true>(a, st, num_sms, stream) : launch_tiles<false>(a, st, num_sms, stream);
 }
 

@@ -331,7 +331,7 @@ def test_binding_refuses_wrong_shapes_types_and_devices(gpu_available):
 
 
 LONG = [
-    # many key tiles an item, query tiles of 128 (below 2,048 rows a document on average, or a narrower window)
+    # many key tiles an item, query tiles of 128
     ([1536], [0], None, 0, 0),
     ([1663], [0], None, 0, 0),
     ([1537], [100], [900], 0, 0),
@@ -400,7 +400,7 @@ def test_long_documents_and_their_neighbours(gpu_available):
 
 
 PAIRS = [
-    # 2,048 rows a document on average and more, where pairs of thread blocks take 256 queries at a time
+    # 2,048 rows a document on average and more (in pairs of thread blocks: test_in_pairs_by_room)
     ([2048], [0], None, 0, 0),
     ([2175], [0], None, 0, 0),
     ([2177], [100], [900], 0, 0),
@@ -455,7 +455,7 @@ def test_pairs_and_their_neighbours(gpu_available):
 @pytest.mark.parametrize("cu,status", [([5, 5], 0), ([2100, 2100], 0), ([7, 8], 0), ([0, 2101], -1), ([-1, 2000], -1),
                                        ([50, 40], -1)])
 def test_room_for_many_rows_that_are_not_there(gpu_available, cu, status):
-    """Rows enough for pairs, offsets that use hardly any or none of them, or that are refused."""
+    """Room for many rows, offsets that use hardly any or none of it, or that are refused."""
     q, k, v = normal(1, 2100, 64 * 192), normal(2, 64, 2100, 192), normal(3, 64, 2100, 128)
     out = run(q, k, v, cu, None, status=status, fill=5.0)
     if status == 0:
@@ -500,7 +500,7 @@ def test_a_document_of_millions_of_keys(gpu_available):
     value = (torch.arange(64, device="cuda") % 3).to(torch.bfloat16)  # (its sums stay below 2^24)
     v[:] = value[:, None, None]
     want = value.repeat_interleave(128)
-    for cu_q in ([0, 1, 6], [0, 130, 2500]):  # (a few rows; rows enough for pairs)
+    for cu_q in ([0, 1, 6], [0, 130, 2500]):  # (a few rows; many)
         q = normal(1, 6 if cu_q[2] == 6 else 4100, 64 * 192)
         out = run(q, k, v, cu_q, [0, keys, keys + short], window=0)
         seen = out[cu_q[1]:cu_q[2]][-short:]
@@ -510,10 +510,10 @@ def test_a_document_of_millions_of_keys(gpu_available):
 
 @gpu
 def test_pairs_captured_and_replayed(gpu_available):
-    """Rows enough for pairs: three calls of one graph after one another, two of them on one workspace, replayed with
+    """Room enough for pairs: three calls of one graph after one another, two of them on one workspace, replayed with
     other offsets (short documents in the room of long ones, none, such as are refused) on two streams at once."""
     import torch
-    N, cap = 6300, 7000
+    N, cap = 12000, 7000  # (room for 4,000 rows a document)
     q, k, v = normal(1, N, 64 * 192), normal(2, 64, cap, 192), normal(3, 64, cap, 128)
     plans = [([0, 2300, 4100, 6300], [0, 2900, 4700, 7000], 0), ([5, 5, 6200, 6291], [3, 40, 6700, 6791], 0),
              ([0, 300, 301, 429], [0, 300, 3000, 3128], 0), ([0, 2000, 1000, 6300], [0, 2000, 4000, 7000], -1),
@@ -552,7 +552,7 @@ def test_pairs_captured_and_replayed(gpu_available):
 
 
 @gpu
-@pytest.mark.parametrize("cu_q,N", [([0, 1, 6], 6), ([0, 200, 2500], 2500), ([0, 130, 4100], 4100)])
+@pytest.mark.parametrize("cu_q,N", [([0, 1, 6], 6), ([0, 200, 2500], 2500), ([0, 130, 4100], 8000)])
 def test_each_key_tile_of_a_long_document_counts_once(gpu_available, cu_q, N):
     """Keys alike, so that a row's answer is the mean of its values; a value is 1 in one dimension of 128 and 0 in the
     others, the next dimension every 96 keys (another first one in each head).  A tile left out, taken twice or from
@@ -577,3 +577,75 @@ def test_each_key_tile_of_a_long_document_counts_once(gpu_available, cu_q, N):
         ref = seen / (last - first)
         got = out[row].double().view(64, 128)
         assert bool(((got - ref).abs() <= (2.0 ** -8 + 2.0 ** -20) * ref).all()), (d, row)
+
+
+PAIRED = [c for c in CASES + LONG + PAIRS if c[3] == 0 or c[3] >= 2048] + [
+    ([2900], [500], None, 2049, 130),
+    ([2500, 2000, 3], [0, 1500, 6000], [200, 3500, 0], 2400, 7),
+    ([300, 256, 1], [4000, 2100, 9000], None, 2048, 100),
+    ([300, 0, 255, 257], [4000, 7, 2100, 1], [4300, 1, 500, 2], 3000, 40),
+]
+
+
+@gpu
+@pytest.mark.parametrize("new,past,prefix,window,sinks", PAIRED)
+def test_in_pairs_by_room(gpu_available, new, past, prefix, window, sinks):
+    """Room for 4,000 rows a document, so that pairs of thread blocks take 256 queries at a time, whatever lies in it."""
+    import torch
+    keys = [a + b for a, b in zip(new, past)]
+    cu_q, cu_k = starts(new, 5), starts(keys, 3)
+    k, v = normal(2, 64, cu_k[-1] + 7, 192), normal(3, 64, cu_k[-1] + 7, 128)
+    q = torch.full((4000 * len(new), 64 * 192), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q[5:cu_q[-1]] = normal(1, cu_q[-1] - 5, 64 * 192)
+    out = run(q, k, v, cu_q, cu_k, prefix, window, sinks, fill=9.0)
+    assert bool((out[:5] == 9).all()) and bool((out[cu_q[-1]:] == 9).all())
+    rows = slice(0, cu_q[-1])
+    check(f64(out[rows]), f64(q[rows]), f64(k), f64(v), cu_q, cu_k, prefix, window, sinks, heads=(0, 37, 63))
+
+
+@gpu
+def test_neighbours_in_pairs_by_room(gpu_available):
+    """NaN and infinities in the other documents, in front of the first and behind the last: the same bits, with rows
+    that have strides."""
+    import torch
+    new, past = [37, 530, 260, 5, 1], [11, 0, 77, 300, 2000]
+    cu_q, cu_k = starts(new, 3), starts([a + b for a, b in zip(new, past)], 9)
+    N = 5 * 4000
+    q = torch.zeros((N, 64 * 192 + 8), dtype=torch.bfloat16, device="cuda")
+    q[:cu_q[-1] + 20] = normal(1, cu_q[-1] + 20, 64 * 192 + 8)
+    k, v = normal(2, 64, cu_k[-1] + 20, 192), normal(3, 64, cu_k[-1] + 20, 128)
+
+    def strided(q, k, v, prefix=None, window=0, sinks=0):
+        wide = torch.full((N, 64 * 128 + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = m.alloc_workspace(m.MODE_DOCUMENTS, 5, N)
+        m.mla_document_attention(q[:, :64 * 192], ints(cu_q), k, v, wide[:, :64 * 128], ws, cu_k=ints(cu_k),
+                                 prefix=None if prefix is None else ints(prefix), window=window, sinks=sinks)
+        assert m.mla_device_status(ws) == 0
+        assert bool((wide[:, 64 * 128:] == 7).all()) and bool((wide[:3] == 7).all()) and bool((wide[cu_q[-1]:] == 7).all())
+        return wide[:cu_q[-1], :64 * 128].contiguous()
+
+    for kw in (dict(), dict(prefix=[5, 0, 300, 305, 1000]), dict(window=2050, sinks=3)):
+        clean = strided(q, k, v, **kw)
+        full = dict(dict(prefix=None, window=0, sinks=0), **kw)
+        check(f64(clean), f64(q[:cu_q[-1], :64 * 192].contiguous()), f64(k), f64(v), cu_q, cu_k, heads=(2, 61), **full)
+        for d in range(5):
+            for value in (float("nan"), float("inf"), -float("inf")):
+                q2, k2, v2 = torch.full_like(q, value), torch.full_like(k, value), torch.full_like(v, value)
+                q2[cu_q[d]:cu_q[d + 1]] = q[cu_q[d]:cu_q[d + 1]]
+                for x2, x in ((k2, k), (v2, v)):
+                    x2[:, cu_k[d]:cu_k[d + 1]] = x[:, cu_k[d]:cu_k[d + 1]]
+                got = strided(q2, k2, v2, **kw)
+                assert torch.equal(got[cu_q[d]:cu_q[d + 1]], clean[cu_q[d]:cu_q[d + 1]]), (kw, d, value)
+
+
+@gpu
+@pytest.mark.parametrize("cu,status", [([5, 5], 0), ([4000, 4000], 0), ([7, 8], 0), ([0, 4001], -1), ([-1, 2000], -1),
+                                       ([50, 40], -1)])
+def test_room_for_a_long_document_that_is_not_there(gpu_available, cu, status):
+    """As test_room_for_many_rows_that_are_not_there, in pairs of thread blocks."""
+    q, k, v = normal(1, 4000, 64 * 192), normal(2, 64, 4000, 192), normal(3, 64, 4000, 128)
+    out = run(q, k, v, cu, None, status=status, fill=5.0)
+    if status == 0:
+        check(f64(out), f64(q), f64(k), f64(v), cu, cu, None, 0, 0)
+        out[cu[0]:cu[1]] = 5
+    assert bool((out == 5).all())
