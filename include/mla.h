@@ -538,8 +538,8 @@ int mla_paged_attention(const mla_paged_cache_t* cache, const mla_params_t* para
  *   params   softmax_scale (the others are not used)
  *   workspace mla_workspace_size(MLA_MODE_WINDOW_ATTN, B, T, 0)
  * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
- * A NaN among a key's values may also reach queries that do not see the key
- * but share a tile with one that does (weight zero times NaN): those less than
+ * A NaN or an infinity among a key's values may also reach queries that do not see
+ * the key but share a tile with one that does (weight zero times it): those less than
  * 256 positions short of it, or past the end of its window.
  * Errors: INVALID_ARG (null pointer, sizes, B * T > 2^24), ALIGNMENT,
  * WORKSPACE, CUDA. */
@@ -582,8 +582,9 @@ int mla_window_attention(const mla_params_t* params, const void* q, int B, int T
  * same bounds either way.
  * Probabilities are rounded to bf16 for the product with V, as in mla_prefill.
  * Keys behind the last one that a query of its tile of up to 256 sees are not used,
- * whatever the caches hold; a NaN among the values of another key may also
- * reach queries of its document that do not see the key, but no other document.
+ * whatever the caches hold; a NaN or an infinity among the values of another key
+ * may also reach queries of its document that do not see the key (weight zero
+ * times it), but no other document.
  * Errors: INVALID_ARG (null pointer, N, cap < 1 or > 2^24, n_docs < 1 or > 2^20,
  * window or sinks < 0, row strides), ALIGNMENT (cu_q, cu_k, prefix: 4 bytes),
  * WORKSPACE, CUDA. */
@@ -726,8 +727,8 @@ int mla_pages_copy(const mla_paged_cache_t* from, const mla_paged_cache_t* to, c
  * this workspace left: MLA_OK, MLA_ERR_TIMEOUT if a bounded device wait
  * gave up (the kernel then skipped its remaining work and returned),
  * MLA_ERR_NO_PAGES (see the mla_pages_ calls), or
- * MLA_ERR_INVALID_ARG if a per-sequence position of a _varlen call was
- * outside [0, P_max].
+ * MLA_ERR_INVALID_ARG if numbers in device memory were outside the ranges
+ * that the call states (positions, lengths, offsets, rows, pages).
  * The word describes one call only: every entry point clears it (and the
  * rest of the status region) on its stream before its first kernel, so a
  * caller that needs the status of a call must read it before enqueueing the
