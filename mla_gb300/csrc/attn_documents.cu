@@ -120,6 +120,7 @@ constexpr long long kGroupBytes = 64ll << 20;    // K/V of the heads worked on a
                                                  // 698, 696, 705)
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
 constexpr int kItemRing = 4;
+constexpr uint64_t kSettleNs = 10000000;         // a copy or a product takes microseconds
 constexpr int kAhead = 4;                        // key tiles left of an item when the next is asked for (3 to 12 alike)
 // Pairs from this many rows of q a document on (8 documents of random lengths around a mean,
 // two draws, back to back in us: 1,536 tokens 384 and 405 as single tiles, 391 and 431 in
@@ -172,9 +173,8 @@ struct Bars {
 
   // A role's wait.  After giving up a role issues nothing more and waits (`drain`) for its own
   // copies and products in flight.  A tile whose copies were issued in part never completes
-  // its barrier: that drain ends at the limit, long after they have arrived, and with it the
-  // warp's others.  (The copies of a pair's odd CTA are counted by the even one: both have
-  // stood still for the limit when they give up, so that these have arrived, too.)
+  // its barrier, and the even CTA of a pair counts the odd one's copies, so a CTA that gives
+  // up also stays for kSettleNs, which any copy is long done in.
   // CLUSTER: for what the other CTA of a pair wrote to shared memory.
   template <bool CLUSTER = false>
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   bool ok = true;
   auto drain = [&](uint64_t& b, uint32_t parity) {
-    const bool done = mbar_drain(&b, parity, st.wait_limit_ns);
+    const bool done = mbar_drain(&b, parity, max(st.wait_limit_ns, kSettleNs));
     if (!done && lane == 0) *static_cast<volatile int*>(&bar->abort) = warp + 1;
     return done;
   };
@@ -1002,7 +1002,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && bar->abort) report_timeout(st, bar->abort);
+  if (*static_cast<volatile int*>(&bar->abort)) {
+    const uint64_t since = globaltimer_ns();
+#pragma unroll 1
+    while (globaltimer_ns() - since < kSettleNs) __nanosleep(100000);
+    if (threadIdx.x == 0) report_timeout(st, bar->abort);
+  }
   __syncwarp();
   if (PAIR) cluster_sync();  // (the other CTA's products, copies and signals are done)
   if (warp == 1) {

@@ -183,6 +183,18 @@ int mla_debug_watched_waits(uint64_t* out, uint64_t limit_ns, int stall, void* s
   return cuda_rc(cudaGetLastError());
 }
 
+int mla_debug_document_attention(const void* q, int N, const int* cu, const void* k, const void* v, int n_docs, void* out,
+                                 uint32_t* status, void* plan, int* first, uint64_t limit_ns, void* stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  const DocAttnArgs a{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                      static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(out), 64 * 192, 64 * 128,
+                      cu, nullptr, nullptr, N, N, n_docs, 0, 0, 0.0721687836f, static_cast<uint8_t*>(plan), first};
+  return cuda_rc(launch_document_attention(a, DevStatusHost{status, limit_ns}, sms, static_cast<cudaStream_t>(stream)));
+}
+
 int mla_debug_umma_probe(float* out, int m, void* stream) {
   if (!out || (m != 64 && m != 128)) return MLA_ERR_INVALID_ARG;
   umma_probe_kernel<<<1, 128, 0, static_cast<cudaStream_t>(stream)>>>(out, m, nullptr);

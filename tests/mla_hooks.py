@@ -13,6 +13,7 @@ _SIGS = {
     "mla_debug_gemm": (_I, [_VP, _I, _VP, _I, _I, _VP, _I, _I, _I, _I, _VP]),
     "mla_debug_wait_timeout": (_I, [_VP, ctypes.c_uint64, _VP]),
     "mla_debug_umma_probe": (_I, [_VP, _I, _VP]),
+    "mla_debug_document_attention": (_I, [_VP, _I, _VP, _VP, _VP, _I] + [_VP] * 4 + [ctypes.c_uint64, _VP]),
     "mla_debug_watched_waits": (_I, [_VP, ctypes.c_uint64, _I, _VP]),
 }
 _lib = None
@@ -64,3 +65,9 @@ def mla_debug_umma_probe(out, m: int):
 
 def mla_debug_watched_waits(out, limit_ns: int, stall: bool):
     _check(lib().mla_debug_watched_waits(_ptr(out), limit_ns, int(stall), _stream()), "mla_debug_watched_waits")
+
+
+def mla_debug_document_attention(q, cu, k, v, out, status, plan, first, limit_ns: int):
+    _check(lib().mla_debug_document_attention(_ptr(q), q.shape[0], _ptr(cu), _ptr(k), _ptr(v), cu.shape[0] - 1, _ptr(out),
+                                              _ptr(status), _ptr(plan), _ptr(first), limit_ns, _stream()),
+           "mla_debug_document_attention")
