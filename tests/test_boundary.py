@@ -43,6 +43,14 @@ def test_product_library_carries_no_test_hooks_and_hooks_library_exports_them():
         assert hasattr(hl, n), f"{n} not exported by the hooks library"
 
 
+def test_hooks_of_the_waits_are_not_in_the_product_library():
+    import mla_hooks
+    hooks = declared_functions([os.path.join(ROOT, "tests", "hooks", "mla_debug_waits.h")])
+    assert hooks == ["mla_debug_document_attention", "mla_debug_watched_waits"]
+    lib, hl = m.lib(), mla_hooks.lib()
+    assert all(not hasattr(lib, n) and hasattr(hl, n) for n in hooks)
+
+
 def test_status_strings():
     for code in (0, -1, -2, -3, -4, -5, -6):
         assert m.STATUS[code] in m.mla_status_string(code)
